@@ -25,6 +25,17 @@ GEMM_ERR_HIP = 6
 GEMM_ERR_UNSUPPORTED_DEVICE = 7
 GEMM_ERR_CAPTURING = 8
 GEMM_ERR_SCRATCH_LIMIT = 9
+GEMM_ERR_INVALID_TYPE = 10
+GEMM_ERR_ALIGNMENT = 11
+
+GEMM_TYPE_F32 = 0
+GEMM_TYPE_BF16 = 1
+GEMM_TYPE_F16 = 2
+
+GEMM_MX_MAX_K = 1 << 24
+GEMM_MX_MOE_MAX_TOKENS = 64
+GEMM_MX_MOE_MAX_EXPERTS = 512
+GEMM_MX_MOE_MAX_TOP_K = 16
 
 GEMM_KERNEL_AUTO = 0
 GEMM_KERNEL_MFMA_256x256 = 1
@@ -92,7 +103,9 @@ EXPORTS = (
     "gemm_f32", "gemm_f32_noalloc", "gemm_f32_noalloc_scratch_bytes", "gemm_f32_workspace_bytes",
     "gemm_f32_ex", "gemm_f32_plan", "gemm_f32_plan_cus",
     "gemm_f32_plan_workspace_bytes", "gemm_f32_with_plan", "gemm_f32_general",
-    "gemm_f32_general_workspace_bytes", "gemm_kernel_name", "gemm_status_string",
+    "gemm_f32_general_workspace_bytes", "gemm_mx_codes_bytes", "gemm_mx_scales_bytes",
+    "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_workspace_bytes",
+    "gemm_mx_moe", "gemm_mx_moe_workspace_bytes", "gemm_kernel_name", "gemm_status_string",
     "gemm_last_hip_error",
 )
 
@@ -174,6 +187,23 @@ def load():
         lib.gemm_f32_general.restype = i
         lib.gemm_f32_general_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
         lib.gemm_f32_general_workspace_bytes.restype = sz
+        lib.gemm_mx_codes_bytes.argtypes = [i, i]
+        lib.gemm_mx_codes_bytes.restype = sz
+        lib.gemm_mx_scales_bytes.argtypes = [i, i]
+        lib.gemm_mx_scales_bytes.restype = sz
+        lib.gemm_mx_quantize.argtypes = [i, i, i, vp, i, i, vp, vp, vp]
+        lib.gemm_mx_quantize.restype = i
+        lib.gemm_mx_dequantize.argtypes = [i, i, i, vp, vp, vp, i, i, vp]
+        lib.gemm_mx_dequantize.restype = i
+        lib.gemm_mx.argtypes = [i, i, i, f, vp, vp, vp, vp, f, vp, i, i, vp, sz, vp]
+        lib.gemm_mx.restype = i
+        lib.gemm_mx_workspace_bytes.argtypes = [i, i, i]
+        lib.gemm_mx_workspace_bytes.restype = sz
+        lib.gemm_mx_moe.argtypes = [i, i, i, i, i, i, vp, i, vp, i, i, vp, vp, vp, vp, vp, i, vp,
+                                    sz, vp]
+        lib.gemm_mx_moe.restype = i
+        lib.gemm_mx_moe_workspace_bytes.argtypes = [i, i, i, i]
+        lib.gemm_mx_moe_workspace_bytes.restype = sz
         lib.gemm_kernel_name.argtypes = [i]
         lib.gemm_kernel_name.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [i]
@@ -263,6 +293,57 @@ def gemm_f32_general_workspace_bytes(trans_a: bool, trans_b: bool, M: int, N: in
                                      lda: int, ldb: int) -> int:
     return int(load().gemm_f32_general_workspace_bytes(int(bool(trans_a)), int(bool(trans_b)),
                                                        M, N, K, lda, ldb))
+
+
+def gemm_mx_codes_bytes(rows: int, K: int) -> int:
+    return int(load().gemm_mx_codes_bytes(rows, K))
+
+
+def gemm_mx_scales_bytes(rows: int, K: int) -> int:
+    return int(load().gemm_mx_scales_bytes(rows, K))
+
+
+def gemm_mx_quantize(trans: bool, rows: int, K: int, X, x_type: int, ldx: int, codes, scales,
+                     stream: int = 0) -> None:
+    _check(load().gemm_mx_quantize(int(bool(trans)), rows, K, _addr(X) or None, x_type, ldx,
+                                   _addr(codes) or None, _addr(scales) or None, stream or None),
+           "gemm_mx_quantize")
+
+
+def gemm_mx_dequantize(trans: bool, rows: int, K: int, codes, scales, Y, y_type: int, ldy: int,
+                       stream: int = 0) -> None:
+    _check(load().gemm_mx_dequantize(int(bool(trans)), rows, K, _addr(codes) or None,
+                                     _addr(scales) or None, _addr(Y) or None, y_type, ldy,
+                                     stream or None), "gemm_mx_dequantize")
+
+
+def gemm_mx(M: int, N: int, K: int, alpha: float, A_codes, A_scales, B_codes, B_scales,
+            beta: float, C, c_type: int, ldc: int, workspace=None, workspace_bytes: int = 0,
+            stream: int = 0) -> None:
+    _check(load().gemm_mx(M, N, K, alpha, _addr(A_codes) or None, _addr(A_scales) or None,
+                          _addr(B_codes) or None, _addr(B_scales) or None, beta, _addr(C) or None,
+                          c_type, ldc, _addr(workspace) or None, workspace_bytes, stream or None),
+           "gemm_mx")
+
+
+def gemm_mx_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().gemm_mx_workspace_bytes(M, N, K))
+
+
+def gemm_mx_moe(tokens: int, hidden: int, inter: int, experts: int, top_k: int, renormalize: bool,
+                logits, ld_logits: int, X, x_type: int, ldx: int, W1_codes, W1_scales, W2_codes,
+                W2_scales, Y, ldy: int, workspace=None, workspace_bytes: int = 0,
+                stream: int = 0) -> None:
+    _check(load().gemm_mx_moe(tokens, hidden, inter, experts, top_k, int(bool(renormalize)),
+                              _addr(logits) or None, ld_logits, _addr(X) or None, x_type, ldx,
+                              _addr(W1_codes) or None, _addr(W1_scales) or None,
+                              _addr(W2_codes) or None, _addr(W2_scales) or None, _addr(Y) or None,
+                              ldy, _addr(workspace) or None, workspace_bytes, stream or None),
+           "gemm_mx_moe")
+
+
+def gemm_mx_moe_workspace_bytes(tokens: int, inter: int, top_k: int, x_type: int) -> int:
+    return int(load().gemm_mx_moe_workspace_bytes(tokens, inter, top_k, x_type))
 
 
 def gemm_kernel_name(kernel: int) -> str:

@@ -13,6 +13,7 @@
 
 #include "dma_launch.hpp"
 #include "gemm_kernels.hpp"
+#include "host_shared.hpp"
 #include "ladder_kernels.hpp"
 
 // The split-K partial sums of gemm_f32_noalloc: a static device array of
@@ -965,6 +966,20 @@ int run_general(Problem p, void *workspace, size_t workspace_bytes, hipStream_t 
 
 }  // namespace
 
+// The parts that the library's other translation units share (host_shared.hpp).
+namespace gemm {
+int host_fail(hipError_t e) { return hip_fail(e); }
+int host_planning_cus() { return planning_cus(); }
+int host_check_device(int *dev, int *cus) { return check_device(dev, cus); }
+bool host_overlaps(const void *p, size_t pb, const void *q, size_t qb) {
+  return overlaps(p, pb, q, qb);
+}
+int host_with_library_workspace(int dev, size_t need, hipStream_t stream,
+                                int (*body)(void *context, void *workspace), void *context) {
+  return with_library_workspace(dev, need, stream, [&](void *ws) { return body(context, ws); });
+}
+}  // namespace gemm
+
 extern "C" {
 
 int gemm_f32(const float *A, const float *B, float *C, int M, int N, int K, hipStream_t stream) {
@@ -1074,6 +1089,8 @@ const char *gemm_status_string(int status) {
     case GEMM_ERR_SCRATCH_LIMIT:
       return "the plan's split-K partial sums exceed the static scratch buffer of "
              "gemm_f32_noalloc (gemm_f32_noalloc_scratch_bytes)";
+    case GEMM_ERR_INVALID_TYPE: return "not a GEMM_TYPE_* element type";
+    case GEMM_ERR_ALIGNMENT: return "pointer not aligned as its operand needs";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,387 @@
+// The gemm_mx* entry points (declared and documented in gemm.h): argument checks,
+// choice of kernel, launches.
+#include "gemm.h"
+
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+#include <type_traits>
+
+#include "host_shared.hpp"
+#include "mx_kernels.hpp"
+#include "mx_moe.hpp"
+
+namespace {
+
+using namespace gemm::mx;
+
+static_assert(kF32 == GEMM_TYPE_F32 && kBf16 == GEMM_TYPE_BF16 && kF16 == GEMM_TYPE_F16,
+              "element types");
+static_assert(kMaxTokens == GEMM_MX_MOE_MAX_TOKENS && kMaxExperts == GEMM_MX_MOE_MAX_EXPERTS &&
+                  kMaxTopK == GEMM_MX_MOE_MAX_TOP_K,
+              "layer limits");
+
+constexpr long long kMaxElements = 1LL << 40;
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+int padded(int K) { return static_cast<int>(ceil_div(K, kAlign) * kAlign); }
+size_t codes_bytes(long long rows, int K) { return static_cast<size_t>(rows) * (padded(K) / 2); }
+size_t scales_bytes(long long rows, int K) { return static_cast<size_t>(rows) * (padded(K) / 32); }
+bool valid_type(int t) { return t == kF32 || t == kBf16 || t == kF16; }
+size_t elem_size(int t) { return t == kF32 ? 4 : 2; }
+bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Rows and K of an operand.
+bool valid_operand(long long rows, int K) {
+  return rows >= 0 && K >= 0 && K <= GEMM_MX_MAX_K && rows * static_cast<long long>(padded(K)) <= kMaxElements;
+}
+
+// Bytes from the first to the last element of a stored matrix.
+size_t extent(long long rows, long long cols, long long ld, int type) {
+  return rows > 0 && cols > 0 ? elem_size(type) * static_cast<size_t>((rows - 1) * ld + cols) : 0;
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GEMM_OK : gemm::host_fail(e);
+}
+
+// Calls f.template operator()<TYPE>() for a valid element type.
+template <class F>
+void with_type(int type, F &&f) {
+  switch (type) {
+    case kF32: f(std::integral_constant<int, kF32>()); break;
+    case kBf16: f(std::integral_constant<int, kBf16>()); break;
+    default: f(std::integral_constant<int, kF16>()); break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Conversion.
+
+// The checks shared by both directions; `mat` is the float matrix.
+int check_convert(int trans, int rows, int K, const void *mat, int type, int ld, const void *codes,
+                  const void *scales, bool to_codes) {
+  const int cols = trans ? rows : K;
+  const long long stored = trans ? K : rows;
+  if (!valid_operand(rows, K) || ld < std::max(1, cols) || stored * ld > kMaxElements)
+    return GEMM_ERR_INVALID_DIM;
+  if (!valid_type(type)) return GEMM_ERR_INVALID_TYPE;
+  if (rows == 0 || K == 0) return GEMM_OK;
+  if (!mat || !codes || !scales) return GEMM_ERR_NULL_PTR;
+  if (!aligned(mat, elem_size(type)) || !aligned(codes, 16) || !aligned(scales, 4))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t mb = extent(stored, cols, ld, type), cb = codes_bytes(rows, K), sb = scales_bytes(rows, K);
+  if (gemm::host_overlaps(mat, mb, codes, cb) || gemm::host_overlaps(mat, mb, scales, sb) ||
+      (to_codes && gemm::host_overlaps(codes, cb, scales, sb)))
+    return GEMM_ERR_ALIAS;
+  return GEMM_OK;
+}
+
+struct RowLaunch {
+  RowMap map;
+  unsigned blocks;
+};
+bool row_launch(int rows, int KP, RowLaunch *l) {
+  const int chunks = KP / 8;
+  int log2 = 4;
+  while (log2 < 8 && (1 << log2) < chunks) ++log2;
+  l->map = RowMap{log2, static_cast<int>(ceil_div(chunks, 1 << log2))};
+  const long long blocks = ceil_div(rows, (256 >> log2) * kRowPasses) * l->map.col_groups;
+  l->blocks = static_cast<unsigned>(blocks);
+  return blocks <= INT32_MAX;
+}
+
+// ---------------------------------------------------------------------------
+// Product.
+struct Product {
+  int M, N, K;
+  float alpha, beta;
+  const unsigned char *ac, *as, *bc, *bs;
+  void *C;
+  int type, ldc;
+};
+
+size_t product_workspace(int, int, int, int) { return 0; }
+
+int launch_product(const Product &p, void *, int cus, hipStream_t stream) {
+  (void)cus;
+  const int tiles_n = static_cast<int>(ceil_div(p.N, 32));
+  with_type(p.type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    typedef typename Elem<T>::store store;
+    hipLaunchKernelGGL(product_simple_kernel<T>,
+                       dim3(static_cast<unsigned>(ceil_div(p.M, 32) * tiles_n)), dim3(64), 0,
+                       stream, p.ac, p.as, p.bc, p.bs, static_cast<store *>(p.C), p.M, p.N,
+                       padded(p.K), p.ldc, p.alpha, p.beta, tiles_n);
+  });
+  return launched();
+}
+
+int launch_scale(const Product &p, int cus, hipStream_t stream) {
+  const long long count = static_cast<long long>(p.M) * p.N;
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>(ceil_div(count, 256), 4LL * cus));
+  with_type(p.type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    hipLaunchKernelGGL(scale_kernel<T>, dim3(blocks), dim3(256), 0, stream,
+                       static_cast<typename Elem<T>::store *>(p.C), count, p.N, p.ldc, p.beta);
+  });
+  return launched();
+}
+
+int check_product(const Product &p) {
+  if (p.M < 0 || p.N < 0 || p.K < 0) return GEMM_ERR_INVALID_DIM;
+  if (!valid_operand(p.M, p.K) || !valid_operand(p.N, p.K) || p.ldc < std::max(1, p.N) ||
+      static_cast<long long>(p.M) * p.ldc > kMaxElements)
+    return GEMM_ERR_INVALID_DIM;
+  if (!valid_type(p.type)) return GEMM_ERR_INVALID_TYPE;
+  if (p.M == 0 || p.N == 0) return GEMM_OK;
+  if (!p.C) return GEMM_ERR_NULL_PTR;
+  const bool uses = p.K > 0 && p.alpha != 0.0f;
+  if (uses && (!p.ac || !p.as || !p.bc || !p.bs)) return GEMM_ERR_NULL_PTR;
+  if (!aligned(p.C, elem_size(p.type))) return GEMM_ERR_ALIGNMENT;
+  if (!uses) return GEMM_OK;
+  if (!aligned(p.ac, 16) || !aligned(p.bc, 16) || !aligned(p.as, 4) || !aligned(p.bs, 4))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t c = extent(p.M, p.N, p.ldc, p.type);
+  if (gemm::host_overlaps(p.C, c, p.ac, codes_bytes(p.M, p.K)) ||
+      gemm::host_overlaps(p.C, c, p.as, scales_bytes(p.M, p.K)) ||
+      gemm::host_overlaps(p.C, c, p.bc, codes_bytes(p.N, p.K)) ||
+      gemm::host_overlaps(p.C, c, p.bs, scales_bytes(p.N, p.K)))
+    return GEMM_ERR_ALIAS;
+  return GEMM_OK;
+}
+
+// A range that a call reads or writes.
+struct Range {
+  const void *p;
+  size_t bytes;
+};
+
+// A caller's workspace (null: the library's) of `need` bytes: large enough,
+// aligned, and apart from everything else that the call touches.
+int check_workspace(const void *workspace, size_t bytes, size_t need, std::initializer_list<Range> others) {
+  if (!workspace || need == 0) return GEMM_OK;
+  if (bytes < need) return GEMM_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return GEMM_ERR_ALIGNMENT;
+  for (const Range &r : others)
+    if (gemm::host_overlaps(workspace, need, r.p, r.bytes)) return GEMM_ERR_ALIAS;
+  return GEMM_OK;
+}
+
+// ---------------------------------------------------------------------------
+// The mixture-of-experts layer.
+size_t moe_workspace(int tokens, int inter, int top_k, int type) {
+  const size_t parts = type == kF32 ? Parts<kF32>::h : Parts<kBf16>::h;
+  return parts * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
+}
+
+int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
+  const bool vec = aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(type)) % 16 == 0;
+  const long long reached = std::min<long long>(static_cast<long long>(a.tokens) * a.top_k, a.experts);
+  const unsigned up = static_cast<unsigned>(
+      std::min<long long>(reached * (padded(a.inter) / 16), 4LL * cus));
+  const unsigned down = static_cast<unsigned>(ceil_div(a.hidden, 16));
+  with_type(type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    if (vec)
+      hipLaunchKernelGGL((moe_up_kernel<T, true>), dim3(up), dim3(kMoeThreads), 0, stream, a);
+    else
+      hipLaunchKernelGGL((moe_up_kernel<T, false>), dim3(up), dim3(kMoeThreads), 0, stream, a);
+  });
+  const int st = launched();
+  if (st != GEMM_OK) return st;
+  with_type(type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(kMoeThreads), 0, stream, a);
+  });
+  return launched();
+}
+
+int check_moe(const MoeArgs &a, int type) {
+  if (a.tokens < 0 || a.tokens > kMaxTokens || a.hidden < 1 || a.inter < 1 || a.experts < 1 ||
+      a.experts > kMaxExperts || a.top_k < 1 || a.top_k > std::min(kMaxTopK, a.experts) ||
+      a.ld_logits < a.experts || a.ldx < a.hidden || a.ldy < a.hidden)
+    return GEMM_ERR_INVALID_DIM;
+  const long long rows1 = 2LL * a.experts * a.inter, rows2 = static_cast<long long>(a.experts) * a.hidden;
+  if (!valid_operand(rows1, a.hidden) || !valid_operand(rows2, a.inter)) return GEMM_ERR_INVALID_DIM;
+  if (!valid_type(type)) return GEMM_ERR_INVALID_TYPE;
+  if (a.tokens == 0) return GEMM_OK;
+  if (!a.logits || !a.x || !a.y || !a.w1c || !a.w1s || !a.w2c || !a.w2s) return GEMM_ERR_NULL_PTR;
+  const size_t es = elem_size(type);
+  if (!aligned(a.logits, 4) || !aligned(a.x, es) || !aligned(a.y, es) || !aligned(a.w1c, 16) ||
+      !aligned(a.w2c, 16) || !aligned(a.w1s, 4) || !aligned(a.w2s, 4))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t y = extent(a.tokens, a.hidden, a.ldy, type);
+  if (gemm::host_overlaps(a.y, y, a.logits, extent(a.tokens, a.experts, a.ld_logits, kF32)) ||
+      gemm::host_overlaps(a.y, y, a.x, extent(a.tokens, a.hidden, a.ldx, type)) ||
+      gemm::host_overlaps(a.y, y, a.w1c, codes_bytes(rows1, a.hidden)) ||
+      gemm::host_overlaps(a.y, y, a.w1s, scales_bytes(rows1, a.hidden)) ||
+      gemm::host_overlaps(a.y, y, a.w2c, codes_bytes(rows2, a.inter)) ||
+      gemm::host_overlaps(a.y, y, a.w2s, scales_bytes(rows2, a.inter)))
+    return GEMM_ERR_ALIAS;
+  return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gemm_mx_codes_bytes(int rows, int K) {
+  return valid_operand(rows, K) ? codes_bytes(rows, K) : 0;
+}
+
+size_t gemm_mx_scales_bytes(int rows, int K) {
+  return valid_operand(rows, K) ? scales_bytes(rows, K) : 0;
+}
+
+int gemm_mx_quantize(int trans, int rows, int K, const void *X, int x_type, int ldx, void *codes,
+                     void *scales, hipStream_t stream) {
+  int st = check_convert(trans, rows, K, X, x_type, ldx, codes, scales, true);
+  if (st != GEMM_OK || rows == 0 || K == 0) return st;
+  const int KP = padded(K);
+  const long long k_tiles = ceil_div(KP, kColK);
+  RowLaunch l;
+  if (trans ? ceil_div(rows, kColRows) * k_tiles > INT32_MAX : !row_launch(rows, KP, &l))
+    return GEMM_ERR_INVALID_DIM;
+  int dev = 0, cus = 0;
+  st = gemm::host_check_device(&dev, &cus);
+  if (st != GEMM_OK) return st;
+  const bool vec = aligned(X, 16) && (static_cast<size_t>(ldx) * elem_size(x_type)) % 16 == 0;
+  unsigned *c = static_cast<unsigned *>(codes);
+  with_type(x_type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    const typename Elem<T>::store *x = static_cast<const typename Elem<T>::store *>(X);
+    if (trans)
+      hipLaunchKernelGGL(quantize_columns_kernel<T>,
+                         dim3(static_cast<unsigned>(ceil_div(rows, kColRows) * k_tiles)), dim3(256),
+                         0, stream, x, ldx, c, static_cast<unsigned *>(scales), rows, K, KP,
+                         static_cast<int>(k_tiles));
+    else if (vec)
+      hipLaunchKernelGGL((quantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, x,
+                         ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
+    else
+      hipLaunchKernelGGL((quantize_rows_kernel<T, false>), dim3(l.blocks), dim3(256), 0, stream, x,
+                         ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
+  });
+  return launched();
+}
+
+int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void *scales, void *Y,
+                       int y_type, int ldy, hipStream_t stream) {
+  int st = check_convert(trans, rows, K, Y, y_type, ldy, codes, scales, false);
+  if (st != GEMM_OK || rows == 0 || K == 0) return st;
+  const int KP = padded(K);
+  const long long k_tiles = ceil_div(KP, kColK);
+  RowLaunch l;
+  if (trans ? ceil_div(rows, kColRows) * k_tiles > INT32_MAX : !row_launch(rows, KP, &l))
+    return GEMM_ERR_INVALID_DIM;
+  int dev = 0, cus = 0;
+  st = gemm::host_check_device(&dev, &cus);
+  if (st != GEMM_OK) return st;
+  const bool vec = aligned(Y, 16) && (static_cast<size_t>(ldy) * elem_size(y_type)) % 16 == 0;
+  const unsigned *c = static_cast<const unsigned *>(codes);
+  const unsigned char *s = static_cast<const unsigned char *>(scales);
+  with_type(y_type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    typename Elem<T>::store *y = static_cast<typename Elem<T>::store *>(Y);
+    if (trans)
+      hipLaunchKernelGGL(dequantize_columns_kernel<T>,
+                         dim3(static_cast<unsigned>(ceil_div(rows, kColRows) * k_tiles)), dim3(256),
+                         0, stream, c, s, y, ldy, rows, K, KP, static_cast<int>(k_tiles));
+    else if (vec)
+      hipLaunchKernelGGL((dequantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, c,
+                         s, y, ldy, rows, K, KP, l.map);
+    else
+      hipLaunchKernelGGL((dequantize_rows_kernel<T, false>), dim3(l.blocks), dim3(256), 0, stream,
+                         c, s, y, ldy, rows, K, KP, l.map);
+  });
+  return launched();
+}
+
+size_t gemm_mx_workspace_bytes(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0 || !valid_operand(M, K) || !valid_operand(N, K)) return 0;
+  return product_workspace(M, N, K, gemm::host_planning_cus());
+}
+
+int gemm_mx(int M, int N, int K, float alpha, const void *A_codes, const void *A_scales,
+            const void *B_codes, const void *B_scales, float beta, void *C, int c_type, int ldc,
+            void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  const Product p{M, N, K, alpha, beta,
+                  static_cast<const unsigned char *>(A_codes), static_cast<const unsigned char *>(A_scales),
+                  static_cast<const unsigned char *>(B_codes), static_cast<const unsigned char *>(B_scales),
+                  C, c_type, ldc};
+  int st = check_product(p);
+  if (st != GEMM_OK || M == 0 || N == 0) return st;
+  const bool uses = K > 0 && alpha != 0.0f;
+  const int cus = gemm::host_planning_cus();
+  const size_t need = uses ? product_workspace(M, N, K, cus) : 0;
+  st = check_workspace(workspace, workspace_bytes, need,
+                       {{C, extent(M, N, ldc, c_type)}, {A_codes, codes_bytes(M, K)},
+                        {A_scales, scales_bytes(M, K)}, {B_codes, codes_bytes(N, K)},
+                        {B_scales, scales_bytes(N, K)}});
+  if (st != GEMM_OK) return st;
+  int dev = 0, dev_cus = 0;
+  st = gemm::host_check_device(&dev, &dev_cus);
+  if (st != GEMM_OK) return st;
+  if (!uses) return launch_scale(p, cus, stream);
+  if (workspace || need == 0) return launch_product(p, workspace, cus, stream);
+  struct Call {
+    const Product *p;
+    int cus;
+    hipStream_t stream;
+  } call{&p, cus, stream};
+  return gemm::host_with_library_workspace(
+      dev, need, stream,
+      [](void *c, void *ws) {
+        const Call *k = static_cast<const Call *>(c);
+        return launch_product(*k->p, ws, k->cus, k->stream);
+      },
+      &call);
+}
+
+size_t gemm_mx_moe_workspace_bytes(int tokens, int inter, int top_k, int x_type) {
+  if (tokens < 1 || tokens > kMaxTokens || top_k < 1 || top_k > kMaxTopK || inter < 1 ||
+      inter > GEMM_MX_MAX_K || !valid_type(x_type))
+    return 0;
+  return moe_workspace(tokens, inter, top_k, x_type);
+}
+
+int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int renormalize,
+                const float *logits, int ld_logits, const void *X, int x_type, int ldx,
+                const void *W1_codes, const void *W1_scales, const void *W2_codes,
+                const void *W2_scales, void *Y, int ldy, void *workspace, size_t workspace_bytes,
+                hipStream_t stream) {
+  MoeArgs a{tokens, hidden, inter, experts, top_k, renormalize != 0, logits, ld_logits, X, ldx,
+            static_cast<const unsigned char *>(W1_codes), static_cast<const unsigned char *>(W1_scales),
+            static_cast<const unsigned char *>(W2_codes), static_cast<const unsigned char *>(W2_scales),
+            Y, ldy, nullptr};
+  int st = check_moe(a, x_type);
+  if (st != GEMM_OK || tokens == 0) return st;
+  const size_t need = moe_workspace(tokens, inter, top_k, x_type);
+  const long long rows1 = 2LL * experts * inter, rows2 = static_cast<long long>(experts) * hidden;
+  st = check_workspace(workspace, workspace_bytes, need,
+                       {{Y, extent(tokens, hidden, ldy, x_type)}, {X, extent(tokens, hidden, ldx, x_type)},
+                        {logits, extent(tokens, experts, ld_logits, kF32)},
+                        {W1_codes, codes_bytes(rows1, hidden)}, {W1_scales, scales_bytes(rows1, hidden)},
+                        {W2_codes, codes_bytes(rows2, inter)}, {W2_scales, scales_bytes(rows2, inter)}});
+  if (st != GEMM_OK) return st;
+  int dev = 0, cus = 0;
+  st = gemm::host_check_device(&dev, &cus);
+  if (st != GEMM_OK) return st;
+  struct Call {
+    MoeArgs *a;
+    int type, cus;
+    hipStream_t stream;
+  } call{&a, x_type, cus, stream};
+  auto body = [](void *c, void *ws) {
+    const Call *k = static_cast<const Call *>(c);
+    if (!ws) return static_cast<int>(GEMM_ERR_WORKSPACE);
+    k->a->h = static_cast<u16 *>(ws);
+    return launch_moe(*k->a, k->type, k->cus, k->stream);
+  };
+  if (workspace) return body(&call, workspace);
+  return gemm::host_with_library_workspace(dev, need, stream, body, &call);
+}
+
+}  // extern "C"

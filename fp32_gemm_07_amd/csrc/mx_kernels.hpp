@@ -1,0 +1,382 @@
+// Kernels on microscaled 4-bit operands (MXFP4: e2m1 numbers, an e8m0 scale for
+// each 32 of them along K): conversion from and to float matrices, the product
+// of two operands, and a mixture-of-experts layer for a few tokens. The formats
+// and entry points are described in gemm.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace gemm {
+namespace mx {
+
+constexpr int kBlock = 32;    // values that share a scale
+constexpr int kAlign = 128;   // a row's values are padded to a multiple of this
+
+constexpr int kF32 = 0, kBf16 = 1, kF16 = 2;   // GEMM_TYPE_*
+
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned short u16;
+
+// ---------------------------------------------------------------------------
+// Element types.
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<kF32> {
+  typedef float store;
+  static __device__ inline float get(float v) { return v; }
+  static __device__ inline float put(float v) { return v; }
+};
+template <>
+struct Elem<kBf16> {
+  typedef u16 store;
+  static __device__ inline float get(u16 v) {
+    return __builtin_bit_cast(float, static_cast<unsigned>(v) << 16);
+  }
+  static __device__ inline u16 put(float v) {
+    return __builtin_bit_cast(u16, static_cast<__bf16>(v));   // nearest, ties to even
+  }
+};
+template <>
+struct Elem<kF16> {
+  typedef u16 store;
+  static __device__ inline float get(u16 v) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, v));
+  }
+  static __device__ inline u16 put(float v) {
+    return __builtin_bit_cast(u16, static_cast<_Float16>(v));
+  }
+};
+
+// 8 consecutive values from p (16-byte aligned for VEC), the first `n` of them
+// (VEC: n >= 8 reads them in 16-byte loads), zeros for the rest.
+template <int TYPE, bool VEC>
+__device__ inline void load8(const typename Elem<TYPE>::store *p, int n, float (&v)[8]) {
+  if (VEC && n >= 8) {
+    if constexpr (TYPE == kF32) {
+      const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0];
+      const f32x4 b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    } else {
+      const uintx4 a = reinterpret_cast<const uintx4 *>(p)[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = Elem<TYPE>::get(static_cast<u16>(a[i]));
+        v[2 * i + 1] = Elem<TYPE>::get(static_cast<u16>(a[i] >> 16));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<TYPE>::get(p[i]) : 0.0f;
+  }
+}
+
+template <int TYPE, bool VEC>
+__device__ inline void store8(typename Elem<TYPE>::store *p, int n, const float (&v)[8]) {
+  if (VEC && n >= 8) {
+    if constexpr (TYPE == kF32) {
+      reinterpret_cast<f32x4 *>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<f32x4 *>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      uintx4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[i] = Elem<TYPE>::put(v[2 * i]) | (static_cast<unsigned>(Elem<TYPE>::put(v[2 * i + 1])) << 16);
+      reinterpret_cast<uintx4 *>(p)[0] = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = Elem<TYPE>::put(v[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The e8m0 scale of a block and its values.
+
+// Scale byte of a block whose largest magnitude has these FP32 bits: the
+// exponent of 2^(floor(log2 max) - 2), so that the maximum falls into [4, 8)
+// where e2m1 ends (6); 255 for an infinity or a NaN (as bits, both lie above
+// every finite number).
+__device__ inline unsigned scale_byte(unsigned max_bits) {
+  const unsigned e = max_bits >> 23;
+  return e == 255 ? 255u : (e < 2 ? 0u : e - 2);
+}
+// 1 / scale as a float; the byte is at most 252 here, so it is normal.
+__device__ inline float inverse_scale(unsigned byte) {
+  return __builtin_bit_cast(float, (254u - byte) << 23);
+}
+// The scale as a float: 2^-127 is subnormal, 255 is NaN.
+__device__ inline float scale_value(unsigned byte) {
+  const unsigned bits = byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23;
+  return __builtin_bit_cast(float, bits);
+}
+__device__ inline unsigned magnitude_bits(float v) {
+  return __builtin_bit_cast(unsigned, v) & 0x7fffffffu;
+}
+
+// 8 values times 1 / scale -> 8 codes, the first in the low bits. The
+// instruction rounds to nearest, ties to even, and saturates at 6.
+__device__ inline unsigned encode8(const float (&v)[8], float inv) {
+  unsigned r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0] * inv, v[1] * inv, 1.0f, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2] * inv, v[3] * inv, 1.0f, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4] * inv, v[5] * inv, 1.0f, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6] * inv, v[7] * inv, 1.0f, 3);
+  return r;
+}
+__device__ inline void decode8(unsigned codes, float scale, float (&v)[8]) {
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
+  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+  v[0] = a[0] * scale; v[1] = a[1] * scale;
+  v[2] = b[0] * scale; v[3] = b[1] * scale;
+  v[4] = c[0] * scale; v[5] = c[1] * scale;
+  v[6] = d[0] * scale; v[7] = d[1] * scale;
+}
+
+// ---------------------------------------------------------------------------
+// Rows of 8-value chunks over workgroups of 256 threads: 2^tpr_log2 threads
+// (16 to 256) side by side along a row, so 256 >> tpr_log2 rows a pass, and
+// PASSES passes. Workgroups run over the column groups first.
+struct RowMap {
+  int tpr_log2;
+  int col_groups;
+};
+constexpr int kRowPasses = 4;
+
+// Quantisation along the stored rows. A block of 32 is 4 neighbouring lanes: the
+// maximum crosses them in two cross-lane steps, each lane writes its 4 bytes of
+// codes.
+template <int TYPE, bool VEC>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(
+    const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
+    unsigned char *__restrict__ scales, int rows, int K, int KP, RowMap map) {
+  const int group = blockIdx.x / map.col_groups;
+  const int tpr = 1 << map.tpr_log2;
+  const int chunk = (blockIdx.x - group * map.col_groups) * tpr + (threadIdx.x & (tpr - 1));
+  const int rows_pass = 256 >> map.tpr_log2;
+  const int k = chunk * 8;
+  if (k >= KP) return;   // whole blocks of lanes: KP is a multiple of 128
+  const long long row0 =
+      static_cast<long long>(group) * (rows_pass * kRowPasses) + (threadIdx.x >> map.tpr_log2);
+  float v[kRowPasses][8];
+#pragma unroll
+  for (int p = 0; p < kRowPasses; ++p) {
+    const long long row = row0 + p * rows_pass;
+    load8<TYPE, VEC>(X + row * ldx + k, row < rows ? K - k : 0, v[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < kRowPasses; ++p) {
+    const long long row = row0 + p * rows_pass;
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude_bits(v[p][i]));
+    m = max(m, static_cast<unsigned>(__shfl_xor(static_cast<int>(m), 1)));
+    m = max(m, static_cast<unsigned>(__shfl_xor(static_cast<int>(m), 2)));
+    const unsigned s = scale_byte(m);
+    const unsigned c = s == 255 ? 0u : encode8(v[p], inverse_scale(s));
+    if (row < rows) {
+      codes[row * (KP / 8) + chunk] = c;
+      if ((chunk & 3) == 0) scales[row * (KP / 32) + (chunk >> 2)] = static_cast<unsigned char>(s);
+    }
+  }
+}
+
+template <int TYPE, bool VEC>
+__global__ __launch_bounds__(256) void dequantize_rows_kernel(
+    const unsigned *__restrict__ codes, const unsigned char *__restrict__ scales,
+    typename Elem<TYPE>::store *__restrict__ Y, int ldy, int rows, int K, int KP, RowMap map) {
+  const int group = blockIdx.x / map.col_groups;
+  const int tpr = 1 << map.tpr_log2;
+  const int chunk = (blockIdx.x - group * map.col_groups) * tpr + (threadIdx.x & (tpr - 1));
+  const int rows_pass = 256 >> map.tpr_log2;
+  const int k = chunk * 8;
+  if (k >= K) return;
+  const long long row0 =
+      static_cast<long long>(group) * (rows_pass * kRowPasses) + (threadIdx.x >> map.tpr_log2);
+  unsigned c[kRowPasses], s[kRowPasses];
+#pragma unroll
+  for (int p = 0; p < kRowPasses; ++p) {
+    const long long row = row0 + p * rows_pass;
+    c[p] = row < rows ? codes[row * (KP / 8) + chunk] : 0u;
+    s[p] = row < rows ? scales[row * (KP / 32) + (chunk >> 2)] : 0u;
+  }
+#pragma unroll
+  for (int p = 0; p < kRowPasses; ++p) {
+    const long long row = row0 + p * rows_pass;
+    if (row >= rows) continue;
+    float v[8];
+    decode8(c[p], scale_value(s[p]), v);
+    store8<TYPE, VEC>(Y + row * ldy + k, K - k, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation across the stored rows (the operand's rows are X's columns):
+// a workgroup of 4 waves takes 64 operand rows by 256 values of K. Lanes run
+// along the stored rows, a lane collecting the 32 values of its block itself;
+// the codes pass through LDS so that each operand row is written in runs of
+// 64 or 128 bytes.
+constexpr int kColRows = 64;       // operand rows of a tile
+constexpr int kColK = 256;         // values of K of a tile
+constexpr int kColStride = 36;     // LDS words of a row's 128 code bytes, padded
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void quantize_columns_kernel(
+    const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
+    unsigned *__restrict__ scales, int rows, int K, int KP, int k_tiles) {
+  __shared__ __attribute__((aligned(16))) unsigned tile[kColRows * kColStride];
+  __shared__ unsigned char tile_scales[kColRows * 8];
+  const int rt = blockIdx.x / k_tiles;
+  const int k0 = (blockIdx.x - rt * k_tiles) * kColK;
+  const long long r0 = static_cast<long long>(rt) * kColRows;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool ok = r0 + lane < rows;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int b = wave + 4 * h;
+    const int kb = k0 + b * kBlock;
+    float v[4][8];
+    unsigned m = 0;
+    if (kb < KP) {
+      const typename Elem<TYPE>::store *p = X + static_cast<long long>(kb) * ldx + r0 + lane;
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) {
+        v[i / 8][i % 8] =
+            ok && kb + i < K ? Elem<TYPE>::get(p[static_cast<long long>(i) * ldx]) : 0.0f;
+        m = max(m, magnitude_bits(v[i / 8][i % 8]));
+      }
+      const unsigned s = scale_byte(m);
+      uintx4 c;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[q] = s == 255 ? 0u : encode8(v[q], inverse_scale(s));
+      *reinterpret_cast<uintx4 *>(&tile[lane * kColStride + b * 4]) = c;
+      tile_scales[lane * 8 + b] = static_cast<unsigned char>(s);
+    }
+  }
+  __syncthreads();
+  const int words = min(kColK, KP - k0) / 8;   // code words of a row here: 16 or 32
+#pragma unroll
+  for (int i = 0; i < kColRows * 8 / 256; ++i) {
+    const int e = threadIdx.x + 256 * i;
+    const int r = e >> 3, w = (e & 7) * 4;
+    if (r0 + r < rows && w < words)
+      *reinterpret_cast<uintx4 *>(codes + (r0 + r) * (KP / 8) + k0 / 8 + w) =
+          *reinterpret_cast<const uintx4 *>(&tile[r * kColStride + w]);
+  }
+  if (threadIdx.x < kColRows * 2) {
+    const int r = threadIdx.x >> 1, w = threadIdx.x & 1;
+    if (r0 + r < rows && w * 16 < words)
+      scales[(r0 + r) * (KP / 128) + k0 / 128 + w] =
+          reinterpret_cast<const unsigned *>(tile_scales)[r * 2 + w];
+  }
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void dequantize_columns_kernel(
+    const unsigned *__restrict__ codes, const unsigned char *__restrict__ scales,
+    typename Elem<TYPE>::store *__restrict__ Y, int ldy, int rows, int K, int KP, int k_tiles) {
+  __shared__ __attribute__((aligned(16))) unsigned tile[kColRows * kColStride];
+  const int rt = blockIdx.x / k_tiles;
+  const int k0 = (blockIdx.x - rt * k_tiles) * kColK;
+  const long long r0 = static_cast<long long>(rt) * kColRows;
+  const int words = min(kColK, KP - k0) / 8;
+#pragma unroll
+  for (int i = 0; i < kColRows * 8 / 256; ++i) {
+    const int e = threadIdx.x + 256 * i;
+    const int r = e >> 3, w = (e & 7) * 4;
+    if (r0 + r < rows && w < words)
+      *reinterpret_cast<uintx4 *>(&tile[r * kColStride + w]) =
+          *reinterpret_cast<const uintx4 *>(codes + (r0 + r) * (KP / 8) + k0 / 8 + w);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (r0 + lane >= rows) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int b = wave + 4 * h;
+    const int kb = k0 + b * kBlock;
+    if (kb >= K) continue;
+    const uintx4 c = *reinterpret_cast<const uintx4 *>(&tile[lane * kColStride + b * 4]);
+    const float s = scale_value(scales[(r0 + lane) * (KP / 32) + kb / 32]);
+    typename Elem<TYPE>::store *p = Y + static_cast<long long>(kb) * ldy + r0 + lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[8];
+      decode8(c[q], s, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (kb + 8 * q + i < K) p[static_cast<long long>(8 * q + i) * ldy] = Elem<TYPE>::put(v[i]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product.
+
+// C <- alpha * sum + beta * C for one element; beta * c is rounded on its own
+// and c not read when beta == 0, as in the FP32 general form.
+template <int TYPE>
+__device__ inline void store_c(typename Elem<TYPE>::store *c, float sum, float alpha, float beta) {
+  const float r = beta == 0.0f ? alpha * sum : fmaf(alpha, sum, beta * Elem<TYPE>::get(*c));
+  *c = Elem<TYPE>::put(r);
+}
+
+__device__ inline intx8 widen(const intx4 v) { return intx8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// One wave per 32 x 32 outputs, operands read from memory into registers:
+// v_mfma_scale_f32_32x32x64, lane (h, i) holding the 32 values h*32.. of row
+// i and their scale.
+template <int TYPE>
+__global__ __launch_bounds__(64) void product_simple_kernel(
+    const unsigned char *__restrict__ ac, const unsigned char *__restrict__ as,
+    const unsigned char *__restrict__ bc, const unsigned char *__restrict__ bs,
+    typename Elem<TYPE>::store *__restrict__ C, int M, int N, int KP, int ldc, float alpha,
+    float beta, int tiles_n) {
+  const int tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
+  const int i = threadIdx.x & 31, h = threadIdx.x >> 5;
+  const long long ra = min(tm * 32 + i, M - 1), rb = min(tn * 32 + i, N - 1);
+  const unsigned char *pa = ac + ra * (KP / 2) + h * 16, *pb = bc + rb * (KP / 2) + h * 16;
+  const unsigned char *sa = as + ra * (KP / 32) + h, *sb = bs + rb * (KP / 32) + h;
+  f32x16 acc = {};
+  for (int k = 0; k < KP; k += 64)
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        widen(*reinterpret_cast<const intx4 *>(pa + k / 2)),
+        widen(*reinterpret_cast<const intx4 *>(pb + k / 2)), acc, 4, 4, 0, sa[k / 32], 0,
+        sb[k / 32]);
+  const int col = tn * 32 + i;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int row = tm * 32 + 8 * (v / 4) + 4 * h + v % 4;
+    if (row < M && col < N)
+      store_c<TYPE>(C + static_cast<long long>(row) * ldc + col, acc[v], alpha, beta);
+  }
+}
+
+// C <- beta * C.
+template <int TYPE>
+__global__ __launch_bounds__(256) void scale_kernel(typename Elem<TYPE>::store *__restrict__ C,
+                                                    long long count, int N, int ldc, float beta) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < count; i += gridDim.x * 256LL) {
+    const long long r = i / N;
+    typename Elem<TYPE>::store *c = C + r * ldc + (i - r * N);
+    *c = Elem<TYPE>::put(beta == 0.0f ? 0.0f : beta * Elem<TYPE>::get(*c));
+  }
+}
+
+}  // namespace mx
+}  // namespace gemm

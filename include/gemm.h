@@ -59,7 +59,8 @@ enum {
   GEMM_ERR_INVALID_DIM = 1,      /* M, N or K negative, or a size too large to index */
   GEMM_ERR_NULL_PTR = 2,         /* null A, B or C that the call would access
                                     (A, B when M, N, K > 0; C when M, N > 0) */
-  GEMM_ERR_ALIAS = 3,            /* C overlaps A or B */
+  GEMM_ERR_ALIAS = 3,            /* C overlaps A or B (gemm_mx*: an output or the
+                                    workspace overlaps something else of the call) */
   GEMM_ERR_WORKSPACE = 4,        /* workspace missing or smaller than required */
   GEMM_ERR_INVALID_PLAN = 5,     /* unknown kernel id, split count < 1 or unusable split_tail */
   GEMM_ERR_HIP = 6,              /* a HIP call failed; see gemm_last_hip_error() */
@@ -68,8 +69,18 @@ enum {
                                      needs the library-owned workspace (pass a
                                      workspace: gemm_f32_ex, gemm_f32_with_plan,
                                      gemm_f32_general) */
-  GEMM_ERR_SCRATCH_LIMIT = 9      /* gemm_f32_noalloc: the plan's partial sums need
+  GEMM_ERR_SCRATCH_LIMIT = 9,     /* gemm_f32_noalloc: the plan's partial sums need
                                      more than its static scratch buffer */
+  GEMM_ERR_INVALID_TYPE = 10,     /* gemm_mx*: not a GEMM_TYPE_* */
+  GEMM_ERR_ALIGNMENT = 11         /* gemm_mx*: a pointer without the alignment that
+                                     its operand needs */
+};
+
+/* Element types of the float matrices that the gemm_mx* entry points take. */
+enum {
+  GEMM_TYPE_F32 = 0,
+  GEMM_TYPE_BF16 = 1,
+  GEMM_TYPE_F16 = 2
 };
 
 /* Kernel identifiers for explicit plans. Tile = the BM x BN output block one
@@ -259,6 +270,104 @@ int gemm_f32_general(int trans_a, int trans_b, int M, int N, int K, float alpha,
  * (0 when it needs none, or for invalid arguments). */
 size_t gemm_f32_general_workspace_bytes(int trans_a, int trans_b, int M, int N, int K, int lda,
                                         int ldb);
+
+/* ---------------------------------------------------------------------------
+ * Products of microscaled 4-bit operands (OCP Microscaling formats, MXFP4).
+ *
+ * A microscaled operand is a matrix of `rows` rows of K values, K being the
+ * axis that a product sums over (rows of A, columns of B). Every block of 32
+ * consecutive values of a row holds e2m1 numbers (4 bits: 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives) that share one e8m0 scale (8 bits: 2^(byte -
+ * 127); 255 makes the block NaN). With KP = K rounded up to a multiple of 128:
+ *   codes   row r at codes + r * KP / 2; element k in byte k / 2, the even k in
+ *           the low half; 16-byte aligned, gemm_mx_codes_bytes(rows, K) bytes;
+ *   scales  row r at scales + r * KP / 32, block b at byte b; 4-byte aligned,
+ *           gemm_mx_scales_bytes(rows, K) bytes.
+ * Values from K to KP are zeros (gemm_mx_quantize writes them; whoever lays
+ * out an operand otherwise writes codes 0 under a scale other than 255 there).
+ * For K a multiple of 128 this is the usual dense layout of MXFP4 weights.
+ * K is at most GEMM_MX_MAX_K; the convention of the top of this file holds
+ * (streams, ownership, argument checks before any work, no overlap of an
+ * output with an input), and float matrices are aligned to their element.
+ */
+enum { GEMM_MX_MAX_K = 1 << 24 };
+
+/* Bytes of an operand's codes (rows * KP / 2) and scales (rows * KP / 32);
+ * 0 for invalid arguments. */
+size_t gemm_mx_codes_bytes(int rows, int K);
+size_t gemm_mx_scales_bytes(int rows, int K);
+
+/* Float matrix -> microscaled operand. trans == 0: X is stored rows x K,
+ * element (r, k) at X[r*ldx + k], ldx >= K; trans != 0: X is stored K x rows,
+ * element (r, k) at X[k*ldx + r], ldx >= rows (so a K x N matrix B of this
+ * library quantises with trans != 0, rows = N, and B^T's operand with trans
+ * == 0, rows = K: the backward products of a layer need both).
+ * x_type: GEMM_TYPE_*. A block's scale is 2^(floor(log2(max |x|)) - 2), at
+ * least 2^-127 (also for a block of zeros); its values are x / scale rounded
+ * to the nearest e2m1 number, ties to the even code, beyond 6 to 6, the sign of
+ * a zero kept. A block that holds an infinity or a NaN has the scale 255 and
+ * codes 0. All of codes and scales is written, the padding included. */
+int gemm_mx_quantize(int trans, int rows, int K, const void *X, int x_type, int ldx, void *codes,
+                     void *scales, hipStream_t stream);
+
+/* Microscaled operand -> the values it stands for, rounded to y_type (exact in
+ * FP32 and bfloat16; past the type's largest value they are infinite); Y
+ * stored as X above, elements between a row's end and its stride are not
+ * written. */
+int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void *scales, void *Y,
+                       int y_type, int ldy, hipStream_t stream);
+
+/* C <- alpha * A * B + beta * C: A an operand of M rows, B one of N rows
+ * (B's columns), both of K values; C is M x N of c_type, row stride ldc >= N.
+ * Products and sums are FP32 (products of e2m1 numbers and scales are exact);
+ * with a split K the partial sums are added in ascending order, so results
+ * are the same from run to run. alpha, beta, K = 0 and the final rounding
+ * as in gemm_f32_general (fmaf(alpha, sum, fl(beta * c)), rounded once more
+ * when c_type has 16 bits): beta == 0 does not read C; alpha == 0 or K == 0
+ * does not read A and B. workspace: null for the library's (not while the
+ * stream captures a graph, when one is needed: GEMM_ERR_CAPTURING), else at
+ * least gemm_mx_workspace_bytes(M, N, K) bytes, 16-byte aligned, used by no
+ * other work until this call's has completed. */
+int gemm_mx(int M, int N, int K, float alpha, const void *A_codes, const void *A_scales,
+            const void *B_codes, const void *B_scales, float beta, void *C, int c_type, int ldc,
+            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes gemm_mx needs for these sizes (at most 64 MiB; 0 when it
+ * needs none, or for invalid arguments). */
+size_t gemm_mx_workspace_bytes(int M, int N, int K);
+
+/* A mixture-of-experts layer for a few tokens, in two kernels. For token t, with
+ * the router's logits l (FP32, tokens x experts, row stride ld_logits; the
+ * product of the tokens and the router's weights, e.g. by gemm_f32):
+ *   p = softmax(l);  S = the top_k experts of largest l, ties to the lowest
+ *   index;  w_e = p_e, or p_e / sum_{S} p when renormalize;
+ *   a_e = silu(G_e x) * (U_e x);   Y[t] = sum over e in S of w_e D_e a_e
+ * with silu(v) = v / (1 + exp(-v)). W1 is one operand of experts * 2 * inter
+ * rows of `hidden` values: expert e's G_e (inter rows), then its U_e (inter
+ * rows); W2 is one of experts * hidden rows of `inter` values (expert e's
+ * D_e). X is tokens x hidden of x_type, row stride ldx; Y the same shape and
+ * type, row stride ldy. Only the chosen experts' weights are read; sums are
+ * FP32, in an order that depends on the sizes and the choice alone.
+ * An expert whose logit is -inf is never chosen (a token with no other is
+ * given zeros, one with fewer than top_k others gets those); a NaN or +inf
+ * among a token's logits makes its row of Y NaN.
+ * 1 <= tokens <= GEMM_MX_MOE_MAX_TOKENS (0 does nothing), experts <=
+ * GEMM_MX_MOE_MAX_EXPERTS, top_k <= GEMM_MX_MOE_MAX_TOP_K and <= experts.
+ * workspace: as gemm_mx, gemm_mx_moe_workspace_bytes(...) bytes. */
+enum {
+  GEMM_MX_MOE_MAX_TOKENS = 64,
+  GEMM_MX_MOE_MAX_EXPERTS = 512,
+  GEMM_MX_MOE_MAX_TOP_K = 16
+};
+int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int renormalize,
+                const float *logits, int ld_logits, const void *X, int x_type, int ldx,
+                const void *W1_codes, const void *W1_scales, const void *W2_codes,
+                const void *W2_scales, void *Y, int ldy, void *workspace, size_t workspace_bytes,
+                hipStream_t stream);
+
+/* Workspace bytes gemm_mx_moe needs for these sizes and the type of X
+ * (always some for tokens > 0; 0 for invalid arguments). */
+size_t gemm_mx_moe_workspace_bytes(int tokens, int inter, int top_k, int x_type);
 
 /* Static, human-readable name of a kernel id ("unknown" otherwise). */
 const char *gemm_kernel_name(int kernel);
