@@ -10,6 +10,7 @@
 #include "host_shared.hpp"
 #include "mx_kernels.hpp"
 #include "mx_moe.hpp"
+#include "mx_tile.hpp"
 
 namespace {
 
@@ -102,18 +103,88 @@ struct Product {
   int type, ldc;
 };
 
-size_t product_workspace(int, int, int, int) { return 0; }
+struct ProductPlan {
+  int bm, bn;    // 0: the simple kernel
+  int splits, k_chunk;
+};
 
-int launch_product(const Product &p, void *, int cus, hipStream_t stream) {
-  (void)cus;
-  const int tiles_n = static_cast<int>(ceil_div(p.N, 32));
+constexpr size_t kMaxWorkspace = size_t(64) << 20;
+
+ProductPlan plan_product(int M, int N, int K, int cus) {
+  const int KP = padded(K);
+  ProductPlan best{0, 0, 1, KP};
+  if (M <= 32 && static_cast<long long>(M) * N < 64 * 64) return best;
+  double best_us = 1e30;
+  const int tiles[3][2] = {{256, 256}, {128, 128}, {64, 64}};
+  const double rate[3] = {16384 * 0.6, 16384 * 0.35, 16384 * 0.15};   // flop per clock per CU
+  for (int c = 0; c < 3; ++c) {
+    const long long tm = ceil_div(M, tiles[c][0]), tn = ceil_div(N, tiles[c][1]);
+    for (int s = 1; s <= 64; s *= 2) {
+      const int chunk = static_cast<int>(ceil_div(ceil_div(KP, s), 128) * 128);
+      const int splits = static_cast<int>(ceil_div(KP, chunk));
+      if (s > 1 && (splits < s || chunk < 512)) break;
+      if (s > 1 && 4.0 * splits * M * static_cast<double>(N) > kMaxWorkspace) break;
+      const double rounds = ceil_div(tm * tn * splits, cus);
+      double us = rounds * (2.0 * tiles[c][0] * tiles[c][1] * chunk / rate[c] / 2400 + 2.0);
+      if (splits > 1) us += 3.0 + (2.0 * splits + 1) * 4 * M * static_cast<double>(N) / 4e6;
+      if (us < best_us * 0.99) {
+        best_us = us;
+        best = ProductPlan{tiles[c][0], tiles[c][1], splits, chunk};
+      }
+    }
+  }
+  return best;
+}
+
+size_t product_workspace(int M, int N, int K, int cus) {
+  const ProductPlan plan = plan_product(M, N, K, cus);
+  return plan.splits > 1 ? size_t(4) * plan.splits * M * N : 0;
+}
+
+template <int BM, int BN, int WPE>
+void launch_tile(const Product &p, const ProductPlan &plan, void *ws, hipStream_t stream) {
+  const long long tm = ceil_div(p.M, BM), tn = ceil_div(p.N, BN);
+  TileArgs a{p.ac, p.as, p.bc, p.bs, plan.splits > 1 ? ws : p.C, p.M, p.N, padded(p.K), p.ldc,
+             p.alpha, p.beta, plan.k_chunk, static_cast<int>(tm), static_cast<int>(tn), plan.splits};
+  const dim3 grid(static_cast<unsigned>(tm * tn * plan.splits));
+  if (plan.splits > 1)
+    hipLaunchKernelGGL((tile_kernel<BM, BN, kF32, true, WPE>), grid, dim3(256), 0, stream, a);
+  else
+    with_type(p.type, [&](auto t) {
+      hipLaunchKernelGGL((tile_kernel<BM, BN, decltype(t)::value, false, WPE>), grid, dim3(256), 0,
+                         stream, a);
+    });
+}
+
+int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
+  ProductPlan plan = plan_product(p.M, p.N, p.K, cus);
+  if (plan.splits > 1 && !ws) {   // no workspace to be had: no split
+    plan.splits = 1;
+    plan.k_chunk = padded(p.K);
+  }
+  if (plan.bm == 256) launch_tile<256, 256, 1>(p, plan, ws, stream);
+  else if (plan.bm == 128) launch_tile<128, 128, 2>(p, plan, ws, stream);
+  else if (plan.bm == 64) launch_tile<64, 64, 2>(p, plan, ws, stream);
+  else {
+    const int tiles_n = static_cast<int>(ceil_div(p.N, 32));
+    with_type(p.type, [&](auto t) {
+      constexpr int T = decltype(t)::value;
+      typedef typename Elem<T>::store store;
+      hipLaunchKernelGGL(product_simple_kernel<T>,
+                         dim3(static_cast<unsigned>(ceil_div(p.M, 32) * tiles_n)), dim3(64), 0,
+                         stream, p.ac, p.as, p.bc, p.bs, static_cast<store *>(p.C), p.M, p.N,
+                         padded(p.K), p.ldc, p.alpha, p.beta, tiles_n);
+    });
+  }
+  const int st = launched();
+  if (st != GEMM_OK || plan.splits == 1) return st;
+  const long long count = static_cast<long long>(p.M) * p.N;
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>(ceil_div(count, 256), 8LL * cus));
   with_type(p.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    typedef typename Elem<T>::store store;
-    hipLaunchKernelGGL(product_simple_kernel<T>,
-                       dim3(static_cast<unsigned>(ceil_div(p.M, 32) * tiles_n)), dim3(64), 0,
-                       stream, p.ac, p.as, p.bc, p.bs, static_cast<store *>(p.C), p.M, p.N,
-                       padded(p.K), p.ldc, p.alpha, p.beta, tiles_n);
+    hipLaunchKernelGGL(split_reduce_kernel<T>, dim3(blocks), dim3(256), 0, stream,
+                       static_cast<const float *>(ws), static_cast<typename Elem<T>::store *>(p.C),
+                       count, p.N, p.ldc, plan.splits, p.alpha, p.beta);
   });
   return launched();
 }
