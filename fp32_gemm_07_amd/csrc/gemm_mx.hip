@@ -242,16 +242,19 @@ int check_workspace(const void *workspace, size_t bytes, size_t need, std::initi
 
 // ---------------------------------------------------------------------------
 // The mixture-of-experts layer.
+constexpr size_t kReachedBytes = (kMaxExperts + 1) * sizeof(Reached) / 16 * 16 + 16;   // of the workspace's head
+
 size_t moe_workspace(int tokens, int inter, int top_k, int type) {
   const size_t parts = type == kF32 ? Parts<kF32>::h : Parts<kBf16>::h;
-  return parts * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
+  const size_t hidden = parts * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
+  return hidden + kReachedBytes;
 }
 
 int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
   const bool vec = aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(type)) % 16 == 0;
   const long long reached = std::min<long long>(static_cast<long long>(a.tokens) * a.top_k, a.experts);
   const unsigned up = static_cast<unsigned>(
-      std::min<long long>(reached * (padded(a.inter) / 16), 4LL * cus));
+      std::min<long long>(reached * (padded(a.inter) / 16), 2LL * cus));
   const unsigned down = static_cast<unsigned>(ceil_div(a.hidden, 16));
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
@@ -426,7 +429,7 @@ int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int r
   MoeArgs a{tokens, hidden, inter, experts, top_k, renormalize != 0, logits, ld_logits, X, ldx,
             static_cast<const unsigned char *>(W1_codes), static_cast<const unsigned char *>(W1_scales),
             static_cast<const unsigned char *>(W2_codes), static_cast<const unsigned char *>(W2_scales),
-            Y, ldy, nullptr};
+            Y, ldy, nullptr, nullptr};
   int st = check_moe(a, x_type);
   if (st != GEMM_OK || tokens == 0) return st;
   const size_t need = moe_workspace(tokens, inter, top_k, x_type);
@@ -448,7 +451,8 @@ int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int r
   auto body = [](void *c, void *ws) {
     const Call *k = static_cast<const Call *>(c);
     if (!ws) return static_cast<int>(GEMM_ERR_WORKSPACE);
-    k->a->h = static_cast<u16 *>(ws);
+    k->a->reached = static_cast<Reached *>(ws);
+    k->a->h = reinterpret_cast<u16 *>(static_cast<char *>(ws) + kReachedBytes);
     return launch_moe(*k->a, k->type, k->cus, k->stream);
   };
   if (workspace) return body(&call, workspace);

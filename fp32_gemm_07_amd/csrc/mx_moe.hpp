@@ -2,9 +2,10 @@
 // kernels (the operation is described in gemm.h at gemm_mx_moe):
 //   up:    route, then for each reached expert G x and U x, a = w silu(Gx) Ux
 //          into the workspace;
-//   down:  route again, Y = sum over the reached experts of D a.
-// Every workgroup works the routing out for itself from the logits (a few
-// microseconds at most, and no third launch or hand-over between workgroups).
+//   down:  Y = sum over the reached experts of D a.
+// Every workgroup of the first kernel works the routing out for itself from the
+// logits (a few microseconds at most, and no third launch or hand-over between
+// workgroups); one of them leaves the list of reached experts for the second.
 //
 // Both products stream their weights from memory once, straight into
 // registers: 16 weight rows are the rows of v_mfma_f32_16x16x32_bf16, 16 tokens
@@ -31,11 +32,21 @@ constexpr int kMoeThreads = 64 * kMoeWaves;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;   // GEMM_MX_MOE_MAX_*
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kTokenTiles = kMaxTokens / 16;
+constexpr int kUpTiles = 2;   // tiles of 16 tokens that the first kernel takes at a time
 
 template <int TYPE>
 struct Parts {
   static constexpr int x = TYPE == kF32 ? 3 : TYPE == kF16 ? 2 : 1;   // of the inputs
   static constexpr int h = TYPE == kF32 ? 3 : 2;                      // of the hidden activations
+};
+
+// A reached expert: its number, the tokens that chose it (one bit each) and its
+// first pair. Pairs (token, expert) are numbered by expert, then token; pair
+// numbers index the rows of the hidden activations. Entry 0 of the workspace's
+// list holds how many follow and the tokens whose logits hold a NaN or +inf.
+struct Reached {
+  unsigned expert_base;   // expert in the low, first pair in the high half
+  unsigned lo, hi;
 };
 
 struct MoeArgs {
@@ -47,34 +58,51 @@ struct MoeArgs {
   const unsigned char *w1c, *w1s, *w2c, *w2s;
   void *y;
   int ldy;
-  u16 *h;   // workspace: Parts<TYPE>::h planes of (tokens * top_k) x IP bfloat16
+  u16 *h;       // workspace: Parts<TYPE>::h planes of (tokens * top_k) x IP bfloat16,
+  Reached *reached;   // and what the second kernel needs of the routing
 };
 
-// What a workgroup knows after routing. Pairs (token, expert) are numbered by
-// expert, then token; pair numbers index the rows of the hidden activations.
+// What a workgroup knows after routing.
 struct Routing {
   unsigned lo[kMaxExperts], hi[kMaxExperts];   // tokens that chose the expert, one bit each
-  u16 base[kMaxExperts];                       // the expert's first pair
-  u16 active[kMaxExperts];                     // reached experts, ascending
+  Reached reached[kMaxExperts];                // reached experts, ascending
   unsigned char token[kMaxPairs];              // the pair's token
   float weight[kMaxPairs];                     // the pair's weight
+  u16 base[kMaxExperts];                       // the expert's first pair
   u16 chosen[kMaxTokens * kMaxTopK];           // token t's experts at t * kMaxTopK
   float chosen_weight[kMaxTokens * kMaxTopK];
   unsigned char count[kMaxTokens];             // how many it has
   unsigned nan_lo, nan_hi;                     // tokens whose logits hold a NaN or +inf
-  int num_active;
+  int num_reached;
 };
 
+// Sums, maxima and running sums over a wave by lane shifts within rows of 16
+// (dpp row_shr 1, 2, 4, 8) and broadcasts of the last lane of a row and of the
+// first half (row_bcast 15, 31); the last lane ends with the whole.
+template <int CTRL, int ROWS>
+__device__ inline int dpp(int identity, int v) {
+  return __builtin_amdgcn_update_dpp(identity, v, CTRL, ROWS, 0xf, false);
+}
+template <class OP>
+__device__ inline int wave_scan(int v, int identity, OP &&op) {
+  v = op(v, dpp<0x111, 0xf>(identity, v));
+  v = op(v, dpp<0x112, 0xf>(identity, v));
+  v = op(v, dpp<0x114, 0xf>(identity, v));
+  v = op(v, dpp<0x118, 0xf>(identity, v));
+  v = op(v, dpp<0x142, 0xa>(identity, v));
+  return op(v, dpp<0x143, 0xc>(identity, v));
+}
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+  const int s = wave_scan(__builtin_bit_cast(int, v), 0, [](int a, int b) {
+    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+  });
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(s, 63));
 }
 __device__ inline unsigned wave_max(unsigned v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2)
-    v = max(v, static_cast<unsigned>(__shfl_xor(static_cast<int>(v), d)));
-  return v;
+  const int m = wave_scan(static_cast<int>(v), 0, [](int a, int b) {
+    return static_cast<int>(max(static_cast<unsigned>(a), static_cast<unsigned>(b)));
+  });
+  return static_cast<unsigned>(__builtin_amdgcn_readlane(m, 63));
 }
 
 // Routes all tokens; ends with a barrier. A wave takes a token at a time, its
@@ -114,7 +142,7 @@ __device__ inline void route(const MoeArgs &a, Routing &r) {
       }
       continue;
     }
-    float top = 0.0f, all = 0.0f, some = 0.0f, mine = 0.0f;
+    float top = 0.0f, mine = -__builtin_inff();
     int n = 0, my_expert = 0;
     for (; n < a.top_k; ++n) {
       unsigned best = 0;
@@ -125,13 +153,7 @@ __device__ inline void route(const MoeArgs &a, Routing &r) {
       if (best == 0) break;
       const float logit =
           __builtin_bit_cast(float, best & 0x80000000u ? best & 0x7fffffffu : ~best);
-      if (n == 0) {
-        top = logit;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (j * 64 < a.experts) all += expf(val[j] - top);
-        all = wave_sum(all);
-      }
+      if (n == 0) top = logit;
       int expert = -1;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -144,40 +166,46 @@ __device__ inline void route(const MoeArgs &a, Routing &r) {
           }
         }
       }
-      const float p = expf(logit - top);
-      some += p;
       if (lane == n) {
-        mine = p;
+        mine = logit;
         my_expert = expert;
       }
     }
+    // softmax: lane n < top_k has the n-th chosen logit, -inf behind them
+    const float p = expf(mine - top);
+    float sum = p;
+    if (!a.renormalize) {
+      sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j * 64 < a.experts) sum += expf(val[j] - top);
+    }
+    sum = wave_sum(sum);
     if (lane == 0) r.count[t] = static_cast<unsigned char>(n);
     if (lane < n) {
       r.chosen[t * kMaxTopK + lane] = static_cast<u16>(my_expert);
-      r.chosen_weight[t * kMaxTopK + lane] = mine / (a.renormalize ? some : all);
+      r.chosen_weight[t * kMaxTopK + lane] = p / sum;
       atomicOr(t < 32 ? &r.lo[my_expert] : &r.hi[my_expert], 1u << (t & 31));
     }
   }
   __syncthreads();
   if (wave == 0) {
-    int pairs = 0, active = 0;
+    int pairs = 0, reached = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
       const int e = e0 + lane;
-      const int c = e < a.experts ? __popc(r.lo[e]) + __popc(r.hi[e]) : 0;
-      int before = c;   // inclusive prefix sum over the lanes
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(before, d);
-        if (lane >= d) before += o;
-      }
+      const unsigned lo = e < a.experts ? r.lo[e] : 0, hi = e < a.experts ? r.hi[e] : 0;
+      const int c = __popc(lo) + __popc(hi);
+      const int upto = wave_scan(c, 0, [](int x, int y) { return x + y; });
       const unsigned long long who = __ballot(c > 0);
-      if (e < a.experts) r.base[e] = static_cast<u16>(pairs + before - c);
+      const unsigned base = static_cast<unsigned>(pairs + upto - c);
+      if (e < a.experts) r.base[e] = static_cast<u16>(base);
       if (c > 0)
-        r.active[active + __popcll(who & ((1ull << lane) - 1))] = static_cast<u16>(e);
-      pairs += __shfl(before, 63);
-      active += __popcll(who);
+        r.reached[reached + __popcll(who & ((1ull << lane) - 1))] =
+            Reached{static_cast<unsigned>(e) | (base << 16), lo, hi};
+      pairs += __builtin_amdgcn_readlane(upto, 63);
+      reached += __popcll(who);
     }
-    if (lane == 0) r.num_active = active;
+    if (lane == 0) r.num_reached = reached;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.tokens * kMaxTopK; i += kMoeThreads) {
@@ -222,28 +250,6 @@ __device__ inline void split8(const float (&v)[8], bf16x8 (&out)[PARTS]) {
   }
 }
 
-// 8 values of x at p (n of them in range) as bfloat16 parts.
-template <int TYPE, bool VEC>
-__device__ inline void load_x8(const typename Elem<TYPE>::store *p, int n,
-                               bf16x8 (&out)[Parts<TYPE>::x]) {
-  if constexpr (TYPE == kBf16) {
-    if (VEC && n >= 8) {
-      out[0] = *reinterpret_cast<const bf16x8 *>(p);
-    } else {
-      uintx4 w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = (2 * i < n ? p[2 * i] : 0u) |
-               (2 * i + 1 < n ? static_cast<unsigned>(p[2 * i + 1]) << 16 : 0u);
-      out[0] = __builtin_bit_cast(bf16x8, w);
-    }
-  } else {
-    float v[8];
-    load8<TYPE, VEC>(p, n, v);
-    split8<Parts<TYPE>::x>(v, out);
-  }
-}
-
 // 8 codes under a scale as bfloat16.
 __device__ inline bf16x8 weights8(unsigned codes, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
@@ -253,8 +259,8 @@ __device__ inline bf16x8 weights8(unsigned codes, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Sums acc over the workgroup's waves into wave order through LDS: afterwards
-// thread i < 64 * TILES holds the sum of lane i % 64's accumulators of tile i / 64.
+// Sums acc over the workgroup's waves through LDS (red: kMoeWaves * TILES * 64),
+// in wave order: afterwards wave w < used holds tile w's sums, the lanes as acc.
 template <int TILES>
 __device__ inline f32x4 reduce_waves(const f32x4 (&acc)[TILES], int used, f32x4 *red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -272,97 +278,201 @@ __device__ inline f32x4 reduce_waves(const f32x4 (&acc)[TILES], int used, f32x4 
   return s;
 }
 
+// 32 values of x of a lane's token as they are loaded, and their parts.
+template <int TYPE>
+struct RawX {
+  uintx4 v[TYPE == kF32 ? 8 : 4];
+  __device__ inline void parts(int j, bf16x8 (&out)[Parts<TYPE>::x]) const {
+    if constexpr (TYPE == kBf16) {
+      out[0] = __builtin_bit_cast(bf16x8, v[j]);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (TYPE == kF32) {
+          const unsigned w = v[2 * j + i / 4][i % 4];   // (the cast of a vector's element itself takes the first)
+          f[i] = __builtin_bit_cast(float, w);
+        } else
+          f[i] = Elem<TYPE>::get(static_cast<u16>(v[j][i / 2] >> (16 * (i % 2))));
+      }
+      split8<Parts<TYPE>::x>(f, out);
+    }
+  }
+  // From p, `left` values in range, the rest zeros.
+  template <bool VEC>
+  __device__ inline void load(const typename Elem<TYPE>::store *p, int left) {
+    constexpr int kEach = TYPE == kF32 ? 4 : 8, kRegs = TYPE == kF32 ? 8 : 4;
+    if (VEC && left >= 32) {
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r) v[r] = reinterpret_cast<const uintx4 *>(p)[r];
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r) {
+        uintx4 w = {};
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+          if (r * kEach + i < left) {
+            if constexpr (TYPE == kF32)
+              w[i] = __builtin_bit_cast(unsigned, p[r * kEach + i]);
+            else
+              w[i / 2] |= static_cast<unsigned>(p[r * kEach + i]) << (16 * (i % 2));
+          }
+        v[r] = w;
+      }
+    }
+  }
+};
+
+// G x, U x and a for the reached experts. An item is 16 of an expert's gate rows
+// and the same up rows; the 8 waves share its K, two chunks of 128 a wave at a
+// time, and the next two's weights (of the next item where this one ends) are
+// on their way meanwhile.
 template <int TYPE, bool VEC>
-__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
+  constexpr int kAt = 2;   // chunks of a wave at a time
   __shared__ Routing r;
-  __shared__ __attribute__((aligned(16))) f32x4 red[kMoeWaves * 2 * kTokenTiles * 64];
+  __shared__ __attribute__((aligned(16))) f32x4 red[kMoeWaves * 2 * kUpTiles * 64];
   route(a, r);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int num_reached = __builtin_amdgcn_readfirstlane(r.num_reached);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) a.reached[0] = Reached{static_cast<unsigned>(num_reached), r.nan_lo, r.nan_hi};
+    for (int n = threadIdx.x; n < num_reached; n += kMoeThreads) a.reached[1 + n] = r.reached[n];
+  }
   const int i16 = lane & 15, g = lane >> 4;
   const int HP = (a.hidden + kAlign - 1) / kAlign * kAlign;
   const int IP = (a.inter + kAlign - 1) / kAlign * kAlign;
-  const int tiles = IP / 16;
+  const int tiles = IP / 16, chunks = HP / 128;
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
   const store *x = static_cast<const store *>(a.x);
-  for (int item = blockIdx.x; item < r.num_active * tiles; item += gridDim.x) {
+  const int items = num_reached * tiles;
+
+  struct Weights {
+    uintx4 gate[kAt], up[kAt];
+    unsigned gate_scale[kAt], up_scale[kAt];
+  };
+  auto load_weights = [&](Weights &w, int item, int c) {
+    if (item >= items) return;
+    const int ai = item / tiles;
+    const int e = r.reached[ai].expert_base & 0xffff;
+    const int row = min((item - ai * tiles) * 16 + i16, a.inter - 1);
+    const long long gate = static_cast<long long>(__builtin_amdgcn_readfirstlane(e)) * 2 * a.inter + row;
+    const long long up = gate + a.inter;
+    const unsigned char *gc = a.w1c + gate * (HP / 2) + g * 16, *gs = a.w1s + gate * (HP / 32) + g;
+    const unsigned char *uc = a.w1c + up * (HP / 2) + g * 16, *us = a.w1s + up * (HP / 32) + g;
+#pragma unroll
+    for (int b = 0; b < kAt; ++b) {
+      const int cb = c + b * kMoeWaves;
+      if (cb < chunks) {
+        w.gate[b] = *reinterpret_cast<const uintx4 *>(gc + cb * 64);
+        w.up[b] = *reinterpret_cast<const uintx4 *>(uc + cb * 64);
+        w.gate_scale[b] = gs[cb * 4];
+        w.up_scale[b] = us[cb * 4];
+      }
+    }
+  };
+
+  Weights cur, next;
+  load_weights(cur, blockIdx.x, wave);
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int ai = item / tiles;
     const int row0 = (item - ai * tiles) * 16;
-    const int e = r.active[ai];
-    const int base = r.base[e];
-    const int count = __popc(r.lo[e]) + __popc(r.hi[e]);
-    const int used = (count + 15) / 16;
-    f32x4 acc[2 * kTokenTiles] = {};   // gate and up of each tile of 16 tokens
-    if (row0 < a.inter) {
-      const long long row = min(row0 + i16, a.inter - 1);
-      const long long gate = static_cast<long long>(e) * 2 * a.inter + row, up = gate + a.inter;
-      const unsigned char *gc = a.w1c + gate * (HP / 2) + g * 16, *gs = a.w1s + gate * (HP / 32) + g;
-      const unsigned char *uc = a.w1c + up * (HP / 2) + g * 16, *us = a.w1s + up * (HP / 32) + g;
-      for (int c = wave; c < HP / 128; c += kMoeWaves) {
-        const uintx4 wg = *reinterpret_cast<const uintx4 *>(gc + c * 64);
-        const uintx4 wu = *reinterpret_cast<const uintx4 *>(uc + c * 64);
-        const float fg = scale_value(gs[c * 4]), fu = scale_value(us[c * 4]);
-        const int k = c * 128 + g * 32;
+    const Reached now = r.reached[ai];
+    const int base = __builtin_amdgcn_readfirstlane(now.expert_base >> 16);
+    const int count = __builtin_amdgcn_readfirstlane(__popc(now.lo) + __popc(now.hi));
+    for (int first = 0; first < count; first += 16 * kUpTiles) {   // tokens of the expert
+      const int used = min(kUpTiles, (count - first + 15) / 16);
+      const bool last = first + 16 * kUpTiles >= count;
+      f32x4 acc[2 * kUpTiles] = {};   // gate and up of each tile of 16 tokens
+      for (int c = wave; c < chunks || c == wave; c += kAt * kMoeWaves) {
+        const bool more = c + kAt * kMoeWaves < chunks;
+        load_weights(next, more || !last ? item : item + gridDim.x, more ? c + kAt * kMoeWaves : wave);
 #pragma unroll
-        for (int t = 0; t < kTokenTiles; ++t) {
+        for (int t = 0; t < kUpTiles; ++t) {
           if (t < used) {
-            const int n = t * 16 + i16;
-            const store *px = x + static_cast<long long>(n < count ? r.token[base + n] : 0) * a.ldx + k;
-            const int left = n < count ? a.hidden - k : 0;
+            const int n = first + t * 16 + i16;
+            const store *px = x + static_cast<long long>(n < count ? r.token[base + n] : 0) * a.ldx + g * 32;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              bf16x8 xv[PX];
-              load_x8<TYPE, VEC>(px + j * 8, left - j * 8, xv);
-              const bf16x8 vg = weights8(wg[j], fg), vu = weights8(wu[j], fu);
+            for (int b = 0; b < kAt; ++b) {
+              const int k = (c + b * kMoeWaves) * 128;
+              if (k < HP) {
+                RawX<TYPE> raw = {};
+                if (n < count) {
+                  if (VEC && k + 128 <= a.hidden)
+                    raw.template load<true>(px + k, 32);
+                  else
+                    raw.template load<false>(px + k, a.hidden - k - g * 32);
+                }
+                const float fg = scale_value(cur.gate_scale[b]), fu = scale_value(cur.up_scale[b]);
 #pragma unroll
-              for (int p = 0; p < PX; ++p) {
-                acc[2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, xv[p], acc[2 * t], 0, 0, 0);
-                acc[2 * t + 1] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, xv[p], acc[2 * t + 1], 0, 0, 0);
+                for (int j = 0; j < 4; ++j) {
+                  bf16x8 xv[PX];
+                  raw.parts(j, xv);
+                  const bf16x8 vg = weights8(cur.gate[b][j], fg), vu = weights8(cur.up[b][j], fu);
+#pragma unroll
+                  for (int p = 0; p < PX; ++p) {
+                    acc[2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, xv[p], acc[2 * t], 0, 0, 0);
+                    acc[2 * t + 1] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, xv[p], acc[2 * t + 1], 0, 0, 0);
+                  }
+                }
               }
             }
           }
         }
+        cur = next;
       }
-    }
-    // thread: tile wave / 2's gate (even waves) or up (odd waves) sums
-    const f32x4 s = reduce_waves<2 * kTokenTiles>(acc, 2 * used, red);
-    if (wave < 2 * used) red[wave * 64 + lane] = s;
-    __syncthreads();
-    if (wave < used) {
-      const f32x4 gv = red[(2 * wave) * 64 + lane], uv = red[(2 * wave + 1) * 64 + lane];
-      const int n = wave * 16 + i16;
-      if (n < count) {
-        const int p = base + n;
-        const float w = r.weight[p];
-        const int row = row0 + 4 * g;
+      const f32x4 s = reduce_waves<2 * kUpTiles>(acc, 2 * used, red);
+      if (wave < 2 * used) red[wave * 64 + lane] = s;
+      __syncthreads();
+      if (wave < used) {
+        const f32x4 gv = red[(2 * wave) * 64 + lane], uv = red[(2 * wave + 1) * 64 + lane];
+        const int n = first + wave * 16 + i16;
+        if (n < count) {
+          const int p = base + n;
+          const float w = r.weight[p];
+          const int row = row0 + 4 * g;
+          u16 parts[PH][4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          // past the last row of an expert: the zeros that pad `inter`
-          float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
+          for (int v = 0; v < 4; ++v) {
+            // past the last row of an expert: the zeros that pad `inter`
+            float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
 #pragma unroll
-          for (int q = 0; q < PH; ++q) {
-            const unsigned b = __builtin_bit_cast(unsigned, rest);
-            const u16 part = q + 1 < PH || PH == 3 ? static_cast<u16>(b >> 16) : Elem<kBf16>::put(rest);
-            a.h[q * plane + static_cast<long long>(p) * IP + row + v] = part;
-            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
+            for (int q = 0; q < PH; ++q) {
+              const unsigned b = __builtin_bit_cast(unsigned, rest);
+              parts[q][v] = q + 1 < PH || PH == 3 ? static_cast<u16>(b >> 16) : Elem<kBf16>::put(rest);
+              rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(parts[q][v]);
+            }
           }
+#pragma unroll
+          for (int q = 0; q < PH; ++q)
+            *reinterpret_cast<uintx2 *>(a.h + q * plane + static_cast<long long>(p) * IP + row) =
+                uintx2{parts[q][0] | (static_cast<unsigned>(parts[q][1]) << 16),
+                       parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
+// Y: a workgroup takes 16 rows of every reached expert's D, its waves the
+// (expert, chunk of 128) steps in turn, two a wave at a time, the next two's
+// weights on their way.
 template <int TYPE>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PH = Parts<TYPE>::h;
-  __shared__ Routing r;
+  constexpr int kAt = 2;
+  __shared__ Reached reached[kMaxExperts + 1];
   __shared__ __attribute__((aligned(16))) f32x4 red[kMoeWaves * kTokenTiles * 64];
-  route(a, r);
+  const int most = min(a.experts, a.tokens * a.top_k) + 1;
+  for (int n = threadIdx.x; n < most; n += kMoeThreads) reached[n] = a.reached[n];
+  __syncthreads();
+  const int num_reached = __builtin_amdgcn_readfirstlane(reached[0].expert_base);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
@@ -372,43 +482,93 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(MoeArgs a) {
   const int row0 = blockIdx.x * 16;
   const int row = min(row0 + i16, a.hidden - 1);
   const int token_tiles = (a.tokens + 15) / 16;
-  f32x4 acc[kTokenTiles] = {};
-  for (int s = wave; s < r.num_active * chunks; s += kMoeWaves) {
-    const int ai = s / chunks, c = s - ai * chunks;
-    const int e = r.active[ai];
-    const long long wr = static_cast<long long>(e) * a.hidden + row;
-    const uintx4 w = *reinterpret_cast<const uintx4 *>(a.w2c + wr * (IP / 2) + c * 64 + g * 16);
-    const float f = scale_value(a.w2s[wr * (IP / 32) + c * 4 + g]);
-    const unsigned long long m = r.lo[e] | (static_cast<unsigned long long>(r.hi[e]) << 32);
+
+  // A step: reached expert `at` (num_reached: none left) and chunk c.
+  struct Step {
+    int at, c;
+  };
+  auto advance = [&](Step s) {
+    s.c += kMoeWaves;
+    while (s.c >= chunks && s.at < num_reached) {
+      s.c -= chunks;
+      ++s.at;
+    }
+    return s;
+  };
+  struct Weights {
+    uintx4 w[kAt];
+    unsigned scale[kAt];
+  };
+  auto load_weights = [&](Weights &w, const Step (&s)[kAt]) {
 #pragma unroll
-    for (int t = 0; t < kTokenTiles; ++t) {
-      if (t < token_tiles && ((m >> (16 * t)) & 0xffffull)) {
-        const int n = t * 16 + i16;
-        const bool has = (m >> n) & 1;
-        const int p = r.base[e] + __popcll(m & ((1ull << n) - 1));
-        const u16 *h = a.h + static_cast<long long>(has ? p : 0) * IP + c * 128 + g * 32;
-        f32x4 next = acc[t];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 v = weights8(w[j], f);
-#pragma unroll
-          for (int q = 0; q < PH; ++q) {
-            bf16x8 hv = {};
-            if (has) hv = *reinterpret_cast<const bf16x8 *>(h + q * plane + j * 8);
-            next = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, hv, next, 0, 0, 0);
-          }
-        }
-        // A token that did not choose this expert keeps its sum, also where the
-        // expert's weights hold a NaN (0 * NaN is not 0).
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[t][v] = has ? next[v] : acc[t][v];
+    for (int b = 0; b < kAt; ++b) {
+      if (s[b].at < num_reached) {
+        const int e = __builtin_amdgcn_readfirstlane(reached[1 + s[b].at].expert_base & 0xffff);
+        const long long wr = static_cast<long long>(e) * a.hidden + row;
+        w.w[b] = *reinterpret_cast<const uintx4 *>(a.w2c + wr * (IP / 2) + s[b].c * 64 + g * 16);
+        w.scale[b] = a.w2s[wr * (IP / 32) + s[b].c * 4 + g];
       }
     }
+  };
+  f32x4 acc[kTokenTiles] = {};
+  Step step[kAt];
+  step[0] = advance(Step{0, wave - kMoeWaves});
+#pragma unroll
+  for (int b = 1; b < kAt; ++b) step[b] = advance(step[b - 1]);
+  Weights cur, next;
+  load_weights(cur, step);
+  while (step[0].at < num_reached) {
+    Step then[kAt];
+    then[0] = advance(step[kAt - 1]);
+#pragma unroll
+    for (int b = 1; b < kAt; ++b) then[b] = advance(then[b - 1]);
+    load_weights(next, then);
+#pragma unroll
+    for (int b = 0; b < kAt; ++b) {
+      if (step[b].at >= num_reached) continue;
+      const Reached now = reached[1 + step[b].at];
+      const unsigned long long m =
+          static_cast<unsigned>(__builtin_amdgcn_readfirstlane(now.lo)) |
+          (static_cast<unsigned long long>(static_cast<unsigned>(__builtin_amdgcn_readfirstlane(now.hi))) << 32);
+      const float f = scale_value(cur.scale[b]);
+#pragma unroll
+      for (int t = 0; t < kTokenTiles; ++t) {
+        if (t < token_tiles && ((m >> (16 * t)) & 0xffffull)) {
+          const int n = t * 16 + i16;
+          const bool has = (m >> n) & 1;
+          bf16x8 hv[PH][4] = {};
+          if (has) {
+            const int p = (now.expert_base >> 16) + __popcll(m & ((1ull << n) - 1));
+            const u16 *h = a.h + static_cast<long long>(p) * IP + step[b].c * 128 + g * 32;
+#pragma unroll
+            for (int q = 0; q < PH; ++q)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                hv[q][j] = *reinterpret_cast<const bf16x8 *>(h + q * plane + j * 8);
+          }
+          f32x4 sum = acc[t];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8 v = weights8(cur.w[b][j], f);
+#pragma unroll
+            for (int q = 0; q < PH; ++q)
+              sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, hv[q][j], sum, 0, 0, 0);
+          }
+          // A token that did not choose this expert keeps its sum, also where the
+          // expert's weights hold a NaN (0 * NaN is not 0).
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[t][v] = has ? sum[v] : acc[t][v];
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kAt; ++b) step[b] = then[b];
+    cur = next;
   }
   const f32x4 sum = reduce_waves<kTokenTiles>(acc, token_tiles, red);
   const int t = wave * 16 + i16;
   if (wave < token_tiles && t < a.tokens) {
-    const bool nan = ((t < 32 ? r.nan_lo : r.nan_hi) >> (t & 31)) & 1;
+    const bool nan = ((t < 32 ? reached[0].lo : reached[0].hi) >> (t & 31)) & 1;
     store *y = static_cast<store *>(a.y) + static_cast<long long>(t) * a.ldy + row0 + 4 * g;
 #pragma unroll
     for (int v = 0; v < 4; ++v)

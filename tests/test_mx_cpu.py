@@ -29,8 +29,11 @@ def test_sizes():
     assert lib.gemm_mx_codes_bytes(2 ** 31 - 1, 4096) == 0   # more than 2^40 values
     # past 32 bits
     assert lib.gemm_mx_codes_bytes(1 << 20, 8192) == (1 << 20) * 4096
-    assert lib.gemm_mx_moe_workspace_bytes(2, 100, 3, lib.GEMM_TYPE_BF16) == 2 * 3 * 128 * 2 * 2
-    assert lib.gemm_mx_moe_workspace_bytes(2, 100, 3, lib.GEMM_TYPE_F32) == 3 * 2 * 3 * 128 * 2
+    # hidden activations in 2 or 3 bfloat16 parts, and the list of reached experts
+    few = lib.gemm_mx_moe_workspace_bytes(1, 1, 1, lib.GEMM_TYPE_BF16) - 2 * 128 * 2
+    assert 0 < few <= 16384
+    assert lib.gemm_mx_moe_workspace_bytes(2, 100, 3, lib.GEMM_TYPE_BF16) == 2 * 3 * 128 * 2 * 2 + few
+    assert lib.gemm_mx_moe_workspace_bytes(2, 100, 3, lib.GEMM_TYPE_F32) == 3 * 2 * 3 * 128 * 2 + few
     for bad in ((0, 1, 1, 0), (65, 1, 1, 0), (1, 0, 1, 0), (1, 1, 0, 0), (1, 1, 17, 0), (1, 1, 1, 3)):
         assert lib.gemm_mx_moe_workspace_bytes(*bad) == 0
 
