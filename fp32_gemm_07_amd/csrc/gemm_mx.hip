@@ -267,7 +267,7 @@ int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
   if (st != GEMM_OK) return st;
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(kMoeThreads), 0, stream, a);
+    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(kDownThreads), 0, stream, a);
   });
   return launched();
 }

@@ -29,6 +29,8 @@ namespace mx {
 
 constexpr int kMoeWaves = 8;
 constexpr int kMoeThreads = 64 * kMoeWaves;
+constexpr int kDownWaves = 16;   // of the second kernel
+constexpr int kDownThreads = 64 * kDownWaves;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;   // GEMM_MX_MOE_MAX_*
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kTokenTiles = kMaxTokens / 16;
@@ -64,141 +66,154 @@ struct MoeArgs {
 
 // What a workgroup knows after routing.
 struct Routing {
-  unsigned lo[kMaxExperts], hi[kMaxExperts];   // tokens that chose the expert, one bit each
-  Reached reached[kMaxExperts];                // reached experts, ascending
-  unsigned char token[kMaxPairs];              // the pair's token
-  float weight[kMaxPairs];                     // the pair's weight
-  u16 base[kMaxExperts];                       // the expert's first pair
-  u16 chosen[kMaxTokens * kMaxTopK];           // token t's experts at t * kMaxTopK
-  float chosen_weight[kMaxTokens * kMaxTopK];
-  unsigned char count[kMaxTokens];             // how many it has
-  unsigned nan_lo, nan_hi;                     // tokens whose logits hold a NaN or +inf
+  Reached reached[kMaxExperts];     // reached experts, ascending
+  float weight[kMaxPairs];          // the pair's weight
+  unsigned char token[kMaxPairs];   // the pair's token
+  unsigned nan_lo, nan_hi;          // tokens whose logits hold a NaN or +inf
   int num_reached;
 };
+// What it needs on the way there.
+struct RoutingScratch {
+  unsigned lo[kMaxExperts], hi[kMaxExperts];   // tokens that chose the expert, one bit each
+  u16 base[kMaxExperts];                       // the expert's first pair
+  u16 chosen[kMaxTokens * kMaxTopK];           // token t's experts at t * kMaxTopK, 0xffff: none
+  float chosen_weight[kMaxTokens * kMaxTopK];
+};
 
-// Sums, maxima and running sums over a wave by lane shifts within rows of 16
-// (dpp row_shr 1, 2, 4, 8) and broadcasts of the last lane of a row and of the
-// first half (row_bcast 15, 31); the last lane ends with the whole.
 template <int CTRL, int ROWS>
 __device__ inline int dpp(int identity, int v) {
   return __builtin_amdgcn_update_dpp(identity, v, CTRL, ROWS, 0xf, false);
 }
+// op over the 16 lanes of a row (rotations by 1, 2, 4, 8), in every lane.
 template <class OP>
-__device__ inline int wave_scan(int v, int identity, OP &&op) {
-  v = op(v, dpp<0x111, 0xf>(identity, v));
-  v = op(v, dpp<0x112, 0xf>(identity, v));
-  v = op(v, dpp<0x114, 0xf>(identity, v));
-  v = op(v, dpp<0x118, 0xf>(identity, v));
-  v = op(v, dpp<0x142, 0xa>(identity, v));
-  return op(v, dpp<0x143, 0xc>(identity, v));
+__device__ inline int row_all(int v, OP &&op) {
+  v = op(v, dpp<0x121, 0xf>(0, v));
+  v = op(v, dpp<0x122, 0xf>(0, v));
+  v = op(v, dpp<0x124, 0xf>(0, v));
+  return op(v, dpp<0x128, 0xf>(0, v));
 }
-__device__ inline float wave_sum(float v) {
-  const int s = wave_scan(__builtin_bit_cast(int, v), 0, [](int a, int b) {
-    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
-  });
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(s, 63));
-}
-__device__ inline unsigned wave_max(unsigned v) {
-  const int m = wave_scan(static_cast<int>(v), 0, [](int a, int b) {
+__device__ inline unsigned row_max(unsigned v) {
+  return static_cast<unsigned>(row_all(static_cast<int>(v), [](int a, int b) {
     return static_cast<int>(max(static_cast<unsigned>(a), static_cast<unsigned>(b)));
-  });
-  return static_cast<unsigned>(__builtin_amdgcn_readlane(m, 63));
+  }));
+}
+__device__ inline int row_min(int v) {
+  return row_all(v, [](int a, int b) { return min(a, b); });
+}
+__device__ inline float row_sum(float v) {
+  return __builtin_bit_cast(float, row_all(__builtin_bit_cast(int, v), [](int a, int b) {
+    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+  }));
+}
+// Running sums over a wave: shifts within rows, then the last lane of each row
+// and of the first half handed on (row_bcast 15, 31).
+__device__ inline int wave_running_sum(int v) {
+  v += dpp<0x111, 0xf>(0, v);
+  v += dpp<0x112, 0xf>(0, v);
+  v += dpp<0x114, 0xf>(0, v);
+  v += dpp<0x118, 0xf>(0, v);
+  v += dpp<0x142, 0xa>(0, v);
+  return v + dpp<0x143, 0xc>(0, v);
 }
 
-// Routes all tokens; ends with a barrier. A wave takes a token at a time, its
-// lanes the experts lane, lane + 64, ..: top_k rounds of a maximum over the
-// wave. Logits are compared as whole numbers in their order (0: not to be
-// chosen).
-__device__ inline void route(const MoeArgs &a, Routing &r) {
-  constexpr int kPer = kMaxExperts / 64;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int e = threadIdx.x; e < a.experts; e += kMoeThreads) r.lo[e] = r.hi[e] = 0;
-  if (threadIdx.x == 0) r.nan_lo = r.nan_hi = 0;
-  __syncthreads();
-  for (int t = wave; t < a.tokens; t += kMoeWaves) {
-    const float *l = a.logits + static_cast<long long>(t) * a.ld_logits;
-    unsigned key[kPer];
-    float val[kPer];
-    bool bad = false;
+// The choice of 4 tokens, one to each row of 16 lanes, whose lanes hold the
+// experts l, l + 16, ..: top_k rounds of a maximum over the row. Logits are
+// compared as whole numbers in their order (0: not to be chosen).
+template <int PER>
+__device__ inline void choose(const MoeArgs &a, int t, Routing &r, RoutingScratch &s) {
+  const int l16 = threadIdx.x & 15;
+  const bool ok = t < a.tokens;
+  const float *l = a.logits + static_cast<long long>(ok ? t : 0) * a.ld_logits;
+  float val[PER];
+  unsigned key[PER];
+  bool bad = false;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = j * 64 + lane;
-      key[j] = 0;
-      val[j] = -__builtin_inff();
-      if (j * 64 < a.experts && e < a.experts) {
-        val[j] = l[e] + 0.0f;   // -0 compares equal to +0
-        const unsigned b = __builtin_bit_cast(unsigned, val[j]);
-        if (magnitude_bits(val[j]) > 0x7f800000u || b == 0x7f800000u)
-          bad = true;
-        else if (b != 0xff800000u)
-          key[j] = b & 0x80000000u ? ~b : b | 0x80000000u;
-      }
+  for (int j = 0; j < PER; ++j) {
+    const int e = j * 16 + l16;
+    val[j] = ok && e < a.experts ? l[e] + 0.0f : -__builtin_inff();   // -0 equals +0
+  }
+  unsigned best = 0;
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const unsigned b = __builtin_bit_cast(unsigned, val[j]);
+    if (magnitude_bits(val[j]) > 0x7f800000u || b == 0x7f800000u) bad = true;
+    key[j] = b == 0xff800000u ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+    if (key[j] > best) {
+      best = key[j];
+      at = j;
     }
-    if (__ballot(bad)) {
-      if (lane == 0) {
-        atomicOr(t < 32 ? &r.nan_lo : &r.nan_hi, 1u << (t & 31));
-        r.count[t] = 0;
-      }
-      continue;
+  }
+  bad = row_max(bad) != 0;
+  float top = 0.0f, mine = -__builtin_inff();
+  int my_expert = 0xffff;
+  for (int n = 0; n < a.top_k; ++n) {
+    const unsigned most = row_max(best);
+    const int expert = row_min(best == most ? at * 16 + l16 : kMaxExperts);
+    const bool some = most != 0 && !bad;
+    const float logit = __builtin_bit_cast(float, most & 0x80000000u ? most & 0x7fffffffu : ~most);
+    if (n == 0) top = logit;
+    if (l16 == n && some) {
+      mine = logit;
+      my_expert = expert;
     }
-    float top = 0.0f, mine = -__builtin_inff();
-    int n = 0, my_expert = 0;
-    for (; n < a.top_k; ++n) {
-      unsigned best = 0;
+    if (expert == at * 16 + l16) {   // its lane looks for its next
+      const int gone = at;
+      best = 0;
+      at = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j * 64 < a.experts) best = max(best, key[j]);
-      best = wave_max(best);
-      if (best == 0) break;
-      const float logit =
-          __builtin_bit_cast(float, best & 0x80000000u ? best & 0x7fffffffu : ~best);
-      if (n == 0) top = logit;
-      int expert = -1;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (j * 64 < a.experts && expert < 0) {
-          const unsigned long long who = __ballot(key[j] == best);
-          if (who) {
-            const int first = __builtin_ctzll(who);
-            expert = j * 64 + first;
-            if (lane == first) key[j] = 0;
-          }
+      for (int j = 0; j < PER; ++j) {
+        if (j == gone) key[j] = 0;
+        if (key[j] > best) {
+          best = key[j];
+          at = j;
         }
       }
-      if (lane == n) {
-        mine = logit;
-        my_expert = expert;
-      }
     }
-    // softmax: lane n < top_k has the n-th chosen logit, -inf behind them
-    const float p = expf(mine - top);
-    float sum = p;
-    if (!a.renormalize) {
-      sum = 0.0f;
+  }
+  // softmax: lane n < top_k has the n-th chosen logit, -inf behind them
+  const float p = expf(mine - top);
+  float sum = p;
+  if (!a.renormalize) {
+    sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j * 64 < a.experts) sum += expf(val[j] - top);
-    }
-    sum = wave_sum(sum);
-    if (lane == 0) r.count[t] = static_cast<unsigned char>(n);
-    if (lane < n) {
-      r.chosen[t * kMaxTopK + lane] = static_cast<u16>(my_expert);
-      r.chosen_weight[t * kMaxTopK + lane] = p / sum;
-      atomicOr(t < 32 ? &r.lo[my_expert] : &r.hi[my_expert], 1u << (t & 31));
-    }
+    for (int j = 0; j < PER; ++j) sum += expf(val[j] - top);
+  }
+  sum = row_sum(sum);
+  if (ok) {
+    s.chosen[t * kMaxTopK + l16] = static_cast<u16>(my_expert);
+    s.chosen_weight[t * kMaxTopK + l16] = p / sum;
+    if (my_expert != 0xffff)
+      atomicOr(t < 32 ? &s.lo[my_expert] : &s.hi[my_expert], 1u << (t & 31));
+    if (bad && l16 == 0) atomicOr(t < 32 ? &r.nan_lo : &r.nan_hi, 1u << (t & 31));
+  }
+}
+
+// Routes all tokens; ends with a barrier.
+__device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int e = threadIdx.x; e < a.experts; e += kMoeThreads) s.lo[e] = s.hi[e] = 0;
+  if (threadIdx.x == 0) r.nan_lo = r.nan_hi = 0;
+  __syncthreads();
+  for (int t0 = wave * 4; t0 < a.tokens; t0 += kMoeWaves * 4) {
+    const int t = t0 + (lane >> 4);
+    if (a.experts <= 64) choose<4>(a, t, r, s);
+    else if (a.experts <= 128) choose<8>(a, t, r, s);
+    else if (a.experts <= 256) choose<16>(a, t, r, s);
+    else choose<32>(a, t, r, s);
   }
   __syncthreads();
   if (wave == 0) {
     int pairs = 0, reached = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
       const int e = e0 + lane;
-      const unsigned lo = e < a.experts ? r.lo[e] : 0, hi = e < a.experts ? r.hi[e] : 0;
+      const unsigned lo = e < a.experts ? s.lo[e] : 0, hi = e < a.experts ? s.hi[e] : 0;
       const int c = __popc(lo) + __popc(hi);
-      const int upto = wave_scan(c, 0, [](int x, int y) { return x + y; });
+      const int upto = wave_running_sum(c);
       const unsigned long long who = __ballot(c > 0);
       const unsigned base = static_cast<unsigned>(pairs + upto - c);
-      if (e < a.experts) r.base[e] = static_cast<u16>(base);
+      if (e < a.experts) s.base[e] = static_cast<u16>(base);
       if (c > 0)
         r.reached[reached + __popcll(who & ((1ull << lane) - 1))] =
             Reached{static_cast<unsigned>(e) | (base << 16), lo, hi};
@@ -209,13 +224,13 @@ __device__ inline void route(const MoeArgs &a, Routing &r) {
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.tokens * kMaxTopK; i += kMoeThreads) {
-    const int t = i / kMaxTopK, n = i % kMaxTopK;
-    if (n < r.count[t]) {
-      const int e = r.chosen[i];
-      const unsigned long long m = r.lo[e] | (static_cast<unsigned long long>(r.hi[e]) << 32);
-      const int p = r.base[e] + __popcll(m & ((1ull << t) - 1));
+    const int e = s.chosen[i];
+    if (e != 0xffff) {
+      const int t = i / kMaxTopK;
+      const unsigned long long m = s.lo[e] | (static_cast<unsigned long long>(s.hi[e]) << 32);
+      const int p = s.base[e] + __popcll(m & ((1ull << t) - 1));
       r.token[p] = static_cast<unsigned char>(t);
-      r.weight[p] = r.chosen_weight[i];
+      r.weight[p] = s.chosen_weight[i];
     }
   }
   __syncthreads();
@@ -259,9 +274,9 @@ __device__ inline bf16x8 weights8(unsigned codes, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Sums acc over the workgroup's waves through LDS (red: kMoeWaves * TILES * 64),
-// in wave order: afterwards wave w < used holds tile w's sums, the lanes as acc.
-template <int TILES>
+// Sums acc over the workgroup's waves through LDS (red: WAVES * TILES * 64), in
+// wave order: afterwards wave w < used holds tile w's sums, the lanes as acc.
+template <int TILES, int WAVES>
 __device__ inline f32x4 reduce_waves(const f32x4 (&acc)[TILES], int used, f32x4 *red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -272,9 +287,8 @@ __device__ inline f32x4 reduce_waves(const f32x4 (&acc)[TILES], int used, f32x4 
   if (wave < used) {
     s = red[wave * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) s += red[(w * TILES + wave) * 64 + lane];
+    for (int w = 1; w < WAVES; ++w) s += red[(w * TILES + wave) * 64 + lane];
   }
-  __syncthreads();
   return s;
 }
 
@@ -333,8 +347,12 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_
   constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
   constexpr int kAt = 2;   // chunks of a wave at a time
   __shared__ Routing r;
-  __shared__ __attribute__((aligned(16))) f32x4 red[kMoeWaves * 2 * kUpTiles * 64];
-  route(a, r);
+  // partial sums of the waves, of two items in turn; scratch of the routing first
+  constexpr int kRed = kMoeWaves * 2 * kUpTiles * 64;
+  __shared__ __attribute__((aligned(16))) f32x4 red[2 * kRed];
+  static_assert(sizeof(RoutingScratch) <= sizeof(red), "scratch fits");
+  route(a, r, *reinterpret_cast<RoutingScratch *>(red));
+  int half = 0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int num_reached = __builtin_amdgcn_readfirstlane(r.num_reached);
@@ -425,11 +443,21 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_
         }
         cur = next;
       }
-      const f32x4 s = reduce_waves<2 * kUpTiles>(acc, 2 * used, red);
-      if (wave < 2 * used) red[wave * 64 + lane] = s;
+      // One barrier an item: the next one's sums go to the other half, and nobody
+      // writes this half again before having passed the next barrier.
+      f32x4 *mine = red + half * kRed;
+      half ^= 1;
+#pragma unroll
+      for (int t = 0; t < 2 * kUpTiles; ++t)
+        if (t < 2 * used) mine[(wave * 2 * kUpTiles + t) * 64 + lane] = acc[t];
       __syncthreads();
       if (wave < used) {
-        const f32x4 gv = red[(2 * wave) * 64 + lane], uv = red[(2 * wave + 1) * 64 + lane];
+        f32x4 gv = mine[(2 * wave) * 64 + lane], uv = mine[(2 * wave + 1) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kMoeWaves; ++w) {
+          gv += mine[(w * 2 * kUpTiles + 2 * wave) * 64 + lane];
+          uv += mine[(w * 2 * kUpTiles + 2 * wave + 1) * 64 + lane];
+        }
         const int n = first + wave * 16 + i16;
         if (n < count) {
           const int p = base + n;
@@ -454,7 +482,6 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_
                        parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
         }
       }
-      __syncthreads();
     }
   }
 }
@@ -463,14 +490,14 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_
 // (expert, chunk of 128) steps in turn, two a wave at a time, the next two's
 // weights on their way.
 template <int TYPE>
-__global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kDownThreads, 4) void moe_down_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PH = Parts<TYPE>::h;
   constexpr int kAt = 2;
   __shared__ Reached reached[kMaxExperts + 1];
-  __shared__ __attribute__((aligned(16))) f32x4 red[kMoeWaves * kTokenTiles * 64];
+  __shared__ __attribute__((aligned(16))) f32x4 red[kDownWaves * kTokenTiles * 64];
   const int most = min(a.experts, a.tokens * a.top_k) + 1;
-  for (int n = threadIdx.x; n < most; n += kMoeThreads) reached[n] = a.reached[n];
+  for (int n = threadIdx.x; n < most; n += kDownThreads) reached[n] = a.reached[n];
   __syncthreads();
   const int num_reached = __builtin_amdgcn_readfirstlane(reached[0].expert_base);
   const int lane = threadIdx.x & 63;
@@ -488,7 +515,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a) {
     int at, c;
   };
   auto advance = [&](Step s) {
-    s.c += kMoeWaves;
+    s.c += kDownWaves;
     while (s.c >= chunks && s.at < num_reached) {
       s.c -= chunks;
       ++s.at;
@@ -512,7 +539,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a) {
   };
   f32x4 acc[kTokenTiles] = {};
   Step step[kAt];
-  step[0] = advance(Step{0, wave - kMoeWaves});
+  step[0] = advance(Step{0, wave - kDownWaves});
 #pragma unroll
   for (int b = 1; b < kAt; ++b) step[b] = advance(step[b - 1]);
   Weights cur, next;
@@ -565,7 +592,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_down_kernel(MoeArgs a) {
     for (int b = 0; b < kAt; ++b) step[b] = then[b];
     cur = next;
   }
-  const f32x4 sum = reduce_waves<kTokenTiles>(acc, token_tiles, red);
+  const f32x4 sum = reduce_waves<kTokenTiles, kDownWaves>(acc, token_tiles, red);
   const int t = wave * 16 + i16;
   if (wave < token_tiles && t < a.tokens) {
     const bool nan = ((t < 32 ? reached[0].lo : reached[0].hi) >> (t & 31)) & 1;
