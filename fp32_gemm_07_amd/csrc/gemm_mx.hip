@@ -242,19 +242,20 @@ int check_workspace(const void *workspace, size_t bytes, size_t need, std::initi
 
 // ---------------------------------------------------------------------------
 // The mixture-of-experts layer.
-constexpr size_t kReachedBytes = (kMaxExperts + 1) * sizeof(Reached) / 16 * 16 + 16;   // of the workspace's head
+constexpr size_t kGroupBytes = (kMaxGroups + 1) * sizeof(Group) / 16 * 16 + 16;   // the workspace's head
 
 size_t moe_workspace(int tokens, int inter, int top_k, int type) {
   const size_t parts = type == kF32 ? Parts<kF32>::h : Parts<kBf16>::h;
   const size_t hidden = parts * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
-  return hidden + kReachedBytes;
+  return hidden + kGroupBytes;
 }
 
 int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
-  const bool vec = aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(type)) % 16 == 0;
-  const long long reached = std::min<long long>(static_cast<long long>(a.tokens) * a.top_k, a.experts);
+  const bool vec = a.hidden % 8 == 0 && aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(type)) % 16 == 0;
+  const long long pairs = static_cast<long long>(a.tokens) * a.top_k;
+  const long long groups = std::min<long long>(pairs, a.experts) + pairs / kGroup;
   const unsigned up = static_cast<unsigned>(
-      std::min<long long>(reached * (padded(a.inter) / 16), 2LL * cus));
+      std::min<long long>(groups * (padded(a.inter) / 16), 2LL * cus));
   const unsigned down = static_cast<unsigned>(ceil_div(a.hidden, 16));
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
@@ -267,7 +268,7 @@ int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
   if (st != GEMM_OK) return st;
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(kDownThreads), 0, stream, a);
+    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(64 * Parts<T>::down_waves), 0, stream, a);
   });
   return launched();
 }
@@ -451,8 +452,8 @@ int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int r
   auto body = [](void *c, void *ws) {
     const Call *k = static_cast<const Call *>(c);
     if (!ws) return static_cast<int>(GEMM_ERR_WORKSPACE);
-    k->a->reached = static_cast<Reached *>(ws);
-    k->a->h = reinterpret_cast<u16 *>(static_cast<char *>(ws) + kReachedBytes);
+    k->a->groups = static_cast<Group *>(ws);
+    k->a->h = reinterpret_cast<u16 *>(static_cast<char *>(ws) + kGroupBytes);
     return launch_moe(*k->a, k->type, k->cus, k->stream);
   };
   if (workspace) return body(&call, workspace);

@@ -5,7 +5,8 @@
 //   down:  Y = sum over the reached experts of D a.
 // Every workgroup of the first kernel works the routing out for itself from the
 // logits (a few microseconds at most, and no third launch or hand-over between
-// workgroups); one of them leaves the list of reached experts for the second.
+// workgroups); one of them leaves the list of the reached experts and their tokens for the
+// second.
 //
 // Both products stream their weights from memory once, straight into
 // registers: 16 weight rows are the rows of v_mfma_f32_16x16x32_bf16, 16 tokens
@@ -27,29 +28,41 @@
 namespace gemm {
 namespace mx {
 
-constexpr int kMoeWaves = 8;
+constexpr int kMoeWaves = 8;   // of the first kernel
 constexpr int kMoeThreads = 64 * kMoeWaves;
-constexpr int kDownWaves = 16;   // of the second kernel
-constexpr int kDownThreads = 64 * kDownWaves;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;   // GEMM_MX_MOE_MAX_*
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
-constexpr int kTokenTiles = kMaxTokens / 16;
-constexpr int kUpTiles = 2;   // tiles of 16 tokens that the first kernel takes at a time
+constexpr int kGroup = 8;   // tokens of an expert taken at a time
+constexpr int kMaxGroups = kMaxExperts + kMaxPairs / kGroup;
 
 template <int TYPE>
 struct Parts {
   static constexpr int x = TYPE == kF32 ? 3 : TYPE == kF16 ? 2 : 1;   // of the inputs
   static constexpr int h = TYPE == kF32 ? 3 : 2;                      // of the hidden activations
+  // waves of the second kernel, and the waves a SIMD that both are built for, by
+  // the registers that the parts in flight take
+  static constexpr int down_waves = TYPE == kF32 ? 8 : 16;
+  static constexpr int up_per_simd = TYPE == kBf16 ? 4 : 2, down_per_simd = TYPE == kF32 ? 2 : 4;
 };
 
-// A reached expert: its number, the tokens that chose it (one bit each) and its
-// first pair. Pairs (token, expert) are numbered by expert, then token; pair
-// numbers index the rows of the hidden activations. Entry 0 of the workspace's
-// list holds how many follow and the tokens whose logits hold a NaN or +inf.
-struct Reached {
-  unsigned expert_base;   // expert in the low, first pair in the high half
+// Up to kGroup tokens of one expert: the expert, how many tokens, their first
+// pair and the tokens (a byte each, the first one again where there are fewer).
+// Pairs (token, expert) are numbered by expert, then token; pair numbers index the
+// rows of the hidden activations. Entry 0 of the workspace's list holds how many
+// follow and the tokens whose logits hold a NaN or +inf, one bit each.
+struct Group {
+  unsigned packed;   // expert | count << 9 | first pair << 13
   unsigned lo, hi;
+  __device__ inline int expert() const { return packed & 511; }
+  __device__ inline int count() const { return (packed >> 9) & 15; }
+  __device__ inline int base() const { return packed >> 13; }
 };
+static_assert(kMaxExperts <= 512 && kGroup == 8, "Group's fields");
+__device__ inline Group uniform(const Group &g) {
+  return Group{static_cast<unsigned>(__builtin_amdgcn_readfirstlane(g.packed)),
+               static_cast<unsigned>(__builtin_amdgcn_readfirstlane(g.lo)),
+               static_cast<unsigned>(__builtin_amdgcn_readfirstlane(g.hi))};
+}
 
 struct MoeArgs {
   int tokens, hidden, inter, experts, top_k, renormalize;
@@ -61,16 +74,15 @@ struct MoeArgs {
   void *y;
   int ldy;
   u16 *h;       // workspace: Parts<TYPE>::h planes of (tokens * top_k) x IP bfloat16,
-  Reached *reached;   // and what the second kernel needs of the routing
+  Group *groups;   // and what the second kernel needs of the routing
 };
 
 // What a workgroup knows after routing.
 struct Routing {
-  Reached reached[kMaxExperts];     // reached experts, ascending
+  Group groups[kMaxGroups];         // of the reached experts, ascending
   float weight[kMaxPairs];          // the pair's weight
-  unsigned char token[kMaxPairs];   // the pair's token
   unsigned nan_lo, nan_hi;          // tokens whose logits hold a NaN or +inf
-  int num_reached;
+  int num_groups;
 };
 // What it needs on the way there.
 struct RoutingScratch {
@@ -205,22 +217,33 @@ __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
   }
   __syncthreads();
   if (wave == 0) {
-    int pairs = 0, reached = 0;
+    int pairs = 0, groups = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
       const int e = e0 + lane;
-      const unsigned lo = e < a.experts ? s.lo[e] : 0, hi = e < a.experts ? s.hi[e] : 0;
-      const int c = __popc(lo) + __popc(hi);
-      const int upto = wave_running_sum(c);
-      const unsigned long long who = __ballot(c > 0);
-      const unsigned base = static_cast<unsigned>(pairs + upto - c);
+      unsigned long long m =
+          e < a.experts ? s.lo[e] | (static_cast<unsigned long long>(s.hi[e]) << 32) : 0;
+      const int c = __popcll(m);
+      const int pairs_to = wave_running_sum(c);
+      const int groups_to = wave_running_sum((c + kGroup - 1) / kGroup);
+      int base = pairs + pairs_to - c, at = groups + groups_to - (c + kGroup - 1) / kGroup;
       if (e < a.experts) s.base[e] = static_cast<u16>(base);
-      if (c > 0)
-        r.reached[reached + __popcll(who & ((1ull << lane) - 1))] =
-            Reached{static_cast<unsigned>(e) | (base << 16), lo, hi};
-      pairs += __builtin_amdgcn_readlane(upto, 63);
-      reached += __popcll(who);
+      while (m) {
+        unsigned tokens[2] = {};
+        const int first = __builtin_ctzll(m);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          tokens[i / 4] |= static_cast<unsigned>(m ? __builtin_ctzll(m) : first) << (8 * (i % 4));
+          n += m != 0;
+          m &= m - 1;
+        }
+        r.groups[at++] = Group{static_cast<unsigned>(e | (n << 9) | (base << 13)), tokens[0], tokens[1]};
+        base += n;
+      }
+      pairs += __builtin_amdgcn_readlane(pairs_to, 63);
+      groups += __builtin_amdgcn_readlane(groups_to, 63);
     }
-    if (lane == 0) r.num_reached = reached;
+    if (lane == 0) r.num_groups = groups;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.tokens * kMaxTopK; i += kMoeThreads) {
@@ -229,7 +252,6 @@ __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
       const int t = i / kMaxTopK;
       const unsigned long long m = s.lo[e] | (static_cast<unsigned long long>(s.hi[e]) << 32);
       const int p = s.base[e] + __popcll(m & ((1ull << t) - 1));
-      r.token[p] = static_cast<unsigned char>(t);
       r.weight[p] = s.chosen_weight[i];
     }
   }
@@ -274,51 +296,43 @@ __device__ inline bf16x8 weights8(unsigned codes, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Sums acc over the workgroup's waves through LDS (red: WAVES * TILES * 64), in
-// wave order: afterwards wave w < used holds tile w's sums, the lanes as acc.
-template <int TILES, int WAVES>
-__device__ inline f32x4 reduce_waves(const f32x4 (&acc)[TILES], int used, f32x4 *red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int t = 0; t < TILES; ++t)
-    if (t < used) red[(wave * TILES + t) * 64 + lane] = acc[t];
-  __syncthreads();
-  f32x4 s = {};
-  if (wave < used) {
-    s = red[wave * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += red[(w * TILES + wave) * 64 + lane];
-  }
-  return s;
+// Activations on their way from memory to a matrix instruction. 128 values of up
+// to kGroup tokens are loaded with all lanes busy, lane (s, c) = (lane / 16,
+// lane % 16) taking values 8c .. 8c + 7 of tokens s and 4 + s, and kept in
+// registers until they are needed; then they pass through a piece of LDS of
+// the wave's own, [part][token][16 pieces of 16 bytes], token t's piece c
+// at c ^ t so that the 8 lanes that read one piece of 8 tokens meet no bank
+// twice. Lane (g, n) of an instruction reads pieces 4g .. 4g + 3 of token n.
+constexpr int kStagePart = kGroup * 256;   // bytes
+
+__device__ inline void stage_write(unsigned char *stage, int part, int token, int piece, bf16x8 v) {
+  *reinterpret_cast<bf16x8 *>(stage + part * kStagePart + token * 256 + ((piece ^ token) & 15) * 16) = v;
+}
+__device__ inline bf16x8 stage_read(const unsigned char *stage, int part, int token, int piece) {
+  return *reinterpret_cast<const bf16x8 *>(stage + part * kStagePart + token * 256 +
+                                           ((piece ^ token) & 15) * 16);
+}
+// Order between the lanes of a wave: LDS serves a wave's accesses in order, so
+// only the compiler has to keep them.
+__device__ inline void stage_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// 32 values of x of a lane's token as they are loaded, and their parts.
+// 8 values of x as loaded, `left` of them in range (the rest zeros).
 template <int TYPE>
-struct RawX {
-  uintx4 v[TYPE == kF32 ? 8 : 4];
-  __device__ inline void parts(int j, bf16x8 (&out)[Parts<TYPE>::x]) const {
-    if constexpr (TYPE == kBf16) {
-      out[0] = __builtin_bit_cast(bf16x8, v[j]);
-    } else {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (TYPE == kF32) {
-          const unsigned w = v[2 * j + i / 4][i % 4];   // (the cast of a vector's element itself takes the first)
-          f[i] = __builtin_bit_cast(float, w);
-        } else
-          f[i] = Elem<TYPE>::get(static_cast<u16>(v[j][i / 2] >> (16 * (i % 2))));
-      }
-      split8<Parts<TYPE>::x>(f, out);
-    }
-  }
-  // From p, `left` values in range, the rest zeros.
+struct Raw8 {
+  uintx4 v[TYPE == kF32 ? 2 : 1];
+  // VEC: 16-byte aligned, and all or none of them in range; for none the row's
+  // last 8 are loaded (no branch among the loads), to be cleared before use.
   template <bool VEC>
   __device__ inline void load(const typename Elem<TYPE>::store *p, int left) {
-    constexpr int kEach = TYPE == kF32 ? 4 : 8, kRegs = TYPE == kF32 ? 8 : 4;
-    if (VEC && left >= 32) {
+    constexpr int kRegs = TYPE == kF32 ? 2 : 1, kEach = 8 / kRegs;
+    if constexpr (VEC) {
+      const auto *q = reinterpret_cast<const uintx4 *>(left > 0 ? p : p - (8 - left));
 #pragma unroll
-      for (int r = 0; r < kRegs; ++r) v[r] = reinterpret_cast<const uintx4 *>(p)[r];
+      for (int r = 0; r < kRegs; ++r) v[r] = q[r];
     } else {
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
@@ -335,272 +349,321 @@ struct RawX {
       }
     }
   }
+  __device__ inline void clear() {
+#pragma unroll
+    for (int r = 0; r < (TYPE == kF32 ? 2 : 1); ++r) v[r] = uintx4{};
+  }
+  __device__ inline void parts(bf16x8 (&out)[Parts<TYPE>::x]) const {
+    if constexpr (TYPE == kBf16) {
+      out[0] = __builtin_bit_cast(bf16x8, v[0]);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (TYPE == kF32) {
+          const unsigned w = v[i / 4][i % 4];   // (the cast of a vector's element itself takes the first)
+          f[i] = __builtin_bit_cast(float, w);
+        } else {
+          f[i] = Elem<TYPE>::get(static_cast<u16>(v[0][i / 2] >> (16 * (i % 2))));
+        }
+      }
+      split8<Parts<TYPE>::x>(f, out);
+    }
+  }
 };
 
 // G x, U x and a for the reached experts. An item is 16 of an expert's gate rows
-// and the same up rows; the 8 waves share its K, two chunks of 128 a wave at a
-// time, and the next two's weights (of the next item where this one ends) are
-// on their way meanwhile.
+// and the same up rows for one group of its tokens. The 8 waves share its K, a
+// wave taking two neighbouring chunks of 128 at a time (a whole 128-byte line
+// of a row's codes); the next two's weights and activations (of the next item
+// where this one ends) are on their way meanwhile, in the other of two
+// sets of registers.
 template <int TYPE, bool VEC>
-__global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::x == 1 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
   constexpr int kAt = 2;   // chunks of a wave at a time
   __shared__ Routing r;
   // partial sums of the waves, of two items in turn; scratch of the routing first
-  constexpr int kRed = kMoeWaves * 2 * kUpTiles * 64;
+  constexpr int kRed = kMoeWaves * 2 * 64;
   __shared__ __attribute__((aligned(16))) f32x4 red[2 * kRed];
+  __shared__ __attribute__((aligned(16))) unsigned char stages[kMoeWaves * PX * kStagePart];
   static_assert(sizeof(RoutingScratch) <= sizeof(red), "scratch fits");
   route(a, r, *reinterpret_cast<RoutingScratch *>(red));
-  int half = 0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int num_reached = __builtin_amdgcn_readfirstlane(r.num_reached);
+  const int num_groups = __builtin_amdgcn_readfirstlane(r.num_groups);
   if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) a.reached[0] = Reached{static_cast<unsigned>(num_reached), r.nan_lo, r.nan_hi};
-    for (int n = threadIdx.x; n < num_reached; n += kMoeThreads) a.reached[1 + n] = r.reached[n];
+    if (threadIdx.x == 0) a.groups[0] = Group{static_cast<unsigned>(num_groups), r.nan_lo, r.nan_hi};
+    for (int n = threadIdx.x; n < num_groups; n += kMoeThreads) a.groups[1 + n] = r.groups[n];
   }
+  unsigned char *stage = stages + wave * (PX * kStagePart);
   const int i16 = lane & 15, g = lane >> 4;
   const int HP = (a.hidden + kAlign - 1) / kAlign * kAlign;
   const int IP = (a.inter + kAlign - 1) / kAlign * kAlign;
   const int tiles = IP / 16, chunks = HP / 128;
+  const int batches = (chunks + kAt * kMoeWaves - 1) / (kAt * kMoeWaves);
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
-  const store *x = static_cast<const store *>(a.x);
-  const int items = num_reached * tiles;
+  const int items = num_groups * tiles;
 
-  struct Weights {
+  // What an item's loads need: bases of the expert's rows, the lane's row and
+  // tokens.
+  struct Item {
+    int row0;
+    Group group;
+  };
+  auto item_of = [&](int item) {
+    const int gi = item / tiles;
+    return Item{(item - gi * tiles) * 16, uniform(r.groups[gi])};
+  };
+  struct Fetched {
     uintx4 gate[kAt], up[kAt];
     unsigned gate_scale[kAt], up_scale[kAt];
+    Raw8<TYPE> x[kAt][2];
   };
-  auto load_weights = [&](Weights &w, int item, int c) {
-    if (item >= items) return;
-    const int ai = item / tiles;
-    const int e = r.reached[ai].expert_base & 0xffff;
-    const int row = min((item - ai * tiles) * 16 + i16, a.inter - 1);
-    const long long gate = static_cast<long long>(__builtin_amdgcn_readfirstlane(e)) * 2 * a.inter + row;
-    const long long up = gate + a.inter;
-    const unsigned char *gc = a.w1c + gate * (HP / 2) + g * 16, *gs = a.w1s + gate * (HP / 32) + g;
-    const unsigned char *uc = a.w1c + up * (HP / 2) + g * 16, *us = a.w1s + up * (HP / 32) + g;
+  const long long up_codes = static_cast<long long>(a.inter) * (HP / 2);
+  const long long up_scales = static_cast<long long>(a.inter) * (HP / 32);
+  auto fetch = [&](Fetched &f, const Item &t, int batch) __attribute__((always_inline)) {
+    const int c = (batch * kMoeWaves + wave) * kAt;
+    // rows past the expert's last: the last one again (their results are not kept)
+    const int first = min(t.row0, a.inter - 1), i = min(i16, a.inter - 1 - first);
+    const long long row = static_cast<long long>(t.group.expert()) * 2 * a.inter + first;
+    const unsigned char *codes = a.w1c + row * (HP / 2) + c * 64, *scales = a.w1s + row * (HP / 32) + c * 4;
+    const unsigned code_off = static_cast<unsigned>(i * (HP / 2) + g * 16);
+    const unsigned scale_off = static_cast<unsigned>(i * (HP / 32) + g);
+    const store *x = static_cast<const store *>(a.x) + c * 128 + i16 * 8;
+    const store *x0 = x + static_cast<long long>((t.group.lo >> (8 * g)) & 255) * a.ldx;
+    const store *x1 = x + static_cast<long long>((t.group.hi >> (8 * g)) & 255) * a.ldx;
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-      const int cb = c + b * kMoeWaves;
-      if (cb < chunks) {
-        w.gate[b] = *reinterpret_cast<const uintx4 *>(gc + cb * 64);
-        w.up[b] = *reinterpret_cast<const uintx4 *>(uc + cb * 64);
-        w.gate_scale[b] = gs[cb * 4];
-        w.up_scale[b] = us[cb * 4];
-      }
+      const int past = max(0, c + b - (chunks - 1));   // the last chunk again, not used
+      const unsigned char *pc = codes + (b - past) * 64, *ps = scales + (b - past) * 4;
+      f.gate[b] = *reinterpret_cast<const uintx4 *>(pc + code_off);
+      f.up[b] = *reinterpret_cast<const uintx4 *>(pc + up_codes + code_off);
+      f.gate_scale[b] = ps[scale_off];
+      f.up_scale[b] = (ps + up_scales)[scale_off];
+      const int left = a.hidden - (c + b - past) * 128 - i16 * 8;
+      f.x[b][0].template load<VEC>(x0 + (b - past) * 128, left);
+      f.x[b][1].template load<VEC>(x1 + (b - past) * 128, left);
     }
   };
 
-  Weights cur, next;
-  load_weights(cur, blockIdx.x, wave);
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int ai = item / tiles;
-    const int row0 = (item - ai * tiles) * 16;
-    const Reached now = r.reached[ai];
-    const int base = __builtin_amdgcn_readfirstlane(now.expert_base >> 16);
-    const int count = __builtin_amdgcn_readfirstlane(__popc(now.lo) + __popc(now.hi));
-    for (int first = 0; first < count; first += 16 * kUpTiles) {   // tokens of the expert
-      const int used = min(kUpTiles, (count - first + 15) / 16);
-      const bool last = first + 16 * kUpTiles >= count;
-      f32x4 acc[2 * kUpTiles] = {};   // gate and up of each tile of 16 tokens
-      for (int c = wave; c < chunks || c == wave; c += kAt * kMoeWaves) {
-        const bool more = c + kAt * kMoeWaves < chunks;
-        load_weights(next, more || !last ? item : item + gridDim.x, more ? c + kAt * kMoeWaves : wave);
+  int item = blockIdx.x, batch = 0, turn = 0;
+  if (item >= items) return;
+  Item now = item_of(item), then = now;
+  f32x4 acc_gate = {}, acc_up = {};
+  // One batch of an item from one set of registers, the next one's loads into the
+  // other. Returns whether there is a next one.
+  auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
+    const bool last = batch + 1 == batches;
+    const bool more = !last || item + static_cast<int>(gridDim.x) < items;
+    if (last && more) then = item_of(item + gridDim.x);
+    if (more) fetch(next, then, last ? 0 : batch + 1);
+    const int c = (batch * kMoeWaves + wave) * kAt;
 #pragma unroll
-        for (int t = 0; t < kUpTiles; ++t) {
-          if (t < used) {
-            const int n = first + t * 16 + i16;
-            const store *px = x + static_cast<long long>(n < count ? r.token[base + n] : 0) * a.ldx + g * 32;
+    for (int b = 0; b < kAt; ++b) {
+      if (c + b < chunks) {
+        stage_order();
+        Raw8<TYPE> first = cur.x[b][0], second = cur.x[b][1];
+        if (VEC && (c + b) * 128 + 128 > a.hidden && (c + b) * 128 + i16 * 8 >= a.hidden) {
+          first.clear();
+          second.clear();
+        }
+        bf16x8 parts[PX];
+        first.parts(parts);
 #pragma unroll
-            for (int b = 0; b < kAt; ++b) {
-              const int k = (c + b * kMoeWaves) * 128;
-              if (k < HP) {
-                RawX<TYPE> raw = {};
-                if (n < count) {
-                  if (VEC && k + 128 <= a.hidden)
-                    raw.template load<true>(px + k, 32);
-                  else
-                    raw.template load<false>(px + k, a.hidden - k - g * 32);
-                }
-                const float fg = scale_value(cur.gate_scale[b]), fu = scale_value(cur.up_scale[b]);
+        for (int p = 0; p < PX; ++p) stage_write(stage, p, g, i16, parts[p]);
+        second.parts(parts);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  bf16x8 xv[PX];
-                  raw.parts(j, xv);
-                  const bf16x8 vg = weights8(cur.gate[b][j], fg), vu = weights8(cur.up[b][j], fu);
+        for (int p = 0; p < PX; ++p) stage_write(stage, p, 4 + g, i16, parts[p]);
+        stage_order();
+        const float fg = scale_value(cur.gate_scale[b]), fu = scale_value(cur.up_scale[b]);
 #pragma unroll
-                  for (int p = 0; p < PX; ++p) {
-                    acc[2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, xv[p], acc[2 * t], 0, 0, 0);
-                    acc[2 * t + 1] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, xv[p], acc[2 * t + 1], 0, 0, 0);
-                  }
-                }
-              }
-            }
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 vg = weights8(cur.gate[b][j], fg), vu = weights8(cur.up[b][j], fu);
+#pragma unroll
+          for (int p = 0; p < PX; ++p) {
+            const bf16x8 xv = stage_read(stage, p, i16 & (kGroup - 1), 4 * g + j);
+            acc_gate = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, xv, acc_gate, 0, 0, 0);
+            acc_up = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, xv, acc_up, 0, 0, 0);
           }
         }
-        cur = next;
-      }
-      // One barrier an item: the next one's sums go to the other half, and nobody
-      // writes this half again before having passed the next barrier.
-      f32x4 *mine = red + half * kRed;
-      half ^= 1;
-#pragma unroll
-      for (int t = 0; t < 2 * kUpTiles; ++t)
-        if (t < 2 * used) mine[(wave * 2 * kUpTiles + t) * 64 + lane] = acc[t];
-      __syncthreads();
-      if (wave < used) {
-        f32x4 gv = mine[(2 * wave) * 64 + lane], uv = mine[(2 * wave + 1) * 64 + lane];
-#pragma unroll
-        for (int w = 1; w < kMoeWaves; ++w) {
-          gv += mine[(w * 2 * kUpTiles + 2 * wave) * 64 + lane];
-          uv += mine[(w * 2 * kUpTiles + 2 * wave + 1) * 64 + lane];
-        }
-        const int n = first + wave * 16 + i16;
-        if (n < count) {
-          const int p = base + n;
-          const float w = r.weight[p];
-          const int row = row0 + 4 * g;
-          u16 parts[PH][4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            // past the last row of an expert: the zeros that pad `inter`
-            float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
-#pragma unroll
-            for (int q = 0; q < PH; ++q) {
-              const unsigned b = __builtin_bit_cast(unsigned, rest);
-              parts[q][v] = q + 1 < PH || PH == 3 ? static_cast<u16>(b >> 16) : Elem<kBf16>::put(rest);
-              rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(parts[q][v]);
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < PH; ++q)
-            *reinterpret_cast<uintx2 *>(a.h + q * plane + static_cast<long long>(p) * IP + row) =
-                uintx2{parts[q][0] | (static_cast<unsigned>(parts[q][1]) << 16),
-                       parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
-        }
+        __builtin_amdgcn_sched_barrier(0);   // one chunk's registers at a time
       }
     }
+    if (!last) {
+      ++batch;
+      return true;
+    }
+    // One barrier an item: the next one's sums go to the other half, and nobody
+    // writes this half again before having passed the next barrier.
+    f32x4 *sums = red + (turn & 1) * kRed;
+    sums[wave * 128 + lane] = acc_gate;
+    sums[wave * 128 + 64 + lane] = acc_up;
+    __syncthreads();
+    if (wave == (turn & (kMoeWaves - 1))) {
+      f32x4 gv = sums[lane], uv = sums[64 + lane];
+#pragma unroll
+      for (int w = 1; w < kMoeWaves; ++w) {
+        gv += sums[w * 128 + lane];
+        uv += sums[w * 128 + 64 + lane];
+      }
+      if (i16 < now.group.count()) {
+        const int p = now.group.base() + i16;
+        const float w = r.weight[p];
+        const int row = now.row0 + 4 * g;
+        u16 parts[PH][4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          // past the last row of an expert: the zeros that pad `inter`
+          float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
+#pragma unroll
+          for (int q = 0; q < PH; ++q) {
+            const unsigned bits = __builtin_bit_cast(unsigned, rest);
+            parts[q][v] = q + 1 < PH || PH == 3 ? static_cast<u16>(bits >> 16) : Elem<kBf16>::put(rest);
+            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(parts[q][v]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < PH; ++q)
+          *reinterpret_cast<uintx2 *>(a.h + q * plane + static_cast<long long>(p) * IP + row) =
+              uintx2{parts[q][0] | (static_cast<unsigned>(parts[q][1]) << 16),
+                     parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
+      }
+    }
+    acc_gate = f32x4{};
+    acc_up = f32x4{};
+    item += gridDim.x;
+    batch = 0;
+    ++turn;
+    now = then;
+    return more;
+  };
+  Fetched even, odd;
+  fetch(even, now, 0);
+  while (step(even, odd) && step(odd, even)) {
   }
 }
 
-// Y: a workgroup takes 16 rows of every reached expert's D, its waves the
-// (expert, chunk of 128) steps in turn, two a wave at a time, the next two's
-// weights on their way.
+// Y: a workgroup takes 16 rows of every reached expert's D. Its waves take the
+// steps (group of tokens, two neighbouring chunks of 128) in turn, the next
+// step's weights and activations on their way. An instruction's columns are the
+// group's tokens, so a step's sums are then added to the wave's own sums of
+// those tokens, in LDS; at the end the waves' sums are added in order.
 template <int TYPE>
-__global__ __launch_bounds__(kDownThreads, 4) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per_simd) void moe_down_kernel(
+    MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
-  constexpr int PH = Parts<TYPE>::h;
+  constexpr int PH = Parts<TYPE>::h, W = Parts<TYPE>::down_waves, THREADS = 64 * W;
   constexpr int kAt = 2;
-  __shared__ Reached reached[kMaxExperts + 1];
-  __shared__ __attribute__((aligned(16))) f32x4 red[kDownWaves * kTokenTiles * 64];
-  const int most = min(a.experts, a.tokens * a.top_k) + 1;
-  for (int n = threadIdx.x; n < most; n += kDownThreads) reached[n] = a.reached[n];
-  __syncthreads();
-  const int num_reached = __builtin_amdgcn_readfirstlane(reached[0].expert_base);
+  __shared__ Group groups[kMaxGroups + 1];
+  __shared__ __attribute__((aligned(16))) unsigned char stages[W * PH * kStagePart];
+  __shared__ __attribute__((aligned(16))) float sums[W * kMaxTokens * 16];   // [wave][token][row]
+  const int most = min(a.experts, a.tokens * a.top_k) + a.tokens * a.top_k / kGroup + 1;
+  for (int n = threadIdx.x; n < most; n += THREADS) groups[n] = a.groups[n];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
+  unsigned char *stage = stages + wave * (PH * kStagePart);
+  float *mine = sums + wave * (kMaxTokens * 16);
+  for (int n = lane; n < a.tokens * 4; n += 64) reinterpret_cast<f32x4 *>(mine)[n] = f32x4{};
+  __syncthreads();
+  const int num_groups = __builtin_amdgcn_readfirstlane(groups[0].packed);
   const int IP = (a.inter + kAlign - 1) / kAlign * kAlign;
-  const int chunks = IP / 128;
+  const int chunks = IP / 128, batches = (chunks + kAt - 1) / kAt;
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
   const int row0 = blockIdx.x * 16;
-  const int row = min(row0 + i16, a.hidden - 1);
-  const int token_tiles = (a.tokens + 15) / 16;
+  const int row = min(i16, a.hidden - 1 - row0);
+  const unsigned code_off = static_cast<unsigned>(row * (IP / 2) + g * 16);
+  const unsigned scale_off = static_cast<unsigned>(row * (IP / 32) + g);
+  const unsigned h_off = static_cast<unsigned>(g * IP), h4_off = static_cast<unsigned>((4 + g) * IP);
 
-  // A step: reached expert `at` (num_reached: none left) and chunk c.
-  struct Step {
-    int at, c;
-  };
-  auto advance = [&](Step s) {
-    s.c += kDownWaves;
-    while (s.c >= chunks && s.at < num_reached) {
-      s.c -= chunks;
-      ++s.at;
-    }
-    return s;
-  };
-  struct Weights {
+  struct Fetched {
     uintx4 w[kAt];
     unsigned scale[kAt];
+    uintx4 h[kAt][PH][2];
   };
-  auto load_weights = [&](Weights &w, const Step (&s)[kAt]) {
+  auto fetch = [&](Fetched &f, const Group &now, int batch) __attribute__((always_inline)) {
+    const long long wr = static_cast<long long>(now.expert()) * a.hidden + row0;
+    const unsigned char *codes = a.w2c + wr * (IP / 2), *scales = a.w2s + wr * (IP / 32);
+    const u16 *h = a.h + static_cast<long long>(now.base()) * IP + i16 * 8;
+    const unsigned last = static_cast<unsigned>((now.count() - 1) * IP);
+    const unsigned h0 = min(h_off, last), h1 = min(h4_off, last);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-      if (s[b].at < num_reached) {
-        const int e = __builtin_amdgcn_readfirstlane(reached[1 + s[b].at].expert_base & 0xffff);
-        const long long wr = static_cast<long long>(e) * a.hidden + row;
-        w.w[b] = *reinterpret_cast<const uintx4 *>(a.w2c + wr * (IP / 2) + s[b].c * 64 + g * 16);
-        w.scale[b] = a.w2s[wr * (IP / 32) + s[b].c * 4 + g];
+      const int c = min(batch * kAt + b, chunks - 1);   // past the end: not used
+      f.w[b] = *reinterpret_cast<const uintx4 *>(codes + c * 64 + code_off);
+      f.scale[b] = (scales + c * 4)[scale_off];
+#pragma unroll
+      for (int q = 0; q < PH; ++q) {
+        f.h[b][q][0] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h0);
+        f.h[b][q][1] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h1);
       }
     }
   };
-  f32x4 acc[kTokenTiles] = {};
-  Step step[kAt];
-  step[0] = advance(Step{0, wave - kDownWaves});
-#pragma unroll
-  for (int b = 1; b < kAt; ++b) step[b] = advance(step[b - 1]);
-  Weights cur, next;
-  load_weights(cur, step);
-  while (step[0].at < num_reached) {
-    Step then[kAt];
-    then[0] = advance(step[kAt - 1]);
-#pragma unroll
-    for (int b = 1; b < kAt; ++b) then[b] = advance(then[b - 1]);
-    load_weights(next, then);
+  int at = 0, batch = wave;   // the step: group and batch
+  auto wrap = [&](int &to, int &bt) {
+    while (bt >= batches && to < num_groups) {
+      bt -= batches;
+      ++to;
+    }
+  };
+  wrap(at, batch);
+  Group now = uniform(groups[1 + min(at, kMaxGroups - 1)]);
+  auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
+    int next_at = at, next_batch = batch + W;
+    wrap(next_at, next_batch);
+    const bool more = next_at < num_groups;
+    const Group then = uniform(groups[1 + min(next_at, kMaxGroups - 1)]);
+    if (more) fetch(next, then, next_batch);
+    f32x4 acc = {};
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-      if (step[b].at >= num_reached) continue;
-      const Reached now = reached[1 + step[b].at];
-      const unsigned long long m =
-          static_cast<unsigned>(__builtin_amdgcn_readfirstlane(now.lo)) |
-          (static_cast<unsigned long long>(static_cast<unsigned>(__builtin_amdgcn_readfirstlane(now.hi))) << 32);
-      const float f = scale_value(cur.scale[b]);
+      if (batch * kAt + b < chunks) {
+        stage_order();
 #pragma unroll
-      for (int t = 0; t < kTokenTiles; ++t) {
-        if (t < token_tiles && ((m >> (16 * t)) & 0xffffull)) {
-          const int n = t * 16 + i16;
-          const bool has = (m >> n) & 1;
-          bf16x8 hv[PH][4] = {};
-          if (has) {
-            const int p = (now.expert_base >> 16) + __popcll(m & ((1ull << n) - 1));
-            const u16 *h = a.h + static_cast<long long>(p) * IP + step[b].c * 128 + g * 32;
+        for (int q = 0; q < PH; ++q) {
+          const uintx4 h0 = cur.h[b][q][0], h1 = cur.h[b][q][1];
+          stage_write(stage, q, g, i16, __builtin_bit_cast(bf16x8, h0));
+          stage_write(stage, q, 4 + g, i16, __builtin_bit_cast(bf16x8, h1));
+        }
+        stage_order();
+        const float f = scale_value(cur.scale[b]);
 #pragma unroll
-            for (int q = 0; q < PH; ++q)
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 v = weights8(cur.w[b][j], f);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                hv[q][j] = *reinterpret_cast<const bf16x8 *>(h + q * plane + j * 8);
-          }
-          f32x4 sum = acc[t];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bf16x8 v = weights8(cur.w[b][j], f);
-#pragma unroll
-            for (int q = 0; q < PH; ++q)
-              sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, hv[q][j], sum, 0, 0, 0);
-          }
-          // A token that did not choose this expert keeps its sum, also where the
-          // expert's weights hold a NaN (0 * NaN is not 0).
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[t][v] = has ? sum[v] : acc[t][v];
+          for (int q = 0; q < PH; ++q)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                v, stage_read(stage, q, i16 & (kGroup - 1), 4 * g + j), acc, 0, 0, 0);
         }
       }
     }
-#pragma unroll
-    for (int b = 0; b < kAt; ++b) step[b] = then[b];
-    cur = next;
+    if (i16 < now.count()) {
+      const unsigned t = ((i16 < 4 ? now.lo : now.hi) >> (8 * (i16 & 3))) & 255;
+      *reinterpret_cast<f32x4 *>(mine + t * 16 + g * 4) += acc;
+    }
+    at = next_at;
+    batch = next_batch;
+    now = then;
+    return more;
+  };
+  if (at < num_groups) {
+    Fetched even, odd;
+    fetch(even, now, batch);
+    while (step(even, odd) && step(odd, even)) {
+    }
   }
-  const f32x4 sum = reduce_waves<kTokenTiles, kDownWaves>(acc, token_tiles, red);
-  const int t = wave * 16 + i16;
-  if (wave < token_tiles && t < a.tokens) {
-    const bool nan = ((t < 32 ? reached[0].lo : reached[0].hi) >> (t & 31)) & 1;
-    store *y = static_cast<store *>(a.y) + static_cast<long long>(t) * a.ldy + row0 + 4 * g;
+  __syncthreads();
+  for (int n = threadIdx.x; n < a.tokens * 16; n += THREADS) {
+    const int t = n >> 4, i = n & 15;
+    float s = sums[n];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (row0 + 4 * g + v < a.hidden)
-        y[v] = Elem<TYPE>::put(nan ? __builtin_nanf("") : sum[v]);
+    for (int w = 1; w < W; ++w) s += sums[w * (kMaxTokens * 16) + n];
+    const bool nan = ((t < 32 ? groups[0].lo : groups[0].hi) >> (t & 31)) & 1;
+    if (row0 + i < a.hidden)
+      static_cast<store *>(a.y)[static_cast<long long>(t) * a.ldy + row0 + i] =
+          Elem<TYPE>::put(nan ? __builtin_nanf("") : s);
   }
 }
 
