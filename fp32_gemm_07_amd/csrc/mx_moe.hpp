@@ -320,6 +320,25 @@ __device__ inline void stage_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Waits for a load's registers here, on every path: where a branch that uses
+// them is not taken the compiler would otherwise have to wait for all loads
+// before it gives the registers to something else.
+template <class V>
+__device__ inline void arrived(const V &v) {
+  asm volatile("" : : "v"(v));
+}
+
+// step(cur, next) `n` times, the two sets of registers in turn. No exit in the middle
+// of the loop: loads still on their way there would be waited for at its top.
+template <class F, class S>
+__device__ inline void in_turn(int n, F &even, F &odd, S &&step) {
+  for (; n > 1; n -= 2) {
+    step(even, odd);
+    step(odd, even);
+  }
+  if (n) step(even, odd);
+}
+
 // 8 values of x as loaded, `left` of them in range (the rest zeros).
 template <int TYPE>
 struct Raw8 {
@@ -405,6 +424,7 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
   const int batches = (chunks + kAt * kMoeWaves - 1) / (kAt * kMoeWaves);
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
   const int items = num_groups * tiles;
+  const int stride = __builtin_amdgcn_readfirstlane(gridDim.x);
 
   // What an item's loads need: bases of the expert's rows, the lane's row and
   // tokens.
@@ -423,14 +443,14 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
   };
   const long long up_codes = static_cast<long long>(a.inter) * (HP / 2);
   const long long up_scales = static_cast<long long>(a.inter) * (HP / 32);
-  auto fetch = [&](Fetched &f, const Item &t, int batch) __attribute__((always_inline)) {
+  auto fetch = [&](Fetched &f, const Item &t, int batch, bool wanted) __attribute__((always_inline)) {
     const int c = (batch * kMoeWaves + wave) * kAt;
     // rows past the expert's last: the last one again (their results are not kept)
     const int first = min(t.row0, a.inter - 1), i = min(i16, a.inter - 1 - first);
     const long long row = static_cast<long long>(t.group.expert()) * 2 * a.inter + first;
     const unsigned char *codes = a.w1c + row * (HP / 2) + c * 64, *scales = a.w1s + row * (HP / 32) + c * 4;
-    const unsigned code_off = static_cast<unsigned>(i * (HP / 2) + g * 16);
-    const unsigned scale_off = static_cast<unsigned>(i * (HP / 32) + g);
+    const unsigned code_off = wanted ? static_cast<unsigned>(i * (HP / 2) + g * 16) : 0;
+    const unsigned scale_off = wanted ? static_cast<unsigned>(i * (HP / 32) + g) : 0;
     const store *x = static_cast<const store *>(a.x) + c * 128 + i16 * 8;
     const store *x0 = x + static_cast<long long>((t.group.lo >> (8 * g)) & 255) * a.ldx;
     const store *x1 = x + static_cast<long long>((t.group.hi >> (8 * g)) & 255) * a.ldx;
@@ -450,18 +470,30 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
 
   int item = blockIdx.x, batch = 0, turn = 0;
   if (item >= items) return;
-  Item now = item_of(item), then = now;
+  Item now = item_of(item);
   f32x4 acc_gate = {}, acc_up = {};
   // One batch of an item from one set of registers, the next one's loads into the
-  // other. Returns whether there is a next one.
+  // other.
   auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
     const bool last = batch + 1 == batches;
-    const bool more = !last || item + static_cast<int>(gridDim.x) < items;
-    if (last && more) then = item_of(item + gridDim.x);
-    if (more) fetch(next, then, last ? 0 : batch + 1);
+    const bool more = !last || item + stride < items;
+    const Item then = item_of(last && more ? item + stride : item);
+    // Also after the last one (then all lanes load the same bytes): a branch
+    // around the loads would make the compiler wait for them at its end.
+    fetch(next, then, last ? 0 : batch + 1, more);
+    __builtin_amdgcn_sched_barrier(0);
     const int c = (batch * kMoeWaves + wave) * kAt;
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
+#pragma unroll
+      for (int r = 0; r < (TYPE == kF32 ? 2 : 1); ++r) {
+        arrived(cur.x[b][0].v[r]);
+        arrived(cur.x[b][1].v[r]);
+      }
+      arrived(cur.gate[b]);
+      arrived(cur.up[b]);
+      arrived(cur.gate_scale[b]);
+      arrived(cur.up_scale[b]);
       if (c + b < chunks) {
         stage_order();
         Raw8<TYPE> first = cur.x[b][0], second = cur.x[b][1];
@@ -493,7 +525,7 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
     }
     if (!last) {
       ++batch;
-      return true;
+      return;
     }
     // One barrier an item: the next one's sums go to the other half, and nobody
     // writes this half again before having passed the next barrier.
@@ -533,16 +565,14 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
     }
     acc_gate = f32x4{};
     acc_up = f32x4{};
-    item += gridDim.x;
+    item += stride;
     batch = 0;
     ++turn;
     now = then;
-    return more;
   };
   Fetched even, odd;
-  fetch(even, now, 0);
-  while (step(even, odd) && step(odd, even)) {
-  }
+  fetch(even, now, 0, true);
+  in_turn((items - item + stride - 1) / stride * batches, even, odd, step);
 }
 
 // Y: a workgroup takes 16 rows of every reached expert's D. Its waves take the
@@ -583,7 +613,7 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
     unsigned scale[kAt];
     uintx4 h[kAt][PH][2];
   };
-  auto fetch = [&](Fetched &f, const Group &now, int batch) __attribute__((always_inline)) {
+  auto fetch = [&](Fetched &f, const Group &now, int batch, bool wanted) __attribute__((always_inline)) {
     const long long wr = static_cast<long long>(now.expert()) * a.hidden + row0;
     const unsigned char *codes = a.w2c + wr * (IP / 2), *scales = a.w2s + wr * (IP / 32);
     const u16 *h = a.h + static_cast<long long>(now.base()) * IP + i16 * 8;
@@ -592,8 +622,8 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       const int c = min(batch * kAt + b, chunks - 1);   // past the end: not used
-      f.w[b] = *reinterpret_cast<const uintx4 *>(codes + c * 64 + code_off);
-      f.scale[b] = (scales + c * 4)[scale_off];
+      f.w[b] = *reinterpret_cast<const uintx4 *>(codes + c * 64 + (wanted ? code_off : 0));
+      f.scale[b] = (scales + c * 4)[wanted ? scale_off : 0];
 #pragma unroll
       for (int q = 0; q < PH; ++q) {
         f.h[b][q][0] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h0);
@@ -614,11 +644,19 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
     int next_at = at, next_batch = batch + W;
     wrap(next_at, next_batch);
     const bool more = next_at < num_groups;
-    const Group then = uniform(groups[1 + min(next_at, kMaxGroups - 1)]);
-    if (more) fetch(next, then, next_batch);
+    const Group then = uniform(groups[1 + (more ? next_at : at)]);
+    fetch(next, then, more ? next_batch : batch, more);
+    __builtin_amdgcn_sched_barrier(0);
     f32x4 acc = {};
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
+#pragma unroll
+      for (int q = 0; q < PH; ++q) {
+        arrived(cur.h[b][q][0]);
+        arrived(cur.h[b][q][1]);
+      }
+      arrived(cur.w[b]);
+      arrived(cur.scale[b]);
       if (batch * kAt + b < chunks) {
         stage_order();
 #pragma unroll
@@ -646,13 +684,11 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
     at = next_at;
     batch = next_batch;
     now = then;
-    return more;
   };
   if (at < num_groups) {
     Fetched even, odd;
-    fetch(even, now, batch);
-    while (step(even, odd) && step(odd, even)) {
-    }
+    fetch(even, now, batch, true);
+    in_turn((num_groups * batches - wave + W - 1) / W, even, odd, step);
   }
   __syncthreads();
   for (int n = threadIdx.x; n < a.tokens * 16; n += THREADS) {
