@@ -250,27 +250,40 @@ size_t moe_workspace(int tokens, int inter, int top_k, int type) {
   return hidden + kGroupBytes;
 }
 
-int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
-  const bool vec = a.hidden % 8 == 0 && aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(type)) % 16 == 0;
+// Both kernels for groups of GROUP tokens.
+template <int TYPE, int GROUP>
+int launch_moe_groups(const MoeArgs &a, int cus, hipStream_t stream) {
+  // 16-byte loads of x: whole rows of 8 values
+  const bool vec = a.hidden % 8 == 0 && aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(TYPE)) % 16 == 0;
+  const bool resident = static_cast<long long>(padded(a.hidden)) / 128 * Parts<TYPE>::x * GROUP * 256 <= kUpStage<GROUP>;
   const long long pairs = static_cast<long long>(a.tokens) * a.top_k;
-  const long long groups = std::min<long long>(pairs, a.experts) + pairs / kGroup;
-  const unsigned up = static_cast<unsigned>(
-      std::min<long long>(groups * (padded(a.inter) / 16), 2LL * cus));
-  const unsigned down = static_cast<unsigned>(ceil_div(a.hidden, 16));
-  with_type(type, [&](auto t) {
-    constexpr int T = decltype(t)::value;
-    if (vec)
-      hipLaunchKernelGGL((moe_up_kernel<T, true>), dim3(up), dim3(kMoeThreads), 0, stream, a);
-    else
-      hipLaunchKernelGGL((moe_up_kernel<T, false>), dim3(up), dim3(kMoeThreads), 0, stream, a);
-  });
+  const long long groups = std::min<long long>(pairs, a.experts) + pairs / GROUP;
+  const dim3 up(static_cast<unsigned>(std::min<long long>(groups * (padded(a.inter) / 16), cus)));
+  const dim3 down(static_cast<unsigned>(ceil_div(a.hidden, 16)));
+  if (vec && resident)
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, true, GROUP, true>), up, dim3(kMoeThreads), 0, stream, a);
+  else if (vec)
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, true, GROUP, false>), up, dim3(kMoeThreads), 0, stream, a);
+  else if (resident)
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, false, GROUP, true>), up, dim3(kMoeThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, false, GROUP, false>), up, dim3(kMoeThreads), 0, stream, a);
   const int st = launched();
   if (st != GEMM_OK) return st;
+  hipLaunchKernelGGL((moe_down_kernel<TYPE, GROUP>), down, dim3(64 * Parts<TYPE>::down_waves), 0, stream, a);
+  return launched();
+}
+
+int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
+  int st = GEMM_OK;
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    hipLaunchKernelGGL(moe_down_kernel<T>, dim3(down), dim3(64 * Parts<T>::down_waves), 0, stream, a);
+    // Groups of 8 where an expert has more than 4 tokens on average (its weights are
+    // read once for 8 of them), else of 4 (fewer activations to move).
+    const bool eight = T == kBf16 && static_cast<long long>(a.tokens) * a.top_k > 4LL * a.experts;
+    st = eight ? launch_moe_groups<T, T == kBf16 ? 8 : 4>(a, cus, stream) : launch_moe_groups<T, 4>(a, cus, stream);
   });
-  return launched();
+  return st;
 }
 
 int check_moe(const MoeArgs &a, int type) {

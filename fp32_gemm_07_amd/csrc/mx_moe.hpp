@@ -28,24 +28,22 @@
 namespace gemm {
 namespace mx {
 
-constexpr int kMoeWaves = 8;   // of the first kernel
+constexpr int kMoeWaves = 16;   // of the first kernel: one workgroup a CU
 constexpr int kMoeThreads = 64 * kMoeWaves;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;   // GEMM_MX_MOE_MAX_*
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
-constexpr int kGroup = 8;   // tokens of an expert taken at a time
-constexpr int kMaxGroups = kMaxExperts + kMaxPairs / kGroup;
+// An expert's tokens are taken in groups of GROUP = 4 or 8.
+constexpr int kMaxGroups = kMaxExperts + kMaxPairs / 4;
 
 template <int TYPE>
 struct Parts {
   static constexpr int x = TYPE == kF32 ? 3 : TYPE == kF16 ? 2 : 1;   // of the inputs
   static constexpr int h = TYPE == kF32 ? 3 : 2;                      // of the hidden activations
-  // waves of the second kernel, and the waves a SIMD that both are built for, by
-  // the registers that the parts in flight take
+  // waves of the second kernel, by the registers that the parts in flight take
   static constexpr int down_waves = TYPE == kF32 ? 8 : 16;
-  static constexpr int up_per_simd = TYPE == kBf16 ? 4 : 2, down_per_simd = TYPE == kF32 ? 2 : 4;
 };
 
-// Up to kGroup tokens of one expert: the expert, how many tokens, their first
+// Up to GROUP tokens of one expert: the expert, how many tokens, their first
 // pair and the tokens (a byte each, the first one again where there are fewer).
 // Pairs (token, expert) are numbered by expert, then token; pair numbers index the
 // rows of the hidden activations. Entry 0 of the workspace's list holds how many
@@ -57,7 +55,7 @@ struct Group {
   __device__ inline int count() const { return (packed >> 9) & 15; }
   __device__ inline int base() const { return packed >> 13; }
 };
-static_assert(kMaxExperts <= 512 && kGroup == 8, "Group's fields");
+static_assert(kMaxExperts <= 512, "Group's fields");
 __device__ inline Group uniform(const Group &g) {
   return Group{static_cast<unsigned>(__builtin_amdgcn_readfirstlane(g.packed)),
                static_cast<unsigned>(__builtin_amdgcn_readfirstlane(g.lo)),
@@ -138,25 +136,24 @@ __device__ inline void choose(const MoeArgs &a, int t, Routing &r, RoutingScratc
   const float *l = a.logits + static_cast<long long>(ok ? t : 0) * a.ld_logits;
   float val[PER];
   unsigned key[PER];
-  bool bad = false;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = j * 16 + l16;
     val[j] = ok && e < a.experts ? l[e] + 0.0f : -__builtin_inff();   // -0 equals +0
   }
-  unsigned best = 0;
+  unsigned best = 0, largest = 0;   // largest: of the magnitudes, -inf left out
   int at = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const unsigned b = __builtin_bit_cast(unsigned, val[j]);
-    if (magnitude_bits(val[j]) > 0x7f800000u || b == 0x7f800000u) bad = true;
+    largest = max(largest, b == 0xff800000u ? 0u : magnitude_bits(val[j]));
     key[j] = b == 0xff800000u ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
     if (key[j] > best) {
       best = key[j];
       at = j;
     }
   }
-  bad = row_max(bad) != 0;
+  const bool bad = row_max(largest) >= 0x7f800000u;   // a NaN or +inf
   float top = 0.0f, mine = -__builtin_inff();
   int my_expert = 0xffff;
   for (int n = 0; n < a.top_k; ++n) {
@@ -202,6 +199,7 @@ __device__ inline void choose(const MoeArgs &a, int t, Routing &r, RoutingScratc
 }
 
 // Routes all tokens; ends with a barrier.
+template <int GROUP>
 __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,15 +222,15 @@ __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
           e < a.experts ? s.lo[e] | (static_cast<unsigned long long>(s.hi[e]) << 32) : 0;
       const int c = __popcll(m);
       const int pairs_to = wave_running_sum(c);
-      const int groups_to = wave_running_sum((c + kGroup - 1) / kGroup);
-      int base = pairs + pairs_to - c, at = groups + groups_to - (c + kGroup - 1) / kGroup;
+      const int groups_to = wave_running_sum((c + GROUP - 1) / GROUP);
+      int base = pairs + pairs_to - c, at = groups + groups_to - (c + GROUP - 1) / GROUP;
       if (e < a.experts) s.base[e] = static_cast<u16>(base);
       while (m) {
         unsigned tokens[2] = {};
         const int first = __builtin_ctzll(m);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
+        for (int i = 0; i < GROUP; ++i) {
           tokens[i / 4] |= static_cast<unsigned>(m ? __builtin_ctzll(m) : first) << (8 * (i % 4));
           n += m != 0;
           m &= m - 1;
@@ -297,19 +295,18 @@ __device__ inline bf16x8 weights8(unsigned codes, float scale) {
 }
 
 // Activations on their way from memory to a matrix instruction. 128 values of up
-// to kGroup tokens are loaded with all lanes busy, lane (s, c) = (lane / 16,
-// lane % 16) taking values 8c .. 8c + 7 of tokens s and 4 + s, and kept in
-// registers until they are needed; then they pass through a piece of LDS of
-// the wave's own, [part][token][16 pieces of 16 bytes], token t's piece c
-// at c ^ t so that the 8 lanes that read one piece of 8 tokens meet no bank
-// twice. Lane (g, n) of an instruction reads pieces 4g .. 4g + 3 of token n.
-constexpr int kStagePart = kGroup * 256;   // bytes
-
+// to GROUP tokens are loaded with all lanes busy, lane (s, c) = (lane / 16,
+// lane % 16) taking values 8c .. 8c + 7 of token s (and of token 4 + s), and pass
+// through LDS, [part][token][16 pieces of 16 bytes], token t's piece c at c ^ t
+// so that the 8 lanes that read one piece of 8 tokens meet no bank twice.
+// Lane (g, n) of an instruction reads pieces 4g .. 4g + 3 of token n % GROUP.
+template <int GROUP>
 __device__ inline void stage_write(unsigned char *stage, int part, int token, int piece, bf16x8 v) {
-  *reinterpret_cast<bf16x8 *>(stage + part * kStagePart + token * 256 + ((piece ^ token) & 15) * 16) = v;
+  *reinterpret_cast<bf16x8 *>(stage + (part * GROUP + token) * 256 + ((piece ^ token) & 15) * 16) = v;
 }
+template <int GROUP>
 __device__ inline bf16x8 stage_read(const unsigned char *stage, int part, int token, int piece) {
-  return *reinterpret_cast<const bf16x8 *>(stage + part * kStagePart + token * 256 +
+  return *reinterpret_cast<const bf16x8 *>(stage + (part * GROUP + token) * 256 +
                                            ((piece ^ token) & 15) * 16);
 }
 // Order between the lanes of a wave: LDS serves a wave's accesses in order, so
@@ -318,6 +315,20 @@ __device__ inline void stage_order() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Loads through a buffer resource: a uniform base and the bytes behind it (dwords
+// past them read as zero), a lane's offset and a uniform one.
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const unsigned char *base, long long bytes) {
+  const long long most = 0x7fffffff;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(base), 0,
+                                           static_cast<int>(bytes < most ? bytes : most), 0x00020000);
+}
+__device__ inline uintx4 load16(__amdgpu_buffer_rsrc_t r, unsigned lane_off, int off) {
+  return __builtin_bit_cast(uintx4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
+}
+__device__ inline uintx2 load8(__amdgpu_buffer_rsrc_t r, unsigned lane_off, int off) {
+  return __builtin_bit_cast(uintx2, __builtin_amdgcn_raw_buffer_load_b64(r, lane_off, off, 0));
 }
 
 // Waits for a load's registers here, on every path: where a branch that uses
@@ -391,24 +402,39 @@ struct Raw8 {
   }
 };
 
+// The scale of chunk b (0 or 1) of two chunks' 4 scale bytes each, for lane group g.
+__device__ inline float pair_scale(const uintx2 &s, int b, int g) {
+  const unsigned w = b ? s[1] : s[0];
+  return scale_value((w >> (8 * g)) & 255);
+}
+
 // G x, U x and a for the reached experts. An item is 16 of an expert's gate rows
-// and the same up rows for one group of its tokens. The 8 waves share its K, a
-// wave taking two neighbouring chunks of 128 at a time (a whole 128-byte line
-// of a row's codes); the next two's weights and activations (of the next item
-// where this one ends) are on their way meanwhile, in the other of two
-// sets of registers.
-template <int TYPE, bool VEC>
-__global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_kernel(MoeArgs a) {
+// and the same up rows for one group of its tokens; a workgroup takes a run of
+// items, mostly of one group, whose activations it keeps in LDS (RESIDENT; where
+// all of `hidden` does not fit they are loaded again for every item). The 16
+// waves share an item's K, a wave taking two neighbouring chunks of 128 at a
+// time (a whole 128-byte line of a row's codes); the next two's weights (of the
+// next item where this one ends) are on their way meanwhile, in the other of
+// two sets of registers.
+constexpr int kUpLds = 160 * 1024;
+template <int GROUP>
+constexpr int kUpRed = 2 * kMoeWaves * 2 * 4 * GROUP * 16;   // partial sums, of two items in turn
+// what is left for the activations
+template <int GROUP>
+constexpr int kUpStage = (kUpLds - kUpRed<GROUP> - static_cast<int>(sizeof(Routing))) / 1024 * 1024;
+
+template <int TYPE, bool VEC, int GROUP, bool RESIDENT>
+__global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
   constexpr int kAt = 2;   // chunks of a wave at a time
+  constexpr int kChunkStage = PX * GROUP * 256;
   __shared__ Routing r;
-  // partial sums of the waves, of two items in turn; scratch of the routing first
-  constexpr int kRed = kMoeWaves * 2 * 64;
-  __shared__ __attribute__((aligned(16))) f32x4 red[2 * kRed];
-  __shared__ __attribute__((aligned(16))) unsigned char stages[kMoeWaves * PX * kStagePart];
-  static_assert(sizeof(RoutingScratch) <= sizeof(red), "scratch fits");
-  route(a, r, *reinterpret_cast<RoutingScratch *>(red));
+  __shared__ __attribute__((aligned(16))) unsigned char red[kUpRed<GROUP>];
+  // activations; scratch of the routing first
+  __shared__ __attribute__((aligned(16))) unsigned char stages[RESIDENT ? kUpStage<GROUP> : kMoeWaves * kAt * kChunkStage];
+  static_assert(sizeof(RoutingScratch) <= sizeof(stages), "scratch fits");
+  route<GROUP>(a, r, *reinterpret_cast<RoutingScratch *>(stages));
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int num_groups = __builtin_amdgcn_readfirstlane(r.num_groups);
@@ -416,7 +442,6 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
     if (threadIdx.x == 0) a.groups[0] = Group{static_cast<unsigned>(num_groups), r.nan_lo, r.nan_hi};
     for (int n = threadIdx.x; n < num_groups; n += kMoeThreads) a.groups[1 + n] = r.groups[n];
   }
-  unsigned char *stage = stages + wave * (PX * kStagePart);
   const int i16 = lane & 15, g = lane >> 4;
   const int HP = (a.hidden + kAlign - 1) / kAlign * kAlign;
   const int IP = (a.inter + kAlign - 1) / kAlign * kAlign;
@@ -424,10 +449,11 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
   const int batches = (chunks + kAt * kMoeWaves - 1) / (kAt * kMoeWaves);
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
   const int items = num_groups * tiles;
-  const int stride = __builtin_amdgcn_readfirstlane(gridDim.x);
+  const int wgs = __builtin_amdgcn_readfirstlane(gridDim.x);
+  int item = static_cast<int>(static_cast<long long>(items) * blockIdx.x / wgs);
+  const int end = static_cast<int>(static_cast<long long>(items) * (blockIdx.x + 1) / wgs);
+  if (item >= end) return;
 
-  // What an item's loads need: bases of the expert's rows, the lane's row and
-  // tokens.
   struct Item {
     int row0;
     Group group;
@@ -438,89 +464,101 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
   };
   struct Fetched {
     uintx4 gate[kAt], up[kAt];
-    unsigned gate_scale[kAt], up_scale[kAt];
-    Raw8<TYPE> x[kAt][2];
+    uintx2 gate_scale, up_scale;
   };
-  const long long up_codes = static_cast<long long>(a.inter) * (HP / 2);
-  const long long up_scales = static_cast<long long>(a.inter) * (HP / 32);
+  const long long rows = 2LL * a.experts * a.inter;
   auto fetch = [&](Fetched &f, const Item &t, int batch, bool wanted) __attribute__((always_inline)) {
     const int c = (batch * kMoeWaves + wave) * kAt;
     // rows past the expert's last: the last one again (their results are not kept)
     const int first = min(t.row0, a.inter - 1), i = min(i16, a.inter - 1 - first);
-    const long long row = static_cast<long long>(t.group.expert()) * 2 * a.inter + first;
-    const unsigned char *codes = a.w1c + row * (HP / 2) + c * 64, *scales = a.w1s + row * (HP / 32) + c * 4;
+    const long long gate = static_cast<long long>(t.group.expert()) * 2 * a.inter + first, up = gate + a.inter;
+    const __amdgpu_buffer_rsrc_t gc = buffer(a.w1c + gate * (HP / 2), (rows - gate) * (HP / 2));
+    const __amdgpu_buffer_rsrc_t uc = buffer(a.w1c + up * (HP / 2), (rows - up) * (HP / 2));
+    const __amdgpu_buffer_rsrc_t gs = buffer(a.w1s + gate * (HP / 32), (rows - gate) * (HP / 32));
+    const __amdgpu_buffer_rsrc_t us = buffer(a.w1s + up * (HP / 32), (rows - up) * (HP / 32));
     const unsigned code_off = wanted ? static_cast<unsigned>(i * (HP / 2) + g * 16) : 0;
-    const unsigned scale_off = wanted ? static_cast<unsigned>(i * (HP / 32) + g) : 0;
-    const store *x = static_cast<const store *>(a.x) + c * 128 + i16 * 8;
-    const store *x0 = x + static_cast<long long>((t.group.lo >> (8 * g)) & 255) * a.ldx;
-    const store *x1 = x + static_cast<long long>((t.group.hi >> (8 * g)) & 255) * a.ldx;
+    const unsigned scale_off = wanted ? static_cast<unsigned>(i * (HP / 32)) : 0;
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-      const int past = max(0, c + b - (chunks - 1));   // the last chunk again, not used
-      const unsigned char *pc = codes + (b - past) * 64, *ps = scales + (b - past) * 4;
-      f.gate[b] = *reinterpret_cast<const uintx4 *>(pc + code_off);
-      f.up[b] = *reinterpret_cast<const uintx4 *>(pc + up_codes + code_off);
-      f.gate_scale[b] = ps[scale_off];
-      f.up_scale[b] = (ps + up_scales)[scale_off];
-      const int left = a.hidden - (c + b - past) * 128 - i16 * 8;
-      f.x[b][0].template load<VEC>(x0 + (b - past) * 128, left);
-      f.x[b][1].template load<VEC>(x1 + (b - past) * 128, left);
+      const int cb = min(c + b, chunks - 1);   // past the end: the last chunk again, not used
+      f.gate[b] = load16(gc, code_off, cb * 64);
+      f.up[b] = load16(uc, code_off, cb * 64);
     }
+    const int cs = min(c, chunks - 1);
+    f.gate_scale = load8(gs, scale_off, cs * 4);
+    f.up_scale = load8(us, scale_off, cs * 4);
+  };
+  // The wave's chunks of batch of the group's activations into LDS.
+  auto stage_of = [&](int batch, int b) {
+    return stages + (RESIDENT ? (batch * kMoeWaves + wave) * kAt + b : wave * kAt + b) * kChunkStage;
+  };
+  auto stage_x = [&](unsigned lo, unsigned hi, int batch) __attribute__((always_inline)) {
+    const store *x = static_cast<const store *>(a.x) + i16 * 8;
+    const store *x0 = x + static_cast<long long>((lo >> (8 * g)) & 255) * a.ldx;
+    const store *x1 = x + static_cast<long long>((hi >> (8 * g)) & 255) * a.ldx;
+    const int c = (batch * kMoeWaves + wave) * kAt;
+    stage_order();
+#pragma unroll
+    for (int b = 0; b < kAt; ++b) {
+      if (c + b < chunks) {
+        const int left = a.hidden - (c + b) * 128 - i16 * 8;
+        unsigned char *stage = stage_of(batch, b);
+        Raw8<TYPE> v0, v1;
+        v0.template load<VEC>(x0 + (c + b) * 128, left);
+        if constexpr (GROUP > 4) v1.template load<VEC>(x1 + (c + b) * 128, left);
+        if (left <= 0) {
+          v0.clear();
+          if constexpr (GROUP > 4) v1.clear();
+        }
+        bf16x8 parts[PX];
+        v0.parts(parts);
+#pragma unroll
+        for (int p = 0; p < PX; ++p) stage_write<GROUP>(stage, p, g, i16, parts[p]);
+        if constexpr (GROUP > 4) {
+          v1.parts(parts);
+#pragma unroll
+          for (int p = 0; p < PX; ++p) stage_write<GROUP>(stage, p, 4 + g, i16, parts[p]);
+        }
+      }
+    }
+    stage_order();
   };
 
-  int item = blockIdx.x, batch = 0, turn = 0;
-  if (item >= items) return;
+  int batch = 0, turn = 0;
+  bool fresh = true;   // the group's activations are not in LDS yet
   Item now = item_of(item);
   f32x4 acc_gate = {}, acc_up = {};
   // One batch of an item from one set of registers, the next one's loads into the
   // other.
   auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
     const bool last = batch + 1 == batches;
-    const bool more = !last || item + stride < items;
-    const Item then = item_of(last && more ? item + stride : item);
+    const bool more = !last || item + 1 < end;
+    const Item then = item_of(last && more ? item + 1 : item);
     // Also after the last one (then all lanes load the same bytes): a branch
     // around the loads would make the compiler wait for them at its end.
     fetch(next, then, last ? 0 : batch + 1, more);
     __builtin_amdgcn_sched_barrier(0);
+    if (fresh || !RESIDENT) stage_x(now.group.lo, now.group.hi, batch);
     const int c = (batch * kMoeWaves + wave) * kAt;
+    arrived(cur.gate_scale);
+    arrived(cur.up_scale);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-#pragma unroll
-      for (int r = 0; r < (TYPE == kF32 ? 2 : 1); ++r) {
-        arrived(cur.x[b][0].v[r]);
-        arrived(cur.x[b][1].v[r]);
-      }
       arrived(cur.gate[b]);
       arrived(cur.up[b]);
-      arrived(cur.gate_scale[b]);
-      arrived(cur.up_scale[b]);
       if (c + b < chunks) {
-        stage_order();
-        Raw8<TYPE> first = cur.x[b][0], second = cur.x[b][1];
-        if (VEC && (c + b) * 128 + 128 > a.hidden && (c + b) * 128 + i16 * 8 >= a.hidden) {
-          first.clear();
-          second.clear();
-        }
-        bf16x8 parts[PX];
-        first.parts(parts);
-#pragma unroll
-        for (int p = 0; p < PX; ++p) stage_write(stage, p, g, i16, parts[p]);
-        second.parts(parts);
-#pragma unroll
-        for (int p = 0; p < PX; ++p) stage_write(stage, p, 4 + g, i16, parts[p]);
-        stage_order();
-        const float fg = scale_value(cur.gate_scale[b]), fu = scale_value(cur.up_scale[b]);
+        const unsigned char *stage = stage_of(batch, b);
+        const float fg = pair_scale(cur.gate_scale, b, g), fu = pair_scale(cur.up_scale, b, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const bf16x8 vg = weights8(cur.gate[b][j], fg), vu = weights8(cur.up[b][j], fu);
 #pragma unroll
           for (int p = 0; p < PX; ++p) {
-            const bf16x8 xv = stage_read(stage, p, i16 & (kGroup - 1), 4 * g + j);
+            const bf16x8 xv = stage_read<GROUP>(stage, p, i16 & (GROUP - 1), 4 * g + j);
             acc_gate = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, xv, acc_gate, 0, 0, 0);
             acc_up = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, xv, acc_up, 0, 0, 0);
           }
         }
-        __builtin_amdgcn_sched_barrier(0);   // one chunk's registers at a time
       }
     }
     if (!last) {
@@ -528,51 +566,54 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
       return;
     }
     // One barrier an item: the next one's sums go to the other half, and nobody
-    // writes this half again before having passed the next barrier.
-    f32x4 *sums = red + (turn & 1) * kRed;
-    sums[wave * 128 + lane] = acc_gate;
-    sums[wave * 128 + 64 + lane] = acc_up;
+    // writes this half again before having passed the next barrier. Of the 16
+    // columns the group's are kept: [wave][gate, up][g][column].
+    f32x4 *sums = reinterpret_cast<f32x4 *>(red) + (turn & 1) * (kMoeWaves * 2 * 4 * GROUP);
+    const int at = g * GROUP + i16;
+    if (i16 < GROUP) {
+      sums[wave * (8 * GROUP) + at] = acc_gate;
+      sums[wave * (8 * GROUP) + 4 * GROUP + at] = acc_up;
+    }
     __syncthreads();
-    if (wave == (turn & (kMoeWaves - 1))) {
-      f32x4 gv = sums[lane], uv = sums[64 + lane];
+    if (wave == (turn & (kMoeWaves - 1)) && i16 < now.group.count()) {
+      f32x4 gv = sums[at], uv = sums[4 * GROUP + at];
 #pragma unroll
       for (int w = 1; w < kMoeWaves; ++w) {
-        gv += sums[w * 128 + lane];
-        uv += sums[w * 128 + 64 + lane];
+        gv += sums[w * (8 * GROUP) + at];
+        uv += sums[w * (8 * GROUP) + 4 * GROUP + at];
       }
-      if (i16 < now.group.count()) {
-        const int p = now.group.base() + i16;
-        const float w = r.weight[p];
-        const int row = now.row0 + 4 * g;
-        u16 parts[PH][4];
+      const int p = now.group.base() + i16;
+      const float w = r.weight[p];
+      const int row = now.row0 + 4 * g;
+      u16 parts[PH][4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          // past the last row of an expert: the zeros that pad `inter`
-          float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
+      for (int v = 0; v < 4; ++v) {
+        // past the last row of an expert: the zeros that pad `inter`
+        float rest = row + v < a.inter ? gv[v] / (1.0f + expf(-gv[v])) * uv[v] * w : 0.0f;
 #pragma unroll
-          for (int q = 0; q < PH; ++q) {
-            const unsigned bits = __builtin_bit_cast(unsigned, rest);
-            parts[q][v] = q + 1 < PH || PH == 3 ? static_cast<u16>(bits >> 16) : Elem<kBf16>::put(rest);
-            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(parts[q][v]);
-          }
+        for (int q = 0; q < PH; ++q) {
+          const unsigned bits = __builtin_bit_cast(unsigned, rest);
+          parts[q][v] = q + 1 < PH || PH == 3 ? static_cast<u16>(bits >> 16) : Elem<kBf16>::put(rest);
+          rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(parts[q][v]);
         }
-#pragma unroll
-        for (int q = 0; q < PH; ++q)
-          *reinterpret_cast<uintx2 *>(a.h + q * plane + static_cast<long long>(p) * IP + row) =
-              uintx2{parts[q][0] | (static_cast<unsigned>(parts[q][1]) << 16),
-                     parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
       }
+#pragma unroll
+      for (int q = 0; q < PH; ++q)
+        *reinterpret_cast<uintx2 *>(a.h + q * plane + static_cast<long long>(p) * IP + row) =
+            uintx2{parts[q][0] | (static_cast<unsigned>(parts[q][1]) << 16),
+                   parts[q][2] | (static_cast<unsigned>(parts[q][3]) << 16)};
     }
     acc_gate = f32x4{};
     acc_up = f32x4{};
-    item += stride;
+    ++item;
     batch = 0;
     ++turn;
+    fresh = then.group.packed != now.group.packed;
     now = then;
   };
   Fetched even, odd;
   fetch(even, now, 0, true);
-  in_turn((items - item + stride - 1) / stride * batches, even, odd, step);
+  in_turn((end - item) * batches, even, odd, step);
 }
 
 // Y: a workgroup takes 16 rows of every reached expert's D. Its waves take the
@@ -580,21 +621,22 @@ __global__ __launch_bounds__(kMoeThreads, Parts<TYPE>::up_per_simd) void moe_up_
 // step's weights and activations on their way. An instruction's columns are the
 // group's tokens, so a step's sums are then added to the wave's own sums of
 // those tokens, in LDS; at the end the waves' sums are added in order.
-template <int TYPE>
-__global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per_simd) void moe_down_kernel(
+template <int TYPE, int GROUP>
+__global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_waves / 4) void moe_down_kernel(
     MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PH = Parts<TYPE>::h, W = Parts<TYPE>::down_waves, THREADS = 64 * W;
-  constexpr int kAt = 2;
+  constexpr int kAt = 2, kHalves = GROUP / 4;
+  constexpr int kChunkStage = PH * GROUP * 256;
   __shared__ Group groups[kMaxGroups + 1];
-  __shared__ __attribute__((aligned(16))) unsigned char stages[W * PH * kStagePart];
+  __shared__ __attribute__((aligned(16))) unsigned char stages[W * kChunkStage];
   __shared__ __attribute__((aligned(16))) float sums[W * kMaxTokens * 16];   // [wave][token][row]
-  const int most = min(a.experts, a.tokens * a.top_k) + a.tokens * a.top_k / kGroup + 1;
+  const int most = min(a.experts, a.tokens * a.top_k) + a.tokens * a.top_k / GROUP + 1;
   for (int n = threadIdx.x; n < most; n += THREADS) groups[n] = a.groups[n];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  unsigned char *stage = stages + wave * (PH * kStagePart);
+  unsigned char *stage = stages + wave * kChunkStage;
   float *mine = sums + wave * (kMaxTokens * 16);
   for (int n = lane; n < a.tokens * 4; n += 64) reinterpret_cast<f32x4 *>(mine)[n] = f32x4{};
   __syncthreads();
@@ -605,30 +647,33 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
   const int row0 = blockIdx.x * 16;
   const int row = min(i16, a.hidden - 1 - row0);
   const unsigned code_off = static_cast<unsigned>(row * (IP / 2) + g * 16);
-  const unsigned scale_off = static_cast<unsigned>(row * (IP / 32) + g);
-  const unsigned h_off = static_cast<unsigned>(g * IP), h4_off = static_cast<unsigned>((4 + g) * IP);
+  const unsigned scale_off = static_cast<unsigned>(row * (IP / 32));
+  const long long rows = static_cast<long long>(a.experts) * a.hidden;
 
   struct Fetched {
     uintx4 w[kAt];
-    unsigned scale[kAt];
-    uintx4 h[kAt][PH][2];
+    uintx2 scale;
+    uintx4 h[kAt][PH][kHalves];
   };
   auto fetch = [&](Fetched &f, const Group &now, int batch, bool wanted) __attribute__((always_inline)) {
     const long long wr = static_cast<long long>(now.expert()) * a.hidden + row0;
-    const unsigned char *codes = a.w2c + wr * (IP / 2), *scales = a.w2s + wr * (IP / 32);
-    const u16 *h = a.h + static_cast<long long>(now.base()) * IP + i16 * 8;
-    const unsigned last = static_cast<unsigned>((now.count() - 1) * IP);
-    const unsigned h0 = min(h_off, last), h1 = min(h4_off, last);
+    const __amdgpu_buffer_rsrc_t codes = buffer(a.w2c + wr * (IP / 2), (rows - wr) * (IP / 2));
+    const __amdgpu_buffer_rsrc_t scales = buffer(a.w2s + wr * (IP / 32), (rows - wr) * (IP / 32));
+    const u16 *h = a.h + static_cast<long long>(now.base()) * IP;
+    unsigned h_off[kHalves];   // (tokens past the group's last: the last one again)
+#pragma unroll
+    for (int s = 0; s < kHalves; ++s)
+      h_off[s] = static_cast<unsigned>(min(4 * s + g, now.count() - 1) * IP + i16 * 8);
+    f.scale = load8(scales, wanted ? scale_off : 0, min(batch * kAt, chunks - 1) * 4);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       const int c = min(batch * kAt + b, chunks - 1);   // past the end: not used
-      f.w[b] = *reinterpret_cast<const uintx4 *>(codes + c * 64 + (wanted ? code_off : 0));
-      f.scale[b] = (scales + c * 4)[wanted ? scale_off : 0];
+      f.w[b] = load16(codes, wanted ? code_off : 0, c * 64);
 #pragma unroll
-      for (int q = 0; q < PH; ++q) {
-        f.h[b][q][0] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h0);
-        f.h[b][q][1] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h1);
-      }
+      for (int q = 0; q < PH; ++q)
+#pragma unroll
+        for (int s = 0; s < kHalves; ++s)
+          f.h[b][q][s] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h_off[s]);
     }
   };
   int at = 0, batch = wave;   // the step: group and batch
@@ -648,32 +693,28 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_per
     fetch(next, then, more ? next_batch : batch, more);
     __builtin_amdgcn_sched_barrier(0);
     f32x4 acc = {};
+    arrived(cur.scale);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
-#pragma unroll
-      for (int q = 0; q < PH; ++q) {
-        arrived(cur.h[b][q][0]);
-        arrived(cur.h[b][q][1]);
-      }
       arrived(cur.w[b]);
-      arrived(cur.scale[b]);
-      if (batch * kAt + b < chunks) {
-        stage_order();
+      stage_order();
 #pragma unroll
-        for (int q = 0; q < PH; ++q) {
-          const uintx4 h0 = cur.h[b][q][0], h1 = cur.h[b][q][1];
-          stage_write(stage, q, g, i16, __builtin_bit_cast(bf16x8, h0));
-          stage_write(stage, q, 4 + g, i16, __builtin_bit_cast(bf16x8, h1));
+      for (int q = 0; q < PH; ++q)
+#pragma unroll
+        for (int s = 0; s < kHalves; ++s) {
+          const uintx4 h = cur.h[b][q][s];
+          stage_write<GROUP>(stage, q, 4 * s + g, i16, __builtin_bit_cast(bf16x8, h));
         }
-        stage_order();
-        const float f = scale_value(cur.scale[b]);
+      stage_order();
+      if (batch * kAt + b < chunks) {
+        const float f = pair_scale(cur.scale, b, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const bf16x8 v = weights8(cur.w[b][j], f);
 #pragma unroll
           for (int q = 0; q < PH; ++q)
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                v, stage_read(stage, q, i16 & (kGroup - 1), 4 * g + j), acc, 0, 0, 0);
+                v, stage_read<GROUP>(stage, q, i16 & (GROUP - 1), 4 * g + j), acc, 0, 0, 0);
         }
       }
     }

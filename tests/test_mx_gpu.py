@@ -390,7 +390,11 @@ def check_layer(got, x, logits, w1, w2, I, top_k, renorm, kind):
 
 LAYERS = [  # tokens, hidden, inter, experts, top_k
     (1, 128, 128, 4, 1), (1, 512, 256, 64, 4), (1, 100, 72, 3, 3), (2, 257, 129, 8, 2), (3, 33, 17, 512, 16), (7, 640, 200, 33, 5),
-    (16, 256, 128, 16, 4), (17, 130, 255, 5, 5), (31, 384, 96, 128, 8), (48, 200, 130, 6, 2), (64, 256, 128, 2, 1), (64, 144, 64, 65, 8), (5, 1, 1, 1, 1)]
+    (16, 256, 128, 16, 4), (17, 130, 255, 5, 5), (31, 384, 96, 128, 8), (48, 200, 130, 6, 2), (64, 256, 128, 2, 1), (64, 144, 64, 65, 8), (5, 1, 1, 1, 1),
+    # activations that do not fit LDS: loaded again for every item
+    (2, 17408, 40, 2, 1), (20, 7704, 33, 2, 1), (3, 6001, 20, 2, 2),
+    # several batches of K a wave, experts in every width of the routing
+    (9, 9000, 24, 20, 3), (40, 5120, 16, 200, 4), (33, 96, 4200, 300, 2)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
