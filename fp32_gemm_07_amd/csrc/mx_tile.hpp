@@ -87,7 +87,7 @@ void tile_kernel(TileArgs a) {
   // Instruction q of 4 stages' scales fills rows 64q .. 64q + 63, a lane a row.
   auto copy_scales = [&](int q4, int super) {
     const int q = wave + 4 * q4;
-    if (q * 1024 < S::kScales) {
+    if (S::kScales % 4096 == 0 || q * 1024 < S::kScales) {
       const bool of_a = q * 64 < BM;
       const unsigned row = static_cast<unsigned>(of_a ? q * 64 : q * 64 - BM) + lane;
       const unsigned so = super * 4 < stages ? static_cast<unsigned>(super) * 16u : kOutOfRange;
@@ -121,15 +121,13 @@ void tile_kernel(TileArgs a) {
 
   f32x16 acc[FM][FN] = {};
 
-  // Prologue: the first 4 stages and 8 stages' scales on their way.
+  // Prologue: the first 4 stages and their scales on their way.
 #pragma unroll
   for (int q = 0; q < S::kScaleCopies; ++q) copy_scales(q, 0);
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int q = 0; q < S::kCopies; ++q) copy_codes(q, s, s * S::kStage);
-#pragma unroll
-  for (int q = 0; q < S::kScaleCopies; ++q) copy_scales(q, 1);
   wait_vmcnt<3 * S::kCopies>();
   asm volatile("s_barrier" : : : "memory");
 #pragma unroll
@@ -141,6 +139,13 @@ void tile_kernel(TileArgs a) {
   constexpr int kMfmas = FM * FN;
   for (int t = 0; t < stages; ++t) {
     const int base = (t & 3) * S::kStage, next = ((t + 1) & 3) * S::kStage;
+    // The scales of the next 4 stages, into the half that the 4 before this one had
+    // (all read before the last barrier). A branch after the instructions below
+    // would let the compiler move all of them behind it.
+    if ((t & 3) == 0) {
+#pragma unroll
+      for (int q = 0; q < S::kScaleCopies; ++q) copy_scales(q, (t >> 2) + 1);
+    }
 #pragma unroll
     for (int f = 0; f < FM; ++f) sa[f] = static_cast<int>(static_cast<unsigned>(sa_raw[f]) >> (8 * h));
 #pragma unroll
@@ -184,12 +189,6 @@ void tile_kernel(TileArgs a) {
         constexpr int q0 = (n - kBefore) * S::kCopies / span, q1 = (n - kBefore + 1) * S::kCopies / span;
 #pragma unroll
         for (int q = q0; q < q1; ++q) copy_codes(q, t + NS, base);
-        if constexpr (n == kMfmas - 1) {
-          if ((t & 3) == 3) {
-#pragma unroll
-            for (int q = 0; q < S::kScaleCopies; ++q) copy_scales(q, (t >> 2) + 2);
-          }
-        }
       }
       __builtin_amdgcn_sched_barrier(0);
     });
