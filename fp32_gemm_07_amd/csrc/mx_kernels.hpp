@@ -103,6 +103,14 @@ __device__ inline void store8(typename Elem<TYPE>::store *p, int n, const float 
   }
 }
 
+// Order between the LDS accesses of a wave's lanes: LDS serves them in order, so only
+// the compiler has to keep them.
+__device__ inline void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------
 // The e8m0 scale of a block and its values.
 

@@ -309,14 +309,6 @@ __device__ inline bf16x8 stage_read(const unsigned char *stage, int part, int to
   return *reinterpret_cast<const bf16x8 *>(stage + (part * GROUP + token) * 256 +
                                            ((piece ^ token) & 15) * 16);
 }
-// Order between the lanes of a wave: LDS serves a wave's accesses in order, so
-// only the compiler has to keep them.
-__device__ inline void stage_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Loads through a buffer resource: a uniform base and the bytes behind it (dwords
 // past them read as zero), a lane's offset and a uniform one.
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const unsigned char *base, long long bytes) {
@@ -497,7 +489,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
     const store *x0 = x + static_cast<long long>((lo >> (8 * g)) & 255) * a.ldx;
     const store *x1 = x + static_cast<long long>((hi >> (8 * g)) & 255) * a.ldx;
     const int c = (batch * kMoeWaves + wave) * kAt;
-    stage_order();
+    wave_order();
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       if (c + b < chunks) {
@@ -521,7 +513,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
         }
       }
     }
-    stage_order();
+    wave_order();
   };
 
   int batch = 0, turn = 0;
@@ -697,7 +689,7 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       arrived(cur.w[b]);
-      stage_order();
+      wave_order();
 #pragma unroll
       for (int q = 0; q < PH; ++q)
 #pragma unroll
@@ -705,7 +697,7 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
           const uintx4 h = cur.h[b][q][s];
           stage_write<GROUP>(stage, q, 4 * s + g, i16, __builtin_bit_cast(bf16x8, h));
         }
-      stage_order();
+      wave_order();
       if (batch * kAt + b < chunks) {
         const float f = pair_scale(cur.scale, b, g);
 #pragma unroll

@@ -26,6 +26,23 @@ namespace mx {
 //
 // Rows past M or N and stages past the K range are outside the copies' buffer
 // ranges and read as zeros (a zero scale byte is 2^-127, not NaN).
+// 16 bytes of C: alpha * sums + beta * C, or with RAW the sums.
+template <int TYPE, bool RAW>
+__device__ inline void store_vec(typename Elem<TYPE>::store *c, const float *s, float alpha, float beta) {
+  constexpr int kVec = TYPE == kF32 ? 4 : 8;
+  typedef typename Elem<TYPE>::store store;
+  struct __attribute__((aligned(16))) Vec {
+    store e[kVec];
+  } v;
+  if (!RAW && beta != 0.0f) v = *reinterpret_cast<const Vec *>(c);
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    const float r = RAW ? s[e] : beta == 0.0f ? alpha * s[e] : fmaf(alpha, s[e], beta * Elem<TYPE>::get(v.e[e]));
+    v.e[e] = Elem<TYPE>::put(r);
+  }
+  *reinterpret_cast<Vec *>(c) = v;
+}
+
 struct TileArgs {
   const unsigned char *ac, *as, *bc, *bs;
   void *C;       // of the launch's type, or with a split float partial sums
@@ -155,7 +172,7 @@ void tile_kernel(TileArgs a) {
       constexpr int n = decltype(n_c)::value;
       constexpr int fm = n / FN, fn = n % FN;
       acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          widen(fa[0][fm]), widen(fb[0][fn]), acc[fm][fn], 4, 4, 0, sa[fm], 0, sb[fn]);
+          widen(fb[0][fn]), widen(fa[0][fm]), acc[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
       if constexpr (n < FM) read_a(n, base, 1);
       else if constexpr (n < FM + FN) read_b(n - FM, base, 1);
       if constexpr (n == kMfmas - 1 && FM + FN > kMfmas) {
@@ -176,7 +193,7 @@ void tile_kernel(TileArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
       acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          widen(fa[1][fm]), widen(fb[1][fn]), acc[fm][fn], 4, 4, 2, sa[fm], 2, sb[fn]);
+          widen(fb[1][fn]), widen(fa[1][fm]), acc[fm][fn], 4, 4, 2, sb[fn], 2, sa[fm]);
       if constexpr (n == kBefore) {
         read_scales(t + 1);
 #pragma unroll
@@ -195,26 +212,57 @@ void tile_kernel(TileArgs a) {
   }
   wait_vmcnt<0>();   // no copy may land after the workgroup's LDS is another's
 
-  // Accumulator v of lane (h, i): row 8 (v / 4) + 4 h + v % 4, column i.
+  // B's rows are the instructions' rows: accumulator v of lane (h, i) is row i of C
+  // and column 8 (v / 4) + 4 h + v % 4 of a block, four neighbouring columns at a
+  // time. 32 rows of the wave's tile pass through its own piece of LDS and leave
+  // as whole rows, 16 bytes a lane (each lane storing what it holds, a few bytes
+  // to each of 32 rows, took 14 us for a 256 x 256 tile, this 2 us).
+  asm volatile("s_barrier" : : : "memory");   // everybody has read the last stage
+  constexpr int kCols = BN / 2, kStride = kCols + 4;
+  static_assert(4 * 32 * kStride * 4 <= S::kLds, "fits the ring");
+  float *out = reinterpret_cast<float *>(lds) + wave * (32 * kStride);
+  constexpr int OUT = SPLIT ? kF32 : TYPE;
+  typedef typename Elem<OUT>::store store;
+  constexpr int kVec = OUT == kF32 ? 4 : 8;             // elements of 16 bytes
+  constexpr int kLanes = kCols / kVec, kRows = 64 / kLanes;   // lanes of a row, rows at a time
+  store *c = static_cast<store *>(a.C) + (SPLIT ? static_cast<long long>(split) * a.M * a.N : 0);
+  const long long ldc = SPLIT ? a.N : a.ldc;
+  const int col = n0 + wn * kCols + (lane % kLanes) * kVec;
+  const bool vec = col + kVec <= a.N && ldc % kVec == 0 && reinterpret_cast<uintptr_t>(c) % 16 == 0;
 #pragma unroll
-  for (int fm = 0; fm < FM; ++fm)
+  for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int row = m0 + wm * (BM / 2) + fm * 32 + 8 * (v / 4) + 4 * h + v % 4;
-      if (row < a.M) {
+    for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn) {
-          const int col = n0 + wn * (BN / 2) + fn * 32 + i;
-          if (col < a.N) {
-            if constexpr (SPLIT)
-              static_cast<float *>(a.C)[(static_cast<long long>(split) * a.M + row) * a.N + col] = acc[fm][fn][v];
-            else
-              store_c<TYPE>(static_cast<typename Elem<TYPE>::store *>(a.C) + static_cast<long long>(row) * a.ldc + col,
-                            acc[fm][fn][v], a.alpha, a.beta);
+      for (int v = 0; v < 16; v += 4)
+        *reinterpret_cast<f32x4 *>(out + i * kStride + fn * 32 + 2 * v + 4 * h) =
+            f32x4{acc[fm][fn][v], acc[fm][fn][v + 1], acc[fm][fn][v + 2], acc[fm][fn][v + 3]};
+    wave_order();
+#pragma unroll 4
+    for (int r = lane / kLanes; r < 32; r += kRows) {
+      const int row = m0 + wm * (BM / 2) + fm * 32 + r;
+      float s[kVec];
+#pragma unroll
+      for (int e = 0; e < kVec; e += 4) {
+        const f32x4 q = *reinterpret_cast<const f32x4 *>(out + r * kStride + (lane % kLanes) * kVec + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[e + k] = q[k];
+      }
+      if (row >= a.M) continue;
+      store *p = c + row * ldc + col;
+      if (vec) {
+        store_vec<OUT, SPLIT>(p, s, a.alpha, a.beta);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          if (col + e < a.N) {
+            if constexpr (SPLIT) p[e] = s[e];
+            else store_c<OUT>(p + e, s[e], a.alpha, a.beta);
           }
-        }
       }
     }
+    wave_order();
+  }
 }
 
 // C <- alpha * (sum of the splits' partial sums, in ascending order) + beta * C.
