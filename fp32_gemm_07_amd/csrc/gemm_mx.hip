@@ -93,6 +93,11 @@ bool row_launch(int rows, int KP, RowLaunch *l) {
   return blocks <= INT32_MAX;
 }
 
+// Whether the column kernels can take a stored matrix two neighbours at a time.
+bool pairs_fit(int rows, const void *mat, int ld, int type) {
+  return rows % 2 == 0 && ld % 2 == 0 && aligned(mat, 2 * elem_size(type));
+}
+
 // ---------------------------------------------------------------------------
 // Product.
 struct Product {
@@ -115,9 +120,9 @@ ProductPlan plan_product(int M, int N, int K, int cus) {
   ProductPlan best{0, 0, 1, KP};
   if (M <= 32 && static_cast<long long>(M) * N < 64 * 64) return best;
   double best_us = 1e30;
-  const int tiles[3][2] = {{256, 256}, {128, 128}, {64, 64}};
-  const double rate[3] = {16384 * 0.6, 16384 * 0.35, 16384 * 0.15};   // flop per clock per CU
-  for (int c = 0; c < 3; ++c) {
+  const int tiles[4][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
+  const double rate[4] = {16384 * 0.6, 16384 * 0.5, 16384 * 0.35, 16384 * 0.15};   // flop per clock per CU
+  for (int c = 0; c < 4; ++c) {
     const long long tm = ceil_div(M, tiles[c][0]), tn = ceil_div(N, tiles[c][1]);
     for (int s = 1; s <= 64; s *= 2) {
       const int chunk = static_cast<int>(ceil_div(ceil_div(KP, s), 128) * 128);
@@ -162,7 +167,8 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
     plan.splits = 1;
     plan.k_chunk = padded(p.K);
   }
-  if (plan.bm == 256) launch_tile<256, 256, 1>(p, plan, ws, stream);
+  if (plan.bn == 256) launch_tile<256, 256, 1>(p, plan, ws, stream);
+  else if (plan.bm == 256) launch_tile<256, 128, 1>(p, plan, ws, stream);
   else if (plan.bm == 128) launch_tile<128, 128, 2>(p, plan, ws, stream);
   else if (plan.bm == 64) launch_tile<64, 64, 2>(p, plan, ws, stream);
   else {
@@ -330,21 +336,26 @@ int gemm_mx_quantize(int trans, int rows, int K, const void *X, int x_type, int 
   const int KP = padded(K);
   const long long k_tiles = ceil_div(KP, kColK);
   RowLaunch l;
-  if (trans ? ceil_div(rows, kColRows) * k_tiles > INT32_MAX : !row_launch(rows, KP, &l))
-    return GEMM_ERR_INVALID_DIM;
+  const long long col_blocks = ceil_div(rows, 64) * k_tiles;   // (half as many for pairs)
+  if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
+  const bool pairs = pairs_fit(rows, X, ldx, x_type);
   const bool vec = aligned(X, 16) && (static_cast<size_t>(ldx) * elem_size(x_type)) % 16 == 0;
   unsigned *c = static_cast<unsigned *>(codes);
   with_type(x_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     const typename Elem<T>::store *x = static_cast<const typename Elem<T>::store *>(X);
-    if (trans)
-      hipLaunchKernelGGL(quantize_columns_kernel<T>,
-                         dim3(static_cast<unsigned>(ceil_div(rows, kColRows) * k_tiles)), dim3(256),
-                         0, stream, x, ldx, c, static_cast<unsigned *>(scales), rows, K, KP,
-                         static_cast<int>(k_tiles));
+    if (trans && pairs)
+      hipLaunchKernelGGL((quantize_columns_kernel<T, 2>),
+                         dim3(static_cast<unsigned>(ceil_div(rows, 128) * k_tiles)),
+                         dim3(kColThreads), 0, stream, x, ldx, c, static_cast<unsigned *>(scales),
+                         rows, K, KP, static_cast<int>(k_tiles));
+    else if (trans)
+      hipLaunchKernelGGL((quantize_columns_kernel<T, 1>), dim3(static_cast<unsigned>(col_blocks)),
+                         dim3(kColThreads), 0, stream, x, ldx, c, static_cast<unsigned *>(scales),
+                         rows, K, KP, static_cast<int>(k_tiles));
     else if (vec)
       hipLaunchKernelGGL((quantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, x,
                          ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
@@ -362,21 +373,27 @@ int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void
   const int KP = padded(K);
   const long long k_tiles = ceil_div(KP, kColK);
   RowLaunch l;
-  if (trans ? ceil_div(rows, kColRows) * k_tiles > INT32_MAX : !row_launch(rows, KP, &l))
-    return GEMM_ERR_INVALID_DIM;
+  const long long col_blocks = ceil_div(rows, 64) * k_tiles;   // (half as many for pairs)
+  if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
+  const bool pairs = pairs_fit(rows, Y, ldy, y_type);
   const bool vec = aligned(Y, 16) && (static_cast<size_t>(ldy) * elem_size(y_type)) % 16 == 0;
   const unsigned *c = static_cast<const unsigned *>(codes);
   const unsigned char *s = static_cast<const unsigned char *>(scales);
   with_type(y_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     typename Elem<T>::store *y = static_cast<typename Elem<T>::store *>(Y);
-    if (trans)
-      hipLaunchKernelGGL(dequantize_columns_kernel<T>,
-                         dim3(static_cast<unsigned>(ceil_div(rows, kColRows) * k_tiles)), dim3(256),
-                         0, stream, c, s, y, ldy, rows, K, KP, static_cast<int>(k_tiles));
+    if (trans && pairs)
+      hipLaunchKernelGGL((dequantize_columns_kernel<T, 2>),
+                         dim3(static_cast<unsigned>(ceil_div(rows, 128) * k_tiles)),
+                         dim3(kColThreads), 0, stream, c, s, y, ldy, rows, K, KP,
+                         static_cast<int>(k_tiles));
+    else if (trans)
+      hipLaunchKernelGGL((dequantize_columns_kernel<T, 1>), dim3(static_cast<unsigned>(col_blocks)),
+                         dim3(kColThreads), 0, stream, c, s, y, ldy, rows, K, KP,
+                         static_cast<int>(k_tiles));
     else if (vec)
       hipLaunchKernelGGL((dequantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, c,
                          s, y, ldy, rows, K, KP, l.map);

@@ -234,59 +234,79 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Quantisation across the stored rows (the operand's rows are X's columns):
-// a workgroup of 4 waves takes 64 operand rows by 256 values of K. Lanes run
-// along the stored rows, a lane collecting the 32 values of its block itself;
-// the codes pass through LDS so that each operand row is written in runs of
-// 64 or 128 bytes.
-constexpr int kColRows = 64;       // operand rows of a tile
-constexpr int kColK = 256;         // values of K of a tile
-constexpr int kColStride = 36;     // LDS words of a row's 128 code bytes, padded
+// Quantisation across the stored rows (the operand's rows are X's columns): a
+// workgroup of 8 waves takes 64 * VEC operand rows by 256 values of K, a wave
+// one block of 32 of each row. Lanes run along the stored rows, VEC = 2
+// neighbouring values a lane where their alignment allows it (256 bytes and more
+// a load), and a lane collects the 32 values of its blocks itself; the codes
+// pass through LDS so that each operand row is written in runs of 64 or 128
+// bytes.
+constexpr int kColWaves = 8;
+constexpr int kColThreads = 64 * kColWaves;
+constexpr int kColK = kColWaves * kBlock;   // values of K of a tile
+constexpr int kColStride = 36;              // LDS words of a row's 128 code bytes, padded
 
-template <int TYPE>
-__global__ __launch_bounds__(256) void quantize_columns_kernel(
+// VEC neighbouring elements as loaded or to be stored.
+template <int TYPE, int VEC>
+struct __attribute__((aligned(sizeof(typename Elem<TYPE>::store) * VEC))) Neighbours {
+  typename Elem<TYPE>::store e[VEC];
+};
+
+template <int TYPE, int VEC>
+__global__ __launch_bounds__(kColThreads) void quantize_columns_kernel(
     const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
     unsigned *__restrict__ scales, int rows, int K, int KP, int k_tiles) {
-  __shared__ __attribute__((aligned(16))) unsigned tile[kColRows * kColStride];
-  __shared__ unsigned char tile_scales[kColRows * 8];
+  constexpr int kRows = 64 * VEC;
+  __shared__ __attribute__((aligned(16))) unsigned tile[kRows * kColStride];
+  __shared__ __attribute__((aligned(4))) unsigned char tile_scales[kRows * 8];
   const int rt = blockIdx.x / k_tiles;
   const int k0 = (blockIdx.x - rt * k_tiles) * kColK;
-  const long long r0 = static_cast<long long>(rt) * kColRows;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool ok = r0 + lane < rows;
+  const long long r0 = static_cast<long long>(rt) * kRows;
+  const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
+  const int kb = k0 + b * kBlock;
+  const bool ok = r0 + lane * VEC < rows;   // VEC = 2: `rows` is even
+  if (kb < KP) {
+    typedef Neighbours<TYPE, VEC> Pair;
+    const typename Elem<TYPE>::store *p = X + static_cast<long long>(kb) * ldx + r0 + lane * VEC;
+    Pair raw[kBlock] = {};
+    if (ok && kb + kBlock <= K) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int b = wave + 4 * h;
-    const int kb = k0 + b * kBlock;
-    float v[4][8];
-    unsigned m = 0;
-    if (kb < KP) {
-      const typename Elem<TYPE>::store *p = X + static_cast<long long>(kb) * ldx + r0 + lane;
+      for (int i = 0; i < kBlock; ++i)
+        raw[i] = *reinterpret_cast<const Pair *>(p + static_cast<long long>(i) * ldx);
+    } else if (ok) {
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i)
+        if (kb + i < K) raw[i] = *reinterpret_cast<const Pair *>(p + static_cast<long long>(i) * ldx);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      unsigned m = 0;
+      float v[4][8];
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) {
-        v[i / 8][i % 8] =
-            ok && kb + i < K ? Elem<TYPE>::get(p[static_cast<long long>(i) * ldx]) : 0.0f;
+        v[i / 8][i % 8] = Elem<TYPE>::get(raw[i].e[e]);
         m = max(m, magnitude_bits(v[i / 8][i % 8]));
       }
       const unsigned s = scale_byte(m);
       uintx4 c;
 #pragma unroll
       for (int q = 0; q < 4; ++q) c[q] = s == 255 ? 0u : encode8(v[q], inverse_scale(s));
-      *reinterpret_cast<uintx4 *>(&tile[lane * kColStride + b * 4]) = c;
-      tile_scales[lane * 8 + b] = static_cast<unsigned char>(s);
+      const int row = lane * VEC + e;
+      *reinterpret_cast<uintx4 *>(&tile[row * kColStride + b * 4]) = c;
+      tile_scales[row * 8 + b] = static_cast<unsigned char>(s);
     }
   }
   __syncthreads();
   const int words = min(kColK, KP - k0) / 8;   // code words of a row here: 16 or 32
 #pragma unroll
-  for (int i = 0; i < kColRows * 8 / 256; ++i) {
-    const int e = threadIdx.x + 256 * i;
+  for (int i = 0; i < kRows * 8 / kColThreads; ++i) {
+    const int e = threadIdx.x + kColThreads * i;
     const int r = e >> 3, w = (e & 7) * 4;
     if (r0 + r < rows && w < words)
       *reinterpret_cast<uintx4 *>(codes + (r0 + r) * (KP / 8) + k0 / 8 + w) =
           *reinterpret_cast<const uintx4 *>(&tile[r * kColStride + w]);
   }
-  if (threadIdx.x < kColRows * 2) {
+  if (threadIdx.x < kRows * 2) {
     const int r = threadIdx.x >> 1, w = threadIdx.x & 1;
     if (r0 + r < rows && w * 16 < words)
       scales[(r0 + r) * (KP / 128) + k0 / 128 + w] =
@@ -294,41 +314,51 @@ __global__ __launch_bounds__(256) void quantize_columns_kernel(
   }
 }
 
-template <int TYPE>
-__global__ __launch_bounds__(256) void dequantize_columns_kernel(
+// The way back, the same tiles.
+template <int TYPE, int VEC>
+__global__ __launch_bounds__(kColThreads) void dequantize_columns_kernel(
     const unsigned *__restrict__ codes, const unsigned char *__restrict__ scales,
     typename Elem<TYPE>::store *__restrict__ Y, int ldy, int rows, int K, int KP, int k_tiles) {
-  __shared__ __attribute__((aligned(16))) unsigned tile[kColRows * kColStride];
+  constexpr int kRows = 64 * VEC;
+  __shared__ __attribute__((aligned(16))) unsigned tile[kRows * kColStride];
   const int rt = blockIdx.x / k_tiles;
   const int k0 = (blockIdx.x - rt * k_tiles) * kColK;
-  const long long r0 = static_cast<long long>(rt) * kColRows;
+  const long long r0 = static_cast<long long>(rt) * kRows;
   const int words = min(kColK, KP - k0) / 8;
 #pragma unroll
-  for (int i = 0; i < kColRows * 8 / 256; ++i) {
-    const int e = threadIdx.x + 256 * i;
+  for (int i = 0; i < kRows * 8 / kColThreads; ++i) {
+    const int e = threadIdx.x + kColThreads * i;
     const int r = e >> 3, w = (e & 7) * 4;
     if (r0 + r < rows && w < words)
       *reinterpret_cast<uintx4 *>(&tile[r * kColStride + w]) =
           *reinterpret_cast<const uintx4 *>(codes + (r0 + r) * (KP / 8) + k0 / 8 + w);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (r0 + lane >= rows) return;
+  const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
+  const int kb = k0 + b * kBlock;
+  const long long row = r0 + lane * VEC;
+  if (row >= rows || kb >= K) return;   // VEC = 2: `rows` is even
+  uintx4 c[VEC];
+  float s[VEC];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int b = wave + 4 * h;
-    const int kb = k0 + b * kBlock;
-    if (kb >= K) continue;
-    const uintx4 c = *reinterpret_cast<const uintx4 *>(&tile[lane * kColStride + b * 4]);
-    const float s = scale_value(scales[(r0 + lane) * (KP / 32) + kb / 32]);
-    typename Elem<TYPE>::store *p = Y + static_cast<long long>(kb) * ldy + r0 + lane;
+  for (int e = 0; e < VEC; ++e) {
+    c[e] = *reinterpret_cast<const uintx4 *>(&tile[(lane * VEC + e) * kColStride + b * 4]);
+    s[e] = scale_value(scales[(row + e) * (KP / 32) + kb / 32]);
+  }
+  typedef Neighbours<TYPE, VEC> Pair;
+  typename Elem<TYPE>::store *p = Y + static_cast<long long>(kb) * ldy + row;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[8];
-      decode8(c[q], s, v);
+  for (int q = 0; q < 4; ++q) {
+    float v[VEC][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (kb + 8 * q + i < K) p[static_cast<long long>(8 * q + i) * ldy] = Elem<TYPE>::put(v[i]);
+    for (int e = 0; e < VEC; ++e) decode8(c[e][q], s[e], v[e]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      Pair out;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) out.e[e] = Elem<TYPE>::put(v[e][i]);
+      if (kb + 8 * q + i < K)
+        *reinterpret_cast<Pair *>(p + static_cast<long long>(8 * q + i) * ldy) = out;
     }
   }
 }
