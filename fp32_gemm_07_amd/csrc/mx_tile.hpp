@@ -13,8 +13,8 @@ namespace mx {
 // Both operands are K-contiguous rows of codes, so both are staged the same way:
 // a stage is 128 values of K, 64 bytes a row, copied straight into LDS (16 bytes
 // a lane) through a ring of 4 stages. Within a stage row x keeps its 16-byte
-// chunk c (one block of 32 values) at c ^ ((x >> 1) & 3): 8 consecutive rows of
-// one chunk, which 8 lanes read at a time, then cover all of 128 bytes. The
+// chunk c (one block of 32 values) at c ^ ((x >> 2) & 3): 16 consecutive rows of
+// one chunk, which 16 lanes read at a time, then meet every bank once. The
 // scales of 512 values (16 bytes a row) go through a ring of 2 of their own.
 //
 // A stage is two steps of 64 values: lane (h, i) of an instruction holds block
@@ -92,7 +92,7 @@ void tile_kernel(TileArgs a) {
   const u32x4 rsb = make_buffer_rsrc(a.bs + n0 * scale_row + k0 / 32, (a.N - n0) * scale_row - k0 / 32);
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(lds));
   const unsigned lane_off = static_cast<unsigned>((lane >> 2) * code_row) +
-                            static_cast<unsigned>(((lane & 3) ^ ((lane >> 3) & 3)) * 16);
+                            static_cast<unsigned>(((lane & 3) ^ ((lane >> 4) & 3)) * 16);
   auto copy_codes = [&](int q4, int stage, int base) {
     const int q = wave + 4 * q4;   // q4 is a constant, so is the operand (BM, BN multiples of 64)
     const bool of_a = q4 * 64 < BM;
@@ -117,7 +117,7 @@ void tile_kernel(TileArgs a) {
   // byte 2 * step is the lane's.
   intx4 fa[2][FM], fb[2][FN];
   int sa[FM], sb[FN], sa_raw[FM], sb_raw[FN];
-  const int sw = (i >> 1) & 3;
+  const int sw = (i >> 2) & 3;
   const int off0 = i * 64 + ((h ^ sw) * 16);
   const unsigned char *la = lds + wm * (BM / 2) * 64, *lb = lds + (BM + wn * (BN / 2)) * 64;
   const unsigned char *lsa = lds + NS * S::kStage + (wm * (BM / 2) + i) * 16;
