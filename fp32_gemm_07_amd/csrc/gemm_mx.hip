@@ -108,35 +108,62 @@ struct Product {
   int type, ldc;
 };
 
+// How a product is computed: tiles of bm x bn, or with bm = 0 the kernel for few
+// rows of A; K cut into `splits` ranges of k_chunk.
 struct ProductPlan {
-  int bm, bn;    // 0: the simple kernel
+  int bm, bn;
   int splits, k_chunk;
 };
 
 constexpr size_t kMaxWorkspace = size_t(64) << 20;
 
+// The time of a tile on one CU: us of a 128-value stage of K when it has the CU to
+// itself, when it shares it (or follows others on it), and of its start and end.
+// Fitted on an MI355X over 20 shapes (M 1 .. 6000, K 128 .. 131072), where the
+// tiles take 47, 54, 55 and 90 us in this order at 4096^3 and 40, 29, 30 and
+// 45 us at 2048 x 4096 x 4096.
+struct TileCost {
+  int bm, bn;
+  double alone, shared, ends;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 1.03, 1.03, 9.5},
+    {256, 128, 0.62, 0.62, 5.5},
+    {128, 128, 0.35, 0.38, 1.5},
+    {64, 64, 0.14, 0.165, 0.8},
+};
+// The sum of split partial sums: its launch, and bytes a us.
+constexpr double kSumUs = 3.0, kSumBytesPerUs = 4.5e6;
+
 ProductPlan plan_product(int M, int N, int K, int cus) {
   const int KP = padded(K);
-  ProductPlan best{0, 0, 1, KP};
-  if (M <= 32 && static_cast<long long>(M) * N < 64 * 64) return best;
+  ProductPlan best{};
   double best_us = 1e30;
-  const int tiles[4][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
-  const double rate[4] = {16384 * 0.6, 16384 * 0.5, 16384 * 0.35, 16384 * 0.15};   // flop per clock per CU
-  for (int c = 0; c < 4; ++c) {
-    const long long tm = ceil_div(M, tiles[c][0]), tn = ceil_div(N, tiles[c][1]);
+  for (const TileCost &c : kTiles) {
+    const long long tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
+    if (tiles > INT32_MAX) continue;
     for (int s = 1; s <= 64; s *= 2) {
-      const int chunk = static_cast<int>(ceil_div(ceil_div(KP, s), 128) * 128);
+      const int chunk = static_cast<int>(ceil_div(ceil_div(KP, s), kAlign) * kAlign);
       const int splits = static_cast<int>(ceil_div(KP, chunk));
-      if (s > 1 && (splits < s || chunk < 512)) break;
-      if (s > 1 && 4.0 * splits * M * static_cast<double>(N) > kMaxWorkspace) break;
-      const double rounds = ceil_div(tm * tn * splits, cus);
-      double us = rounds * (2.0 * tiles[c][0] * tiles[c][1] * chunk / rate[c] / 2400 + 2.0);
-      if (splits > 1) us += 3.0 + (2.0 * splits + 1) * 4 * M * static_cast<double>(N) / 4e6;
+      const double partial = 4.0 * splits * M * static_cast<double>(N);
+      if (s > 1 && (chunk < 512 || partial > kMaxWorkspace)) break;
+      const long long rounds = ceil_div(tiles * splits, cus);
+      double us = rounds * (chunk / kAlign * (rounds > 1 ? c.shared : c.alone) + c.ends);
+      if (splits > 1) us += kSumUs + 2 * partial / kSumBytesPerUs;
       if (us < best_us * 0.99) {
         best_us = us;
-        best = ProductPlan{tiles[c][0], tiles[c][1], splits, chunk};
+        best = ProductPlan{c.bm, c.bn, splits, chunk};
       }
     }
+  }
+  // Few rows: a round of one workgroup (16 rows of B) a CU takes 2.2 us for each 4
+  // chunks of its 8 waves, 4.5 with two tiles of A's rows, less a little (no stages
+  // to fill). 1 x 4096 x 4096: 5.2 us against 7.4 (64 x 64, 4 splits); 32 x 4096 x
+  // 4096: 7.6 against 8.3; 24 x 8192 x 4096: 11.6 against 9.5 (64 x 64, whole).
+  if (M <= 32) {
+    const long long rounds = ceil_div(ceil_div(N, 16), cus);
+    const double us = rounds * ceil_div(KP / kAlign, kSkinnyWaves * kSkinnyAt) * (M <= 16 ? 2.2 : 4.5) - 0.3;
+    if (us < best_us) best = ProductPlan{0, 0, 1, KP};
   }
   return best;
 }
@@ -172,14 +199,13 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
   else if (plan.bm == 128) launch_tile<128, 128, 2>(p, plan, ws, stream);
   else if (plan.bm == 64) launch_tile<64, 64, 2>(p, plan, ws, stream);
   else {
-    const int tiles_n = static_cast<int>(ceil_div(p.N, 32));
     with_type(p.type, [&](auto t) {
       constexpr int T = decltype(t)::value;
-      typedef typename Elem<T>::store store;
-      hipLaunchKernelGGL(product_simple_kernel<T>,
-                         dim3(static_cast<unsigned>(ceil_div(p.M, 32) * tiles_n)), dim3(64), 0,
-                         stream, p.ac, p.as, p.bc, p.bs, static_cast<store *>(p.C), p.M, p.N,
-                         padded(p.K), p.ldc, p.alpha, p.beta, tiles_n);
+      auto *kernel = p.M <= 16 ? skinny_kernel<T, 1> : skinny_kernel<T, 2>;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(p.N, 16))),
+                         dim3(64 * kSkinnyWaves), 0, stream, p.ac, p.as, p.bc, p.bs,
+                         static_cast<typename Elem<T>::store *>(p.C), p.M, p.N, padded(p.K), p.ldc,
+                         p.alpha, p.beta);
     });
   }
   const int st = launched();
