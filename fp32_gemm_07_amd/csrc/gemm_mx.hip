@@ -93,11 +93,6 @@ bool row_launch(int rows, int KP, RowLaunch *l) {
   return blocks <= INT32_MAX;
 }
 
-// Whether the column kernels can take a stored matrix two neighbours at a time.
-bool pairs_fit(int rows, const void *mat, int ld, int type) {
-  return rows % 2 == 0 && ld % 2 == 0 && aligned(mat, 2 * elem_size(type));
-}
-
 // ---------------------------------------------------------------------------
 // Product.
 struct Product {
@@ -285,21 +280,15 @@ size_t moe_workspace(int tokens, int inter, int top_k, int type) {
 // Both kernels for groups of GROUP tokens.
 template <int TYPE, int GROUP>
 int launch_moe_groups(const MoeArgs &a, int cus, hipStream_t stream) {
-  // 16-byte loads of x: whole rows of 8 values
-  const bool vec = a.hidden % 8 == 0 && aligned(a.x, 16) && (static_cast<size_t>(a.ldx) * elem_size(TYPE)) % 16 == 0;
   const bool resident = static_cast<long long>(padded(a.hidden)) / 128 * Parts<TYPE>::x * GROUP * 256 <= kUpStage<GROUP>;
   const long long pairs = static_cast<long long>(a.tokens) * a.top_k;
   const long long groups = std::min<long long>(pairs, a.experts) + pairs / GROUP;
   const dim3 up(static_cast<unsigned>(std::min<long long>(groups * (padded(a.inter) / 16), cus)));
   const dim3 down(static_cast<unsigned>(ceil_div(a.hidden, 16)));
-  if (vec && resident)
-    hipLaunchKernelGGL((moe_up_kernel<TYPE, true, GROUP, true>), up, dim3(kMoeThreads), 0, stream, a);
-  else if (vec)
-    hipLaunchKernelGGL((moe_up_kernel<TYPE, true, GROUP, false>), up, dim3(kMoeThreads), 0, stream, a);
-  else if (resident)
-    hipLaunchKernelGGL((moe_up_kernel<TYPE, false, GROUP, true>), up, dim3(kMoeThreads), 0, stream, a);
+  if (resident)
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, GROUP, true>), up, dim3(kMoeThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((moe_up_kernel<TYPE, false, GROUP, false>), up, dim3(kMoeThreads), 0, stream, a);
+    hipLaunchKernelGGL((moe_up_kernel<TYPE, GROUP, false>), up, dim3(kMoeThreads), 0, stream, a);
   const int st = launched();
   if (st != GEMM_OK) return st;
   hipLaunchKernelGGL((moe_down_kernel<TYPE, GROUP>), down, dim3(64 * Parts<TYPE>::down_waves), 0, stream, a);
@@ -362,31 +351,21 @@ int gemm_mx_quantize(int trans, int rows, int K, const void *X, int x_type, int 
   const int KP = padded(K);
   const long long k_tiles = ceil_div(KP, kColK);
   RowLaunch l;
-  const long long col_blocks = ceil_div(rows, 64) * k_tiles;   // (half as many for pairs)
+  const long long col_blocks = ceil_div(rows, kColRows) * k_tiles;
   if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
-  const bool pairs = pairs_fit(rows, X, ldx, x_type);
-  const bool vec = aligned(X, 16) && (static_cast<size_t>(ldx) * elem_size(x_type)) % 16 == 0;
   unsigned *c = static_cast<unsigned *>(codes);
   with_type(x_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     const typename Elem<T>::store *x = static_cast<const typename Elem<T>::store *>(X);
-    if (trans && pairs)
-      hipLaunchKernelGGL((quantize_columns_kernel<T, 2>),
-                         dim3(static_cast<unsigned>(ceil_div(rows, 128) * k_tiles)),
+    if (trans)
+      hipLaunchKernelGGL(quantize_columns_kernel<T>, dim3(static_cast<unsigned>(col_blocks)),
                          dim3(kColThreads), 0, stream, x, ldx, c, static_cast<unsigned *>(scales),
                          rows, K, KP, static_cast<int>(k_tiles));
-    else if (trans)
-      hipLaunchKernelGGL((quantize_columns_kernel<T, 1>), dim3(static_cast<unsigned>(col_blocks)),
-                         dim3(kColThreads), 0, stream, x, ldx, c, static_cast<unsigned *>(scales),
-                         rows, K, KP, static_cast<int>(k_tiles));
-    else if (vec)
-      hipLaunchKernelGGL((quantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, x,
-                         ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
     else
-      hipLaunchKernelGGL((quantize_rows_kernel<T, false>), dim3(l.blocks), dim3(256), 0, stream, x,
+      hipLaunchKernelGGL(quantize_rows_kernel<T>, dim3(l.blocks), dim3(256), 0, stream, x,
                          ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
   });
   return launched();
@@ -399,32 +378,22 @@ int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void
   const int KP = padded(K);
   const long long k_tiles = ceil_div(KP, kColK);
   RowLaunch l;
-  const long long col_blocks = ceil_div(rows, 64) * k_tiles;   // (half as many for pairs)
+  const long long col_blocks = ceil_div(rows, kColRows) * k_tiles;
   if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
-  const bool pairs = pairs_fit(rows, Y, ldy, y_type);
-  const bool vec = aligned(Y, 16) && (static_cast<size_t>(ldy) * elem_size(y_type)) % 16 == 0;
   const unsigned *c = static_cast<const unsigned *>(codes);
   const unsigned char *s = static_cast<const unsigned char *>(scales);
   with_type(y_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     typename Elem<T>::store *y = static_cast<typename Elem<T>::store *>(Y);
-    if (trans && pairs)
-      hipLaunchKernelGGL((dequantize_columns_kernel<T, 2>),
-                         dim3(static_cast<unsigned>(ceil_div(rows, 128) * k_tiles)),
+    if (trans)
+      hipLaunchKernelGGL(dequantize_columns_kernel<T>, dim3(static_cast<unsigned>(col_blocks)),
                          dim3(kColThreads), 0, stream, c, s, y, ldy, rows, K, KP,
                          static_cast<int>(k_tiles));
-    else if (trans)
-      hipLaunchKernelGGL((dequantize_columns_kernel<T, 1>), dim3(static_cast<unsigned>(col_blocks)),
-                         dim3(kColThreads), 0, stream, c, s, y, ldy, rows, K, KP,
-                         static_cast<int>(k_tiles));
-    else if (vec)
-      hipLaunchKernelGGL((dequantize_rows_kernel<T, true>), dim3(l.blocks), dim3(256), 0, stream, c,
-                         s, y, ldy, rows, K, KP, l.map);
     else
-      hipLaunchKernelGGL((dequantize_rows_kernel<T, false>), dim3(l.blocks), dim3(256), 0, stream,
+      hipLaunchKernelGGL(dequantize_rows_kernel<T>, dim3(l.blocks), dim3(256), 0, stream,
                          c, s, y, ldy, rows, K, KP, l.map);
   });
   return launched();

@@ -56,21 +56,25 @@ struct Elem<kF16> {
   }
 };
 
-// 8 consecutive values from p (16-byte aligned for VEC), the first `n` of them
-// (VEC: n >= 8 reads them in 16-byte loads), zeros for the rest.
-template <int TYPE, bool VEC>
+// 16 bytes at any element's address: the memory system takes loads and stores that
+// are not aligned to their size.
+typedef uintx4 uintx4_any __attribute__((aligned(2)));
+
+// 8 consecutive values from p, the first `n` of them, zeros for the rest.
+template <int TYPE>
 __device__ inline void load8(const typename Elem<TYPE>::store *p, int n, float (&v)[8]) {
-  if (VEC && n >= 8) {
+  if (n >= 8) {
     if constexpr (TYPE == kF32) {
-      const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0];
-      const f32x4 b = reinterpret_cast<const f32x4 *>(p)[1];
+      const uintx4 a = reinterpret_cast<const uintx4_any *>(p)[0];
+      const uintx4 b = reinterpret_cast<const uintx4_any *>(p)[1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
+        const unsigned x = a[i], y = b[i];   // (the cast of a vector's element itself takes the first)
+        v[i] = __builtin_bit_cast(float, x);
+        v[4 + i] = __builtin_bit_cast(float, y);
       }
     } else {
-      const uintx4 a = reinterpret_cast<const uintx4 *>(p)[0];
+      const uintx4 a = *reinterpret_cast<const uintx4_any *>(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = Elem<TYPE>::get(static_cast<u16>(a[i]));
@@ -83,18 +87,24 @@ __device__ inline void load8(const typename Elem<TYPE>::store *p, int n, float (
   }
 }
 
-template <int TYPE, bool VEC>
+template <int TYPE>
 __device__ inline void store8(typename Elem<TYPE>::store *p, int n, const float (&v)[8]) {
-  if (VEC && n >= 8) {
+  if (n >= 8) {
     if constexpr (TYPE == kF32) {
-      reinterpret_cast<f32x4 *>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-      reinterpret_cast<f32x4 *>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+      uintx4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = __builtin_bit_cast(unsigned, v[i]);
+        b[i] = __builtin_bit_cast(unsigned, v[4 + i]);
+      }
+      reinterpret_cast<uintx4_any *>(p)[0] = a;
+      reinterpret_cast<uintx4_any *>(p)[1] = b;
     } else {
       uintx4 a;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         a[i] = Elem<TYPE>::put(v[2 * i]) | (static_cast<unsigned>(Elem<TYPE>::put(v[2 * i + 1])) << 16);
-      reinterpret_cast<uintx4 *>(p)[0] = a;
+      *reinterpret_cast<uintx4_any *>(p) = a;
     }
   } else {
 #pragma unroll
@@ -169,7 +179,7 @@ constexpr int kRowPasses = 4;
 // Quantisation along the stored rows. A block of 32 is 4 neighbouring lanes: the
 // maximum crosses them in two cross-lane steps, each lane writes its 4 bytes of
 // codes.
-template <int TYPE, bool VEC>
+template <int TYPE>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(
     const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
     unsigned char *__restrict__ scales, int rows, int K, int KP, RowMap map) {
@@ -185,7 +195,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
 #pragma unroll
   for (int p = 0; p < kRowPasses; ++p) {
     const long long row = row0 + p * rows_pass;
-    load8<TYPE, VEC>(X + row * ldx + k, row < rows ? K - k : 0, v[p]);
+    load8<TYPE>(X + row * ldx + k, row < rows ? K - k : 0, v[p]);
   }
 #pragma unroll
   for (int p = 0; p < kRowPasses; ++p) {
@@ -204,7 +214,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(
   }
 }
 
-template <int TYPE, bool VEC>
+template <int TYPE>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(
     const unsigned *__restrict__ codes, const unsigned char *__restrict__ scales,
     typename Elem<TYPE>::store *__restrict__ Y, int ldy, int rows, int K, int KP, RowMap map) {
@@ -229,34 +239,35 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(
     if (row >= rows) continue;
     float v[8];
     decode8(c[p], scale_value(s[p]), v);
-    store8<TYPE, VEC>(Y + row * ldy + k, K - k, v);
+    store8<TYPE>(Y + row * ldy + k, K - k, v);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Quantisation across the stored rows (the operand's rows are X's columns): a
-// workgroup of 8 waves takes 64 * VEC operand rows by 256 values of K, a wave
-// one block of 32 of each row. Lanes run along the stored rows, VEC = 2
-// neighbouring values a lane where their alignment allows it (256 bytes and more
-// a load), and a lane collects the 32 values of its blocks itself; the codes
-// pass through LDS so that each operand row is written in runs of 64 or 128
-// bytes.
+// workgroup of 8 waves takes 128 operand rows by 256 values of K, a wave one block
+// of 32 of each row. Lanes run along the stored rows, two neighbouring values a
+// lane (256 bytes and more a load), and a lane collects the 32 values of its two
+// blocks itself; the codes pass through LDS so that each operand row is
+// written in runs of 64 or 128 bytes.
 constexpr int kColWaves = 8;
 constexpr int kColThreads = 64 * kColWaves;
 constexpr int kColK = kColWaves * kBlock;   // values of K of a tile
 constexpr int kColStride = 36;              // LDS words of a row's 128 code bytes, padded
 
-// VEC neighbouring elements as loaded or to be stored.
-template <int TYPE, int VEC>
-struct __attribute__((aligned(sizeof(typename Elem<TYPE>::store) * VEC))) Neighbours {
-  typename Elem<TYPE>::store e[VEC];
+constexpr int kColRows = 128;               // operand rows of a tile
+
+// Two neighbouring elements as loaded or to be stored, at any element's address.
+template <int TYPE>
+struct Neighbours {
+  typename Elem<TYPE>::store e[2];
 };
 
-template <int TYPE, int VEC>
+template <int TYPE>
 __global__ __launch_bounds__(kColThreads) void quantize_columns_kernel(
     const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
     unsigned *__restrict__ scales, int rows, int K, int KP, int k_tiles) {
-  constexpr int kRows = 64 * VEC;
+  constexpr int VEC = 2, kRows = kColRows;
   __shared__ __attribute__((aligned(16))) unsigned tile[kRows * kColStride];
   __shared__ __attribute__((aligned(4))) unsigned char tile_scales[kRows * 8];
   const int rt = blockIdx.x / k_tiles;
@@ -264,19 +275,22 @@ __global__ __launch_bounds__(kColThreads) void quantize_columns_kernel(
   const long long r0 = static_cast<long long>(rt) * kRows;
   const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
   const int kb = k0 + b * kBlock;
-  const bool ok = r0 + lane * VEC < rows;   // VEC = 2: `rows` is even
+  const bool both = r0 + lane * VEC + 1 < rows, one = r0 + lane * VEC < rows;
   if (kb < KP) {
-    typedef Neighbours<TYPE, VEC> Pair;
+    typedef Neighbours<TYPE> Pair;
     const typename Elem<TYPE>::store *p = X + static_cast<long long>(kb) * ldx + r0 + lane * VEC;
     Pair raw[kBlock] = {};
-    if (ok && kb + kBlock <= K) {
+    if (both && kb + kBlock <= K) {
 #pragma unroll
       for (int i = 0; i < kBlock; ++i)
         raw[i] = *reinterpret_cast<const Pair *>(p + static_cast<long long>(i) * ldx);
-    } else if (ok) {
+    } else if (one) {
 #pragma unroll
       for (int i = 0; i < kBlock; ++i)
-        if (kb + i < K) raw[i] = *reinterpret_cast<const Pair *>(p + static_cast<long long>(i) * ldx);
+        if (kb + i < K) {
+          raw[i].e[0] = p[static_cast<long long>(i) * ldx];
+          if (both) raw[i].e[1] = p[static_cast<long long>(i) * ldx + 1];
+        }
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -315,11 +329,11 @@ __global__ __launch_bounds__(kColThreads) void quantize_columns_kernel(
 }
 
 // The way back, the same tiles.
-template <int TYPE, int VEC>
+template <int TYPE>
 __global__ __launch_bounds__(kColThreads) void dequantize_columns_kernel(
     const unsigned *__restrict__ codes, const unsigned char *__restrict__ scales,
     typename Elem<TYPE>::store *__restrict__ Y, int ldy, int rows, int K, int KP, int k_tiles) {
-  constexpr int kRows = 64 * VEC;
+  constexpr int VEC = 2, kRows = kColRows;
   __shared__ __attribute__((aligned(16))) unsigned tile[kRows * kColStride];
   const int rt = blockIdx.x / k_tiles;
   const int k0 = (blockIdx.x - rt * k_tiles) * kColK;
@@ -337,15 +351,16 @@ __global__ __launch_bounds__(kColThreads) void dequantize_columns_kernel(
   const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
   const int kb = k0 + b * kBlock;
   const long long row = r0 + lane * VEC;
-  if (row >= rows || kb >= K) return;   // VEC = 2: `rows` is even
+  if (row >= rows || kb >= K) return;
+  const bool both = row + 1 < rows;
   uintx4 c[VEC];
   float s[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     c[e] = *reinterpret_cast<const uintx4 *>(&tile[(lane * VEC + e) * kColStride + b * 4]);
-    s[e] = scale_value(scales[(row + e) * (KP / 32) + kb / 32]);
+    s[e] = scale_value(scales[min(row + e, rows - 1LL) * (KP / 32) + kb / 32]);
   }
-  typedef Neighbours<TYPE, VEC> Pair;
+  typedef Neighbours<TYPE> Pair;
   typename Elem<TYPE>::store *p = Y + static_cast<long long>(kb) * ldy + row;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -357,8 +372,12 @@ __global__ __launch_bounds__(kColThreads) void dequantize_columns_kernel(
       Pair out;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) out.e[e] = Elem<TYPE>::put(v[e][i]);
-      if (kb + 8 * q + i < K)
-        *reinterpret_cast<Pair *>(p + static_cast<long long>(8 * q + i) * ldy) = out;
+      if (kb + 8 * q + i < K) {
+        if (both)
+          *reinterpret_cast<Pair *>(p + static_cast<long long>(8 * q + i) * ldy) = out;
+        else
+          p[static_cast<long long>(8 * q + i) * ldy] = out.e[0];
+      }
     }
   }
 }

@@ -342,57 +342,19 @@ __device__ inline void in_turn(int n, F &even, F &odd, S &&step) {
   if (n) step(even, odd);
 }
 
-// 8 values of x as loaded, `left` of them in range (the rest zeros).
+// 8 values of x, `left` of them in range (the rest zeros), as bfloat16 parts.
 template <int TYPE>
-struct Raw8 {
-  uintx4 v[TYPE == kF32 ? 2 : 1];
-  // VEC: 16-byte aligned, and all or none of them in range; for none the row's
-  // last 8 are loaded (no branch among the loads), to be cleared before use.
-  template <bool VEC>
-  __device__ inline void load(const typename Elem<TYPE>::store *p, int left) {
-    constexpr int kRegs = TYPE == kF32 ? 2 : 1, kEach = 8 / kRegs;
-    if constexpr (VEC) {
-      const auto *q = reinterpret_cast<const uintx4 *>(left > 0 ? p : p - (8 - left));
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r) v[r] = q[r];
-    } else {
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r) {
-        uintx4 w = {};
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (r * kEach + i < left) {
-            if constexpr (TYPE == kF32)
-              w[i] = __builtin_bit_cast(unsigned, p[r * kEach + i]);
-            else
-              w[i / 2] |= static_cast<unsigned>(p[r * kEach + i]) << (16 * (i % 2));
-          }
-        v[r] = w;
-      }
-    }
+__device__ inline void load_parts(const typename Elem<TYPE>::store *p, int left,
+                                  bf16x8 (&out)[Parts<TYPE>::x]) {
+  if (TYPE == kBf16 && left >= 8) {
+    const uintx4 v = *reinterpret_cast<const uintx4_any *>(p);
+    out[0] = __builtin_bit_cast(bf16x8, v);
+  } else {
+    float v[8];
+    load8<TYPE>(p, left, v);
+    split8<Parts<TYPE>::x>(v, out);
   }
-  __device__ inline void clear() {
-#pragma unroll
-    for (int r = 0; r < (TYPE == kF32 ? 2 : 1); ++r) v[r] = uintx4{};
-  }
-  __device__ inline void parts(bf16x8 (&out)[Parts<TYPE>::x]) const {
-    if constexpr (TYPE == kBf16) {
-      out[0] = __builtin_bit_cast(bf16x8, v[0]);
-    } else {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (TYPE == kF32) {
-          const unsigned w = v[i / 4][i % 4];   // (the cast of a vector's element itself takes the first)
-          f[i] = __builtin_bit_cast(float, w);
-        } else {
-          f[i] = Elem<TYPE>::get(static_cast<u16>(v[0][i / 2] >> (16 * (i % 2))));
-        }
-      }
-      split8<Parts<TYPE>::x>(f, out);
-    }
-  }
-};
+}
 
 // The scale of chunk b (0 or 1) of two chunks' 4 scale bytes each, for lane group g.
 __device__ inline float pair_scale(const uintx2 &s, int b, int g) {
@@ -415,7 +377,7 @@ constexpr int kUpRed = 2 * kMoeWaves * 2 * 4 * GROUP * 16;   // partial sums, of
 template <int GROUP>
 constexpr int kUpStage = (kUpLds - kUpRed<GROUP> - static_cast<int>(sizeof(Routing))) / 1024 * 1024;
 
-template <int TYPE, bool VEC, int GROUP, bool RESIDENT>
+template <int TYPE, int GROUP, bool RESIDENT>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
@@ -495,19 +457,12 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
       if (c + b < chunks) {
         const int left = a.hidden - (c + b) * 128 - i16 * 8;
         unsigned char *stage = stage_of(batch, b);
-        Raw8<TYPE> v0, v1;
-        v0.template load<VEC>(x0 + (c + b) * 128, left);
-        if constexpr (GROUP > 4) v1.template load<VEC>(x1 + (c + b) * 128, left);
-        if (left <= 0) {
-          v0.clear();
-          if constexpr (GROUP > 4) v1.clear();
-        }
         bf16x8 parts[PX];
-        v0.parts(parts);
+        load_parts<TYPE>(x0 + (c + b) * 128, left, parts);
 #pragma unroll
         for (int p = 0; p < PX; ++p) stage_write<GROUP>(stage, p, g, i16, parts[p]);
         if constexpr (GROUP > 4) {
-          v1.parts(parts);
+          load_parts<TYPE>(x1 + (c + b) * 128, left, parts);
 #pragma unroll
           for (int p = 0; p < PX; ++p) stage_write<GROUP>(stage, p, 4 + g, i16, parts[p]);
         }
