@@ -178,7 +178,8 @@ constexpr int kRowPasses = 4;
 
 // Quantisation along the stored rows. A block of 32 is 4 neighbouring lanes: the
 // maximum crosses them in two cross-lane steps, each lane writes its 4 bytes of
-// codes.
+// codes. Bound by memory: 8192 x 8192 bfloat16 (134 MB in, 36 MB out) takes 42 us,
+// 4.1 TB/s where a large copy reaches 4.9.
 template <int TYPE>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(
     const typename Elem<TYPE>::store *__restrict__ X, int ldx, unsigned *__restrict__ codes,
@@ -249,7 +250,10 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(
 // of 32 of each row. Lanes run along the stored rows, two neighbouring values a
 // lane (256 bytes and more a load), and a lane collects the 32 values of its two
 // blocks itself; the codes pass through LDS so that each operand row is
-// written in runs of 64 or 128 bytes.
+// written in runs of 64 or 128 bytes. Bound by memory latency: all 32 loads of a
+// lane are in flight at once. 4097 x 4095 FP32 (67 MB in, 9 MB out) takes 28 us.
+// With one value a lane and 4 waves a tile, 4096 x 4096 bfloat16 took 36 us, so
+// 15.
 constexpr int kColWaves = 8;
 constexpr int kColThreads = 64 * kColWaves;
 constexpr int kColK = kColWaves * kBlock;   // values of K of a tile
@@ -399,8 +403,9 @@ __device__ inline intx8 widen(const intx4 v) { return intx8{v[0], v[1], v[2], v[
 // bytes, which are read once, straight from memory into registers: a workgroup
 // takes 16 rows of B (its instructions' rows; A's rows are the columns), its 8
 // waves share K, a wave taking kSkinnyAt neighbouring chunks of 128 at a time.
-// The waves' sums are added in order. At 1 x 4096 x 4096 (8.9 MB) it takes 4.4 us,
-// the tiled kernel with 4 splits and their sum 6.9 us.
+// The waves' sums are added in order. 1 x 4096 x 4096 (8.9 MB, other weights every
+// call) takes 4.7 us, half of it the launch; the tiled kernel with 4 splits and
+// their sum takes 2.2 us more.
 constexpr int kSkinnyWaves = 8, kSkinnyAt = 4;
 
 template <int TYPE, int MT>

@@ -26,6 +26,13 @@ namespace mx {
 //
 // Rows past M or N and stages past the K range are outside the copies' buffer
 // ranges and read as zeros (a zero scale byte is 2^-127, not NaN).
+//
+// 8192^3 with 256 x 256 tiles takes 305 us, 3.6 PFLOP/s. The instructions alone (no
+// reads, copies or stores) take 195 us on the same data: random operands draw so
+// much power that the chip's matrix rate falls from 8.7 to 6.3 PFLOP/s. Copies add
+// 70 us, LDS reads 33, the start and end of a tile about 10 of its 76.
+// Smaller tiles are bound by the latency of a stage (LDS reads and a barrier around
+// few instructions): 0.35 us a stage for 128 x 128, whether 4 or 8 stages are kept.
 // 16 bytes of C: alpha * sums + beta * C, or with RAW the sums.
 template <int TYPE, bool RAW>
 __device__ inline void store_vec(typename Elem<TYPE>::store *c, const float *s, float alpha, float beta) {
