@@ -112,20 +112,20 @@ struct ProductPlan {
 
 constexpr size_t kMaxWorkspace = size_t(64) << 20;
 
-// The time of a tile on one CU: us of a 128-value stage of K when it has the CU to
+// The time of a tile on one CU: us of a 128-value stretch of K when it has the CU to
 // itself, when it shares it (or follows others on it), and of its start and end.
 // Fitted on an MI355X over 20 shapes (M 1 .. 6000, K 128 .. 131072), where the
-// tiles take 47, 54, 55 and 90 us in this order at 4096^3 and 40, 29, 30 and
-// 45 us at 2048 x 4096 x 4096.
+// tiles take 43, 49, 46 and 75 us in this order at 4096^3 and 37, 27, 25 and
+// 39 us at 2048 x 4096 x 4096.
 struct TileCost {
   int bm, bn;
   double alone, shared, ends;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1.03, 1.03, 9.5},
-    {256, 128, 0.62, 0.62, 5.5},
-    {128, 128, 0.35, 0.38, 1.5},
-    {64, 64, 0.14, 0.165, 0.8},
+    {256, 256, 0.94, 0.94, 8.8},
+    {256, 128, 0.55, 0.55, 5.5},
+    {128, 128, 0.33, 0.31, 1.2},
+    {64, 64, 0.125, 0.12, 0.9},
 };
 // The sum of split partial sums: its launch, and bytes a us.
 constexpr double kSumUs = 3.0, kSumBytesPerUs = 4.5e6;
@@ -138,7 +138,8 @@ ProductPlan plan_product(int M, int N, int K, int cus) {
     const long long tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
     if (tiles > INT32_MAX) continue;
     for (int s = 1; s <= 64; s *= 2) {
-      const int chunk = static_cast<int>(ceil_div(ceil_div(KP, s), kAlign) * kAlign);
+      // ranges of whole stages of 256
+      const int chunk = s == 1 ? KP : static_cast<int>(ceil_div(ceil_div(KP, s), 256) * 256);
       const int splits = static_cast<int>(ceil_div(KP, chunk));
       const double partial = 4.0 * splits * M * static_cast<double>(N);
       if (s > 1 && (chunk < 512 || partial > kMaxWorkspace)) break;
@@ -168,17 +169,17 @@ size_t product_workspace(int M, int N, int K, int cus) {
   return plan.splits > 1 ? size_t(4) * plan.splits * M * N : 0;
 }
 
-template <int BM, int BN, int WPE>
+template <int BM, int BN, int NS, int WPE>
 void launch_tile(const Product &p, const ProductPlan &plan, void *ws, hipStream_t stream) {
   const long long tm = ceil_div(p.M, BM), tn = ceil_div(p.N, BN);
   TileArgs a{p.ac, p.as, p.bc, p.bs, plan.splits > 1 ? ws : p.C, p.M, p.N, padded(p.K), p.ldc,
              p.alpha, p.beta, plan.k_chunk, static_cast<int>(tm), static_cast<int>(tn), plan.splits};
   const dim3 grid(static_cast<unsigned>(tm * tn * plan.splits));
   if (plan.splits > 1)
-    hipLaunchKernelGGL((tile_kernel<BM, BN, kF32, true, WPE>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, NS, kF32, true, WPE>), grid, dim3(256), 0, stream, a);
   else
     with_type(p.type, [&](auto t) {
-      hipLaunchKernelGGL((tile_kernel<BM, BN, decltype(t)::value, false, WPE>), grid, dim3(256), 0,
+      hipLaunchKernelGGL((tile_kernel<BM, BN, NS, decltype(t)::value, false, WPE>), grid, dim3(256), 0,
                          stream, a);
     });
 }
@@ -189,10 +190,14 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
     plan.splits = 1;
     plan.k_chunk = padded(p.K);
   }
-  if (plan.bn == 256) launch_tile<256, 256, 1>(p, plan, ws, stream);
-  else if (plan.bm == 256) launch_tile<256, 128, 1>(p, plan, ws, stream);
-  else if (plan.bm == 128) launch_tile<128, 128, 2>(p, plan, ws, stream);
-  else if (plan.bm == 64) launch_tile<64, 64, 2>(p, plan, ws, stream);
+  if (plan.bn == 256) launch_tile<256, 256, 2, 1>(p, plan, ws, stream);
+  else if (plan.bm == 256) launch_tile<256, 128, 2, 1>(p, plan, ws, stream);
+  // Two workgroups of 128 x 128 share a CU; where there is one for each CU at most it
+  // takes twice the stages instead (512 x 512 x 131072: 34 us against 39).
+  else if (plan.bm == 128 && ceil_div(p.M, 128) * ceil_div(p.N, 128) * plan.splits <= cus)
+    launch_tile<128, 128, 4, 1>(p, plan, ws, stream);
+  else if (plan.bm == 128) launch_tile<128, 128, 2, 2>(p, plan, ws, stream);
+  else if (plan.bm == 64) launch_tile<64, 64, 4, 2>(p, plan, ws, stream);
   else {
     with_type(p.type, [&](auto t) {
       constexpr int T = decltype(t)::value;
