@@ -28,7 +28,7 @@ namespace mx {
 // Rows past M or N and stages past the K range are outside the copies' buffer
 // ranges and read as zeros (a zero scale byte is 2^-127, not NaN).
 //
-// 8192^3 with 256 x 256 tiles takes 284 us (3.9 PFLOP/s) to 299 on slower boxes. The
+// 8192^3 with 256 x 256 tiles takes 284 to 299 us from chip to chip (3.9 to 3.7 PFLOP/s). The
 // instructions alone (no reads, copies or stores) take 195 us on the same data:
 // random operands draw so much power that the chip's matrix rate falls from 8.7 to
 // 6.3 PFLOP/s. With stages of 128 values of K it took 305 us.

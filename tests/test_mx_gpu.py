@@ -608,3 +608,84 @@ def test_decoding_step():
     check_layer(host(y), x, logits.cpu().numpy(), q[0], q[1], I, k, True, "bf16")
     codes, scales = ref.quantize(host(y))
     check_product(host(out), (codes, scales), q[2], H, "bf16")
+
+
+# ---------------------------------------------------------------------------
+# Sizes and calls at the edge of what is allowed.
+
+def test_product_of_an_operand_with_itself_into_an_unaligned_c():
+    t = torch()
+    M, K = 150, 700
+    say("product X X^T, C one element off")
+    rng = np.random.default_rng(31)
+    a = operand(rng, M, K, 126, 128)
+    for kind in KINDS:
+        C = t.full((M * M + 2,), 7.0, dtype=dtype(kind), device="cuda:0")
+        lib.gemm_mx(M, M, K, 1.0, a[2], a[3], a[2], a[3], 0.0, C[1:], ref.TYPES[kind], M, None, 0, stream())
+        got = host(C)
+        assert got[0] == 7 and got[-1] == 7
+        check_product(got[1:-1].reshape(M, M), a, a, K, kind)
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (20, 24), (300, 260)])
+def test_product_of_the_longest_rows(M, N):
+    """K = 2^24: rows of 8 MiB of codes, a tile's offsets up to 2^31. Zero but for a
+    few blocks at the ends and in the middle, so that sums are exact."""
+    t = torch()
+    K = lib.GEMM_MX_MAX_K
+    say(f"product {M}x{N}x{K}")
+    rng = np.random.default_rng(32)
+    blocks = [0, 1, 5, K // 64 - 1, K // 64, K // 32 - 3, K // 32 - 1]
+    sides = []
+    for rows in (M, N):
+        c = t.zeros((rows, K // 2), dtype=t.uint8, device="cuda:0")
+        s = t.full((rows, K // 32), 127, dtype=t.uint8, device="cuda:0")
+        part = rng.integers(0, 256, (rows, len(blocks), 16), dtype=np.uint8)
+        for j, b in enumerate(blocks):
+            c[:, 16 * b:16 * b + 16] = bytes_dev(part[:, j])
+        packed = np.zeros((rows, ref.padded(32 * len(blocks)) // 2), np.uint8)
+        packed[:, :16 * len(blocks)] = part.reshape(rows, -1)
+        sides.append((c, s, ref.decode(packed, np.full((rows, packed.shape[1] // 16), 127, np.uint8), 32 * len(blocks))))
+    out = t.full((M, N), float("nan"), device="cuda:0")
+    lib.gemm_mx(M, N, K, 1.0, sides[0][0], sides[0][1], sides[1][0], sides[1][1], 0.0, out, ref.F32, N, None, 0, stream())
+    np.testing.assert_array_equal(host(out), (sides[0][2] @ sides[1][2].T).astype(np.float32))
+
+
+def test_product_with_more_outputs_than_32_bits_count():
+    t = torch()
+    M, N, K = 66001, 33001, 128
+    say(f"product {M}x{N}x{K} bf16")
+    rng = np.random.default_rng(33)
+    a, b = operand(rng, M, K, 126, 127), operand(rng, N, K, 126, 127)
+    C = t.full((M, N), float("nan"), dtype=t.bfloat16, device="cuda:0")
+    lib.gemm_mx(M, N, K, 1.0, a[2], a[3], b[2], b[3], 0.0, C, ref.BF16, N, None, 0, stream())
+    assert not t.isnan(C).any().item()
+    for rows in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 40, M)):
+        part = (a[0][rows], a[1][rows])
+        check_product(host(C[rows]), part, b, K, "bf16")
+
+
+def test_layer_at_its_limits():
+    """64 tokens on 16 of 512 experts; and weights past 2^32 bytes, the last expert
+    chosen."""
+    t = torch()
+    say("layer at its limits: tokens, experts, top_k")
+    for kind in KINDS:
+        x, logits, w1, w2 = layer_case(41, 64, 48, 20, 512, kind)
+        check_layer(run_layer(x, logits, w1, w2, 20, 16, True, kind), x, logits, w1, w2, 20, 16, True, kind)
+    H, I, E = 8192, 8192, 128
+    say(f"layer with {lib.gemm_mx_codes_bytes(E * 2 * I, H) >> 20} MiB of codes")
+    rng = np.random.default_rng(42)
+    one1, one2 = operand(rng, 2 * I, H, 119, 122), operand(rng, H, I, 119, 122)
+    full = []
+    for rows, one, k in ((2 * I, one1, H), (H, one2, I)):
+        c = t.zeros((E, rows, k // 2), dtype=t.uint8, device="cuda:0")
+        s = t.full((E, rows, k // 32), 120, dtype=t.uint8, device="cuda:0")
+        c[E - 1], s[E - 1] = one[2], one[3]
+        full += [c, s]
+    x = ref.to_type(rng.standard_normal((2, H)), ref.BF16)
+    logits = np.zeros((2, E), np.float32)
+    logits[:, E - 1] = 5.0
+    y = t.empty((2, H), dtype=t.bfloat16, device="cuda:0")
+    lib.gemm_mx_moe(2, H, I, E, 1, True, dev(logits), E, dev(x, "bf16"), ref.BF16, H, *full, y, H, None, 0, stream())
+    check_layer(host(y), x, np.zeros((2, 1), np.float32), one1, one2, I, 1, True, "bf16")
