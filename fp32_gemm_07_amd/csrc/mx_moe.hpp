@@ -23,6 +23,7 @@
 // parts cost nothing that shows.
 #pragma once
 
+#include "gemm_kernels.hpp"
 #include "mx_kernels.hpp"
 
 namespace gemm {
@@ -408,34 +409,62 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
   const long long plane = static_cast<long long>(a.tokens) * a.top_k * IP;
   const int items = num_groups * tiles;
   const int wgs = __builtin_amdgcn_readfirstlane(gridDim.x);
-  int item = static_cast<int>(static_cast<long long>(items) * blockIdx.x / wgs);
-  const int end = static_cast<int>(static_cast<long long>(items) * (blockIdx.x + 1) / wgs);
+  // Neighbouring runs on the workgroups of one XCD: where an expert has several
+  // groups, its weights are then read at much the same time through one L2 cache.
+  const int wg = xcd_order(blockIdx.x, wgs);
+  int item = static_cast<int>(static_cast<long long>(items) * wg / wgs);
+  const int end = static_cast<int>(static_cast<long long>(items) * (wg + 1) / wgs);
   if (item >= end) return;
 
+  // An item: its group and tile, the tile's rows that exist (`first`: of the last tile
+  // that has some, where row0 lies in the padding of `inter`) and where the gate
+  // rows' codes and scales begin. Items follow each other, so the next one's are
+  // a step away but for a change of group.
+  const int code_row = HP / 2, scale_row = HP / 32;
+  const unsigned char *scales_end = a.w1s + 2LL * a.experts * a.inter * scale_row;
+  const long long up_codes = static_cast<long long>(a.inter) * code_row;
+  const long long up_scales = static_cast<long long>(a.inter) * scale_row;
   struct Item {
-    int row0;
+    int gi, row0, first;
     Group group;
+    const unsigned char *codes, *scales;
   };
-  auto item_of = [&](int item) {
-    const int gi = item / tiles;
-    return Item{(item - gi * tiles) * 16, uniform(r.groups[gi])};
+  auto item_of = [&](int gi, int row0) __attribute__((always_inline)) {
+    Item t;
+    t.gi = gi;
+    t.row0 = row0;
+    t.first = min(row0, a.inter - 1) / 16 * 16;
+    t.group = uniform(r.groups[gi]);
+    const long long row = static_cast<long long>(t.group.expert()) * 2 * a.inter + t.first;
+    t.codes = a.w1c + row * code_row;
+    t.scales = a.w1s + row * scale_row;
+    return t;
+  };
+  auto after = [&](const Item &s) __attribute__((always_inline)) {
+    Item t = s;
+    t.row0 += 16;
+    if (t.row0 == IP) return item_of(s.gi + 1, 0);
+    if (t.row0 < a.inter) {
+      t.first = t.row0;
+      t.codes += 16 * code_row;
+      t.scales += 16 * scale_row;
+    }
+    return t;
   };
   struct Fetched {
     uintx4 gate[kAt], up[kAt];
     uintx2 gate_scale, up_scale;
   };
-  const long long rows = 2LL * a.experts * a.inter;
   auto fetch = [&](Fetched &f, const Item &t, int batch, bool wanted) __attribute__((always_inline)) {
     const int c = (batch * kMoeWaves + wave) * kAt;
     // rows past the expert's last: the last one again (their results are not kept)
-    const int first = min(t.row0, a.inter - 1), i = min(i16, a.inter - 1 - first);
-    const long long gate = static_cast<long long>(t.group.expert()) * 2 * a.inter + first, up = gate + a.inter;
-    const __amdgpu_buffer_rsrc_t gc = buffer(a.w1c + gate * (HP / 2), (rows - gate) * (HP / 2));
-    const __amdgpu_buffer_rsrc_t uc = buffer(a.w1c + up * (HP / 2), (rows - up) * (HP / 2));
-    const __amdgpu_buffer_rsrc_t gs = buffer(a.w1s + gate * (HP / 32), (rows - gate) * (HP / 32));
-    const __amdgpu_buffer_rsrc_t us = buffer(a.w1s + up * (HP / 32), (rows - up) * (HP / 32));
-    const unsigned code_off = wanted ? static_cast<unsigned>(i * (HP / 2) + g * 16) : 0;
-    const unsigned scale_off = wanted ? static_cast<unsigned>(i * (HP / 32)) : 0;
+    const int i = wanted ? min(i16, a.inter - 1 - t.first) : 0;
+    const __amdgpu_buffer_rsrc_t gc = buffer(t.codes, 0x7fffffff), uc = buffer(t.codes + up_codes, 0x7fffffff);
+    // (a pair of chunks' scales may reach past the operand's last)
+    const __amdgpu_buffer_rsrc_t gs = buffer(t.scales, scales_end - t.scales);
+    const __amdgpu_buffer_rsrc_t us = buffer(t.scales + up_scales, scales_end - t.scales - up_scales);
+    const unsigned code_off = static_cast<unsigned>(i * code_row + (wanted ? g * 16 : 0));
+    const unsigned scale_off = static_cast<unsigned>(i * scale_row);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       const int cb = min(c + b, chunks - 1);   // past the end: the last chunk again, not used
@@ -477,14 +506,15 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
 
   int batch = 0, turn = 0;
   bool fresh = true;   // the group's activations are not in LDS yet
-  Item now = item_of(item);
+  Item now = item_of(item / tiles, item % tiles * 16);
   f32x4 acc_gate = {}, acc_up = {};
   // One batch of an item from one set of registers, the next one's loads into the
   // other.
   auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
     const bool last = batch + 1 == batches;
     const bool more = !last || item + 1 < end;
-    const Item then = item_of(last && more ? item + 1 : item);
+    Item then = now;
+    if (last && more) then = after(now);
     // Also after the last one (then all lanes load the same bytes): a branch
     // around the loads would make the compiler wait for them at its end.
     fetch(next, then, last ? 0 : batch + 1, more);
@@ -601,7 +631,11 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
   const int row = min(i16, a.hidden - 1 - row0);
   const unsigned code_off = static_cast<unsigned>(row * (IP / 2) + g * 16);
   const unsigned scale_off = static_cast<unsigned>(row * (IP / 32));
-  const long long rows = static_cast<long long>(a.experts) * a.hidden;
+  const long long expert_codes = static_cast<long long>(a.hidden) * (IP / 2);
+  const long long expert_scales = static_cast<long long>(a.hidden) * (IP / 32);
+  const unsigned char *codes0 = a.w2c + static_cast<long long>(row0) * (IP / 2);
+  const unsigned char *scales0 = a.w2s + static_cast<long long>(row0) * (IP / 32);
+  const unsigned char *scales_end = a.w2s + a.experts * expert_scales;
 
   struct Fetched {
     uintx4 w[kAt];
@@ -609,9 +643,10 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
     uintx4 h[kAt][PH][kHalves];
   };
   auto fetch = [&](Fetched &f, const Group &now, int batch, bool wanted) __attribute__((always_inline)) {
-    const long long wr = static_cast<long long>(now.expert()) * a.hidden + row0;
-    const __amdgpu_buffer_rsrc_t codes = buffer(a.w2c + wr * (IP / 2), (rows - wr) * (IP / 2));
-    const __amdgpu_buffer_rsrc_t scales = buffer(a.w2s + wr * (IP / 32), (rows - wr) * (IP / 32));
+    const unsigned char *scale_rows = scales0 + now.expert() * expert_scales;
+    const __amdgpu_buffer_rsrc_t codes = buffer(codes0 + now.expert() * expert_codes, 0x7fffffff);
+    // (a pair of chunks' scales may reach past the operand's last)
+    const __amdgpu_buffer_rsrc_t scales = buffer(scale_rows, scales_end - scale_rows);
     const u16 *h = a.h + static_cast<long long>(now.base()) * IP;
     unsigned h_off[kHalves];   // (tokens past the group's last: the last one again)
 #pragma unroll
@@ -631,10 +666,9 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
   };
   int at = 0, batch = wave;   // the step: group and batch
   auto wrap = [&](int &to, int &bt) {
-    while (bt >= batches && to < num_groups) {
-      bt -= batches;
-      ++to;
-    }
+    if (bt < batches) return;
+    to += bt / batches;
+    bt %= batches;
   };
   wrap(at, batch);
   Group now = uniform(groups[1 + min(at, kMaxGroups - 1)]);
