@@ -372,7 +372,7 @@ __device__ inline float pair_scale(const uintx2 &s, int b, int g) {
 // next item where this one ends) are on their way meanwhile, in the other of
 // two sets of registers.
 // Bound by the weights' bytes: 32 tokens on 8 of 128 experts of 4096 x 1024 (0.49 GB
-// of G and U) take 134 us, 10 of them routing, so 4.0 TB/s. With activations
+// of G and U) take 123 us, 10 of them routing, so 4.3 TB/s. With activations
 // loaded anew for each item the vector memory pipe was the bound (155 us, as long
 // with the arithmetic left out).
 constexpr int kUpLds = 160 * 1024;
@@ -556,8 +556,9 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
       sums[wave * (8 * GROUP) + 4 * GROUP + at] = acc_up;
     }
     __syncthreads();
-    // One wave finishes the item, a lane for each output (the others, and the next
-    // barrier, wait for it: four outputs a lane took 0.6 us longer).
+    // One wave finishes the item, a lane for each output. The others wait for it at the
+    // next barrier: with four outputs a lane the layer above took 131 us, and with
+    // four outputs for each wave, which all of them then wait for, 128.
     if (wave == (turn & (kMoeWaves - 1))) {
       const float *s = reinterpret_cast<const float *>(sums);
 #pragma unroll
@@ -609,7 +610,7 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
 // step's weights and activations on their way. An instruction's columns are the
 // group's tokens, so a step's sums are then added to the wave's own sums of
 // those tokens, in LDS; at the end the waves' sums are added in order.
-// 32 tokens on 8 of 128 experts of 4096 x 1024 (0.25 GB of D) take 71 us, 3.5 TB/s;
+// 32 tokens on 8 of 128 experts of 4096 x 1024 (0.25 GB of D) take 69 us, 3.6 TB/s;
 // the activations, as many bytes for a workgroup as its weights, cost the rest.
 template <int TYPE, int GROUP>
 __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_waves / 4) void moe_down_kernel(
