@@ -277,8 +277,8 @@ int check_workspace(const void *workspace, size_t bytes, size_t need, std::initi
 constexpr size_t kGroupBytes = (kMaxGroups + 1) * sizeof(Group) / 16 * 16 + 16;   // the workspace's head
 
 size_t moe_workspace(int tokens, int inter, int top_k, int type) {
-  const size_t parts = type == kF32 ? Parts<kF32>::h : Parts<kBf16>::h;
-  const size_t hidden = parts * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
+  const size_t words = type == kF32 ? Parts<kF32>::h_words : Parts<kBf16>::h_words;
+  const size_t hidden = words * sizeof(u16) * static_cast<size_t>(tokens) * top_k * padded(inter);
   return hidden + kGroupBytes;
 }
 
@@ -292,7 +292,7 @@ int launch_moe_groups(const MoeArgs &a, int cus, hipStream_t stream) {
   hipLaunchKernelGGL((moe_up_kernel<TYPE, GROUP, RESIDENT>), up, dim3(kMoeThreads), 0, stream, a);
   const int st = launched();
   if (st != GEMM_OK) return st;
-  hipLaunchKernelGGL((moe_down_kernel<TYPE, GROUP>), down, dim3(64 * Parts<TYPE>::down_waves), 0, stream, a);
+  hipLaunchKernelGGL((moe_down_kernel<TYPE, GROUP>), down, dim3(64 * kDownWaves<TYPE>), 0, stream, a);
   return launched();
 }
 

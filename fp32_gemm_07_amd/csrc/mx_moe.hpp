@@ -16,11 +16,10 @@
 // group carries is free as long as both operands agree, so lane group g takes
 // block g of a row's 128 values.
 // Activations keep their precision by being split into bfloat16 parts
-// whose sum is exact: a bfloat16 is one part, a half two, a float three; the
-// hidden activations (FP32 sums) are kept in two parts (16 bits) where the
-// outputs are rounded to 16 bits or fewer, in three for FP32 outputs. The
+// whose sum is exact: a bfloat16 is one part, a half two, a float three, and so the
+// hidden activations, which are FP32 whatever the type of X and Y. The
 // matrix instructions are far from the bound (the weights' bytes), so the
-// parts cost nothing that shows.
+// parts cost little that shows.
 #pragma once
 
 #include "gemm_kernels.hpp"
@@ -39,10 +38,14 @@ constexpr int kMaxGroups = kMaxExperts + kMaxPairs / 4;
 template <int TYPE>
 struct Parts {
   static constexpr int x = TYPE == kF32 ? 3 : TYPE == kF16 ? 2 : 1;   // of the inputs
-  static constexpr int h = TYPE == kF32 ? 3 : 2;                      // of the hidden activations
-  // waves of the second kernel, by the registers that the parts in flight take
-  static constexpr int down_waves = TYPE == kF32 ? 8 : 16;
+  static constexpr int h = 3;                                         // of the hidden activations
+  // 16-bit words of a hidden activation in the workspace: its three parts, or the
+  // float, which the second kernel then splits.
+  static constexpr int h_words = TYPE == kF32 ? 3 : 2;
 };
+// Waves of the second kernel, by the registers that the activations in flight take.
+template <int TYPE>
+constexpr int kDownWaves = TYPE == kF32 ? 8 : 16;
 
 // Up to GROUP tokens of one expert: the expert, how many tokens, their first
 // pair and the tokens (a byte each, the first one again where there are fewer).
@@ -72,7 +75,8 @@ struct MoeArgs {
   const unsigned char *w1c, *w1s, *w2c, *w2s;
   void *y;
   int ldy;
-  u16 *h;       // workspace: Parts<TYPE>::h planes of (tokens * top_k) x IP bfloat16,
+  u16 *h;       // workspace: (tokens * top_k) x IP hidden activations, 3 planes of their
+                // bfloat16 parts (FP32 inputs) or floats,
   Group *groups;   // and what the second kernel needs of the routing
 };
 
@@ -94,6 +98,11 @@ struct RoutingScratch {
 template <int CTRL, int ROWS>
 __device__ inline int dpp(int identity, int v) {
   return __builtin_amdgcn_update_dpp(identity, v, CTRL, ROWS, 0xf, false);
+}
+// v of the lane N further on in its row of 16 (0 past the row).
+template <int N>
+__device__ inline float from_lane(float v) {
+  return __builtin_bit_cast(float, dpp<0x100 + N, 0xf>(0, __builtin_bit_cast(int, v)));
 }
 // op over the 16 lanes of a row (rotations by 1, 2, 4, 8), in every lane.
 template <class OP>
@@ -259,8 +268,10 @@ __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
 
 // 8 floats into PARTS bfloat16 vectors whose sum is exact for PARTS = 3 (and for
 // fewer bits accordingly): each part is what is left, cut off after its 8 bits.
-// Past an infinity nothing is left.
-template <int PARTS>
+// (Below 2^-110 the last part falls under bfloat16's smallest number: the sum is then
+// cut off to a multiple of 2^-133.) Past an infinity nothing is left, or without INF,
+// which saves two instructions a value and part, a NaN.
+template <int PARTS, bool INF = true>
 __device__ inline void split8(const float (&v)[8], bf16x8 (&out)[PARTS]) {
   float rest[8];
 #pragma unroll
@@ -272,7 +283,7 @@ __device__ inline void split8(const float (&v)[8], bf16x8 (&out)[PARTS]) {
     for (int i = 0; i < 4; ++i) {
       const unsigned a = __builtin_bit_cast(unsigned, rest[2 * i]);
       const unsigned b = __builtin_bit_cast(unsigned, rest[2 * i + 1]);
-      w[i] = (a >> 16) | (b & 0xffff0000u);
+      w[i] = __builtin_amdgcn_perm(b, a, 0x07060302);   // the high halves
     }
     out[p] = __builtin_bit_cast(bf16x8, w);
     if (p + 1 < PARTS) {
@@ -280,7 +291,7 @@ __device__ inline void split8(const float (&v)[8], bf16x8 (&out)[PARTS]) {
       for (int i = 0; i < 8; ++i) {
         const float part =
             __builtin_bit_cast(float, __builtin_bit_cast(unsigned, rest[i]) & 0xffff0000u);
-        rest[i] = __builtin_isinf(rest[i]) ? 0.0f : rest[i] - part;
+        rest[i] = INF && __builtin_isinf(rest[i]) ? 0.0f : rest[i] - part;
       }
     }
   }
@@ -298,17 +309,18 @@ __device__ inline bf16x8 weights8(unsigned codes, float scale) {
 // Activations on their way from memory to a matrix instruction. 128 values of up
 // to GROUP tokens are loaded with all lanes busy, lane (s, c) = (lane / 16,
 // lane % 16) taking values 8c .. 8c + 7 of token s (and of token 4 + s), and pass
-// through LDS, [part][token][16 pieces of 16 bytes], token t's piece c at c ^ t
-// so that the 8 lanes that read one piece of 8 tokens meet no bank twice.
-// Lane (g, n) of an instruction reads pieces 4g .. 4g + 3 of token n % GROUP.
+// through LDS, [part][token][16 pieces of 16 bytes], row r's piece c at c ^ r
+// so that the lanes that read one piece of several rows meet no bank twice.
+// Lane (g, n) of an instruction reads pieces 4g .. 4g + 3 of one row.
 template <int GROUP>
 __device__ inline void stage_write(unsigned char *stage, int part, int token, int piece, bf16x8 v) {
-  *reinterpret_cast<bf16x8 *>(stage + (part * GROUP + token) * 256 + ((piece ^ token) & 15) * 16) = v;
+  const int row = part * GROUP + token;
+  *reinterpret_cast<bf16x8 *>(stage + row * 256 + ((piece ^ row) & 15) * 16) = v;
 }
 template <int GROUP>
 __device__ inline bf16x8 stage_read(const unsigned char *stage, int part, int token, int piece) {
-  return *reinterpret_cast<const bf16x8 *>(stage + (part * GROUP + token) * 256 +
-                                           ((piece ^ token) & 15) * 16);
+  const int row = part * GROUP + token;
+  return *reinterpret_cast<const bf16x8 *>(stage + row * 256 + ((piece ^ row) & 15) * 16);
 }
 // Loads through a buffer resource: a uniform base and the bytes behind it (dwords
 // past them read as zero), a lane's offset and a uniform one.
@@ -385,7 +397,7 @@ constexpr int kUpStage = (kUpLds - kUpRed<GROUP> - static_cast<int>(sizeof(Routi
 template <int TYPE, int GROUP, bool RESIDENT>
 __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
-  constexpr int PX = Parts<TYPE>::x, PH = Parts<TYPE>::h;
+  constexpr int PX = Parts<TYPE>::x;
   constexpr int kAt = 2;   // chunks of a wave at a time
   constexpr int kChunkStage = PX * GROUP * 256;
   __shared__ Routing r;
@@ -581,13 +593,16 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
           // past the last row of an expert: the zeros that pad `inter`
           float rest = now.row0 + row < a.inter
                            ? gv[0] / (1.0f + expf(-gv[0])) * uv[0] * r.weight[p] : 0.0f;
-          u16 *h = a.h + static_cast<long long>(p) * IP + now.row0 + row;
+          const long long at_h = static_cast<long long>(p) * IP + now.row0 + row;
+          if constexpr (TYPE == kF32) {
 #pragma unroll
-          for (int q = 0; q < PH; ++q) {
-            const unsigned bits = __builtin_bit_cast(unsigned, rest);
-            const u16 part = q + 1 < PH || PH == 3 ? static_cast<u16>(bits >> 16) : Elem<kBf16>::put(rest);
-            h[q * plane] = part;
-            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
+            for (int q = 0; q < 3; ++q) {
+              const u16 part = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
+              a.h[q * plane + at_h] = part;
+              rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
+            }
+          } else {
+            reinterpret_cast<float *>(a.h)[at_h] = rest;
           }
         }
       }
@@ -607,18 +622,23 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
 
 // Y: a workgroup takes 16 rows of every reached expert's D. Its waves take the
 // steps (group of tokens, two neighbouring chunks of 128) in turn, the next
-// step's weights and activations on their way. An instruction's columns are the
-// group's tokens, so a step's sums are then added to the wave's own sums of
-// those tokens, in LDS; at the end the waves' sums are added in order.
+// step's weights and activations on their way. An instruction's columns are the three
+// parts of four tokens' activations (columns 4 part + token; the last four repeat
+// the third part): all parts at the price of one instruction and one read from
+// LDS, where a column for each token would take three. A step's sums over the
+// parts are added to the wave's own sums of those tokens, in LDS; at the end
+// the waves' sums are added in order. Where the first part's sum is not finite it is the
+// result: the other parts of an infinity are NaN.
 // 32 tokens on 8 of 128 experts of 4096 x 1024 (0.25 GB of D) take 69 us, 3.6 TB/s;
 // the activations, as many bytes for a workgroup as its weights, cost the rest.
 template <int TYPE, int GROUP>
-__global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_waves / 4) void moe_down_kernel(
+__global__ __launch_bounds__(64 * kDownWaves<TYPE>, kDownWaves<TYPE> / 4) void moe_down_kernel(
     MoeArgs a) {
   typedef typename Elem<TYPE>::store store;
-  constexpr int PH = Parts<TYPE>::h, W = Parts<TYPE>::down_waves, THREADS = 64 * W;
-  constexpr int kAt = 2, kHalves = GROUP / 4;
-  constexpr int kChunkStage = PH * GROUP * 256;
+  constexpr int PH = Parts<TYPE>::h, W = kDownWaves<TYPE>, THREADS = 64 * W;
+  constexpr int kLoads = Parts<TYPE>::h_words;   // of 16 bytes, for 8 hidden activations
+  constexpr int kAt = 2, kHalves = GROUP / 4;   // chunks at a time; fours of tokens
+  constexpr int kChunkStage = PH * 4 * 256;
   __shared__ Group groups[kMaxGroups + 1];
   __shared__ __attribute__((aligned(16))) unsigned char stages[W * kChunkStage];
   __shared__ __attribute__((aligned(16))) float sums[W * kMaxTokens * 16];   // [wave][token][row]
@@ -648,28 +668,31 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
   struct Fetched {
     uintx4 w[kAt];
     uintx2 scale;
-    uintx4 h[kAt][PH][kHalves];
+    uintx4 h[kAt][kLoads][kHalves];
   };
   auto fetch = [&](Fetched &f, const Group &now, int batch, bool wanted) __attribute__((always_inline)) {
     const unsigned char *scale_rows = scales0 + now.expert() * expert_scales;
     const __amdgpu_buffer_rsrc_t codes = buffer(codes0 + now.expert() * expert_codes, 0x7fffffff);
     // (a pair of chunks' scales may reach past the operand's last)
     const __amdgpu_buffer_rsrc_t scales = buffer(scale_rows, scales_end - scale_rows);
-    const u16 *h = a.h + static_cast<long long>(now.base()) * IP;
+    // of a plane's parts, or of the floats
+    constexpr int kBytes = TYPE == kF32 ? 2 : 4;
+    const unsigned char *h = reinterpret_cast<const unsigned char *>(a.h) + static_cast<long long>(now.base()) * IP * kBytes;
     unsigned h_off[kHalves];   // (tokens past the group's last: the last one again)
 #pragma unroll
     for (int s = 0; s < kHalves; ++s)
-      h_off[s] = static_cast<unsigned>(min(4 * s + g, now.count() - 1) * IP + i16 * 8);
+      h_off[s] = static_cast<unsigned>((min(4 * s + g, now.count() - 1) * IP + i16 * 8) * kBytes);
     f.scale = load8(scales, wanted ? scale_off : 0, min(batch * kAt, chunks - 1) * 4);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       const int c = min(batch * kAt + b, chunks - 1);   // past the end: not used
       f.w[b] = load16(codes, wanted ? code_off : 0, c * 64);
 #pragma unroll
-      for (int q = 0; q < PH; ++q)
+      for (int q = 0; q < kLoads; ++q)
 #pragma unroll
         for (int s = 0; s < kHalves; ++s)
-          f.h[b][q][s] = *reinterpret_cast<const uintx4 *>(h + q * plane + c * 128 + h_off[s]);
+          f.h[b][q][s] = load16(buffer(h + (TYPE == kF32 ? 2 * q * plane : 16 * q), 0x7fffffff), h_off[s],
+                                c * 128 * kBytes);
     }
   };
   int at = 0, batch = wave;   // the step: group and batch
@@ -687,35 +710,61 @@ __global__ __launch_bounds__(64 * Parts<TYPE>::down_waves, Parts<TYPE>::down_wav
     const Group then = uniform(groups[1 + (more ? next_at : at)]);
     fetch(next, then, more ? next_batch : batch, more);
     __builtin_amdgcn_sched_barrier(0);
-    f32x4 acc = {};
+    f32x4 acc[kHalves] = {};
     arrived(cur.scale);
 #pragma unroll
     for (int b = 0; b < kAt; ++b) {
       arrived(cur.w[b]);
-      wave_order();
 #pragma unroll
-      for (int q = 0; q < PH; ++q)
+      for (int q = 0; q < kLoads; ++q)
 #pragma unroll
-        for (int s = 0; s < kHalves; ++s) {
-          const uintx4 h = cur.h[b][q][s];
-          stage_write<GROUP>(stage, q, 4 * s + g, i16, __builtin_bit_cast(bf16x8, h));
-        }
-      wave_order();
+        for (int s = 0; s < kHalves; ++s) arrived(cur.h[b][q][s]);
       if (batch * kAt + b < chunks) {
         const float f = pair_scale(cur.scale, b, g);
+        bf16x8 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 v = weights8(cur.w[b][j], f);
+        for (int j = 0; j < 4; ++j) w[j] = weights8(cur.w[b][j], f);
 #pragma unroll
-          for (int q = 0; q < PH; ++q)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                v, stage_read<GROUP>(stage, q, i16 & (GROUP - 1), 4 * g + j), acc, 0, 0, 0);
+        for (int s = 0; s < kHalves; ++s) {
+          bf16x8 parts[PH];
+          if constexpr (TYPE == kF32) {
+#pragma unroll
+            for (int q = 0; q < PH; ++q) {
+              const uintx4 h = cur.h[b][q][s];
+              parts[q] = __builtin_bit_cast(bf16x8, h);
+            }
+          } else {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const unsigned h = cur.h[b][i / 4][s][i % 4];
+              v[i] = __builtin_bit_cast(float, h);
+            }
+            split8<PH, false>(v, parts);   // (the sums below look after infinities)
+          }
+          wave_order();
+#pragma unroll
+          for (int q = 0; q < PH; ++q) stage_write<4>(stage, q, g, i16, parts[q]);
+          wave_order();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                w[j], stage_read<4>(stage, min(i16 / 4, PH - 1), i16 & 3, 4 * g + j), acc[s], 0, 0, 0);
         }
       }
     }
-    if (i16 < now.count()) {
-      const unsigned t = ((i16 < 4 ? now.lo : now.hi) >> (8 * (i16 & 3))) & 255;
-      *reinterpret_cast<f32x4 *>(mine + t * 16 + g * 4) += acc;
+#pragma unroll
+    for (int s = 0; s < kHalves; ++s) {
+      f32x4 sum;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float first = acc[s][v], rest = from_lane<4>(first) + from_lane<8>(first);
+        sum[v] = __builtin_isfinite(first) ? first + rest : first;
+      }
+      if (i16 < 4 && 4 * s + i16 < now.count()) {
+        const unsigned t = ((s == 0 ? now.lo : now.hi) >> (8 * i16)) & 255;
+        *reinterpret_cast<f32x4 *>(mine + t * 16 + g * 4) += sum;
+      }
     }
     at = next_at;
     batch = next_batch;

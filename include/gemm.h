@@ -346,8 +346,9 @@ size_t gemm_mx_workspace_bytes(int M, int N, int K);
  * rows of `hidden` values: expert e's G_e (inter rows), then its U_e (inter
  * rows); W2 is one of experts * hidden rows of `inter` values (expert e's
  * D_e). X is tokens x hidden of x_type, row stride ldx; Y the same shape and
- * type, row stride ldy. Only the chosen experts' weights are read; sums are
- * FP32, in an order that depends on the sizes and the choice alone.
+ * type, row stride ldy. Only the chosen experts' weights are read; sums and the
+ * hidden activations w_e a_e are FP32, the sums in an order that depends on the
+ * sizes and the choice alone.
  * An expert whose logit is -inf is never chosen (a token with no other is
  * given zeros, one with fewer than top_k others gets those); a NaN or +inf
  * among a token's logits makes its row of Y NaN.
