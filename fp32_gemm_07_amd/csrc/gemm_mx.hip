@@ -47,6 +47,19 @@ int launched() {
   return e == hipSuccess ? GEMM_OK : gemm::host_fail(e);
 }
 
+// A launch takes fewer than 2^32 threads, so at most this many workgroups.
+constexpr long long max_blocks(long long threads) { return ((1LL << 32) - 1) / threads; }
+
+// launch(at, count), which returns a status, for successive ranges of at most `most`
+// of `total`.
+template <class F>
+int in_ranges(long long total, long long most, F &&launch) {
+  int st = GEMM_OK;
+  for (long long at = 0; at < total && st == GEMM_OK; at += most)
+    st = launch(at, static_cast<int>(std::min(most, total - at)));
+  return st;
+}
+
 // Calls f.template operator()<TYPE>() for a valid element type.
 template <class F>
 void with_type(int type, F &&f) {
@@ -79,19 +92,28 @@ int check_convert(int trans, int rows, int K, const void *mat, int type, int ld,
   return GEMM_OK;
 }
 
+// Workgroups of the kernels along rows, which take whole groups of group_rows rows.
 struct RowLaunch {
   RowMap map;
-  unsigned blocks;
+  long long group_rows;
+  dim3 grid(int rows) const { return dim3(static_cast<unsigned>(ceil_div(rows, group_rows) * map.col_groups)); }
+  // Rows of one launch.
+  long long most() const { return max_blocks(256) / map.col_groups * group_rows; }
 };
-bool row_launch(int rows, int KP, RowLaunch *l) {
+RowLaunch row_launch(int KP) {
   const int chunks = KP / 8;
   int log2 = 4;
   while (log2 < 8 && (1 << log2) < chunks) ++log2;
-  l->map = RowMap{log2, static_cast<int>(ceil_div(chunks, 1 << log2))};
-  const long long blocks = ceil_div(rows, (256 >> log2) * kRowPasses) * l->map.col_groups;
-  l->blocks = static_cast<unsigned>(blocks);
-  return blocks <= INT32_MAX;
+  return RowLaunch{RowMap{log2, static_cast<int>(ceil_div(chunks, 1 << log2))}, (256 >> log2) * kRowPasses};
 }
+
+// The same for the kernels across the stored rows.
+struct ColumnLaunch {
+  int k_tiles;
+  dim3 grid(int rows) const { return dim3(static_cast<unsigned>(ceil_div(rows, kColRows) * k_tiles)); }
+  long long most() const { return max_blocks(kColThreads) / k_tiles * kColRows; }
+};
+ColumnLaunch column_launch(int KP) { return ColumnLaunch{static_cast<int>(ceil_div(KP, kColK))}; }
 
 // ---------------------------------------------------------------------------
 // Product.
@@ -136,7 +158,6 @@ ProductPlan plan_product(int M, int N, int K, int cus) {
   double best_us = 1e30;
   for (const TileCost &c : kTiles) {
     const long long tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn);
-    if (tiles > INT32_MAX) continue;
     for (int s = 1; s <= 64; s *= 2) {
       // ranges of whole stages of 256
       const int chunk = s == 1 ? KP : static_cast<int>(ceil_div(ceil_div(KP, s), 256) * 256);
@@ -170,18 +191,32 @@ size_t product_workspace(int M, int N, int K, int cus) {
 }
 
 template <int BM, int BN, int NS, int WPE>
-void launch_tile(const Product &p, const ProductPlan &plan, void *ws, hipStream_t stream) {
-  const long long tm = ceil_div(p.M, BM), tn = ceil_div(p.N, BN);
-  TileArgs a{p.ac, p.as, p.bc, p.bs, plan.splits > 1 ? ws : p.C, p.M, p.N, padded(p.K), p.ldc,
-             p.alpha, p.beta, plan.k_chunk, static_cast<int>(tm), static_cast<int>(tn), plan.splits};
-  const dim3 grid(static_cast<unsigned>(tm * tn * plan.splits));
-  if (plan.splits > 1)
-    hipLaunchKernelGGL((tile_kernel<BM, BN, NS, kF32, true, WPE>), grid, dim3(256), 0, stream, a);
-  else
-    with_type(p.type, [&](auto t) {
-      hipLaunchKernelGGL((tile_kernel<BM, BN, NS, decltype(t)::value, false, WPE>), grid, dim3(256), 0,
-                         stream, a);
+int launch_tile(const Product &p, const ProductPlan &plan, void *ws, hipStream_t stream) {
+  const int KP = padded(p.K);
+  if (plan.splits > 1) {   // few tiles: the partial sums fit the workspace
+    const long long tm = ceil_div(p.M, BM), tn = ceil_div(p.N, BN);
+    const TileArgs a{p.ac, p.as, p.bc, p.bs, ws, p.M, p.N, KP, p.ldc, p.alpha, p.beta, plan.k_chunk,
+                     static_cast<int>(tm), static_cast<int>(tn), plan.splits};
+    hipLaunchKernelGGL((tile_kernel<BM, BN, NS, kF32, true, WPE>),
+                       dim3(static_cast<unsigned>(tm * tn * plan.splits)), dim3(256), 0, stream, a);
+    return launched();
+  }
+  // A launch takes as many columns of C as it can, and as many rows of those.
+  const long long wide = std::min(ceil_div(p.N, BN), max_blocks(256));
+  return in_ranges(p.N, wide * BN, [&](long long n0, int N) {
+    return in_ranges(p.M, max_blocks(256) / wide * BM, [&](long long m0, int M) {
+      const long long tm = ceil_div(M, BM), tn = ceil_div(N, BN);
+      const TileArgs a{p.ac + m0 * (KP / 2), p.as + m0 * (KP / 32), p.bc + n0 * (KP / 2), p.bs + n0 * (KP / 32),
+                       static_cast<char *>(p.C) + (m0 * p.ldc + n0) * static_cast<long long>(elem_size(p.type)),
+                       M, N, KP, p.ldc, p.alpha, p.beta, plan.k_chunk, static_cast<int>(tm),
+                       static_cast<int>(tn), 1};
+      with_type(p.type, [&](auto t) {
+        hipLaunchKernelGGL((tile_kernel<BM, BN, NS, decltype(t)::value, false, WPE>),
+                           dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, a);
+      });
+      return launched();
     });
+  });
 }
 
 int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
@@ -190,15 +225,17 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
     plan.splits = 1;
     plan.k_chunk = padded(p.K);
   }
-  if (plan.bn == 256) launch_tile<256, 256, 2, 1>(p, plan, ws, stream);
-  else if (plan.bm == 256) launch_tile<256, 128, 2, 1>(p, plan, ws, stream);
+  int st = GEMM_OK;
+  if (plan.bn == 256) st = launch_tile<256, 256, 2, 1>(p, plan, ws, stream);
+  else if (plan.bm == 256) st = launch_tile<256, 128, 2, 1>(p, plan, ws, stream);
   // Two workgroups of 128 x 128 share a CU; where there is one for each CU at most it
   // takes twice the stages instead (512 x 512 x 131072: 34 us against 39).
   else if (plan.bm == 128 && ceil_div(p.M, 128) * ceil_div(p.N, 128) * plan.splits <= cus)
-    launch_tile<128, 128, 4, 1>(p, plan, ws, stream);
-  else if (plan.bm == 128) launch_tile<128, 128, 2, 2>(p, plan, ws, stream);
-  else if (plan.bm == 64) launch_tile<64, 64, 4, 2>(p, plan, ws, stream);
+    st = launch_tile<128, 128, 4, 1>(p, plan, ws, stream);
+  else if (plan.bm == 128) st = launch_tile<128, 128, 2, 2>(p, plan, ws, stream);
+  else if (plan.bm == 64) st = launch_tile<64, 64, 4, 2>(p, plan, ws, stream);
   else {
+    // (One launch: with more workgroups than one takes a tile is always chosen above.)
     with_type(p.type, [&](auto t) {
       constexpr int T = decltype(t)::value;
       auto *kernel = p.M <= 16 ? skinny_kernel<T, 1> : skinny_kernel<T, 2>;
@@ -207,8 +244,8 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
                          static_cast<typename Elem<T>::store *>(p.C), p.M, p.N, padded(p.K), p.ldc,
                          p.alpha, p.beta);
     });
+    st = launched();
   }
-  const int st = launched();
   if (st != GEMM_OK || plan.splits == 1) return st;
   const long long count = static_cast<long long>(p.M) * p.N;
   const unsigned blocks = static_cast<unsigned>(std::min<long long>(ceil_div(count, 256), 8LL * cus));
@@ -360,55 +397,65 @@ int gemm_mx_quantize(int trans, int rows, int K, const void *X, int x_type, int 
                      void *scales, hipStream_t stream) {
   int st = check_convert(trans, rows, K, X, x_type, ldx, codes, scales, true);
   if (st != GEMM_OK || rows == 0 || K == 0) return st;
-  const int KP = padded(K);
-  const long long k_tiles = ceil_div(KP, kColK);
-  RowLaunch l;
-  const long long col_blocks = ceil_div(rows, kColRows) * k_tiles;
-  if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
-  unsigned *c = static_cast<unsigned *>(codes);
+  const int KP = padded(K);
   with_type(x_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     const typename Elem<T>::store *x = static_cast<const typename Elem<T>::store *>(X);
-    if (trans)
-      hipLaunchKernelGGL(quantize_columns_kernel<T>, dim3(static_cast<unsigned>(col_blocks)),
-                         dim3(kColThreads), 0, stream, x, ldx, c, static_cast<unsigned *>(scales),
-                         rows, K, KP, static_cast<int>(k_tiles));
-    else
-      hipLaunchKernelGGL(quantize_rows_kernel<T>, dim3(l.blocks), dim3(256), 0, stream, x,
-                         ldx, c, static_cast<unsigned char *>(scales), rows, K, KP, l.map);
+    // codes and scales of row r
+    auto c = [&](long long r) { return static_cast<unsigned *>(codes) + r * (KP / 8); };
+    auto s = [&](long long r) { return static_cast<unsigned char *>(scales) + r * (KP / 32); };
+    if (trans) {
+      const ColumnLaunch l = column_launch(KP);
+      st = in_ranges(rows, l.most(), [&](long long r, int n) {
+        hipLaunchKernelGGL(quantize_columns_kernel<T>, l.grid(n), dim3(kColThreads), 0, stream, x + r, ldx,
+                           c(r), reinterpret_cast<unsigned *>(s(r)), n, K, KP, l.k_tiles);
+        return launched();
+      });
+    } else {
+      const RowLaunch l = row_launch(KP);
+      st = in_ranges(rows, l.most(), [&](long long r, int n) {
+        hipLaunchKernelGGL(quantize_rows_kernel<T>, l.grid(n), dim3(256), 0, stream, x + r * ldx, ldx,
+                           c(r), s(r), n, K, KP, l.map);
+        return launched();
+      });
+    }
   });
-  return launched();
+  return st;
 }
 
 int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void *scales, void *Y,
                        int y_type, int ldy, hipStream_t stream) {
   int st = check_convert(trans, rows, K, Y, y_type, ldy, codes, scales, false);
   if (st != GEMM_OK || rows == 0 || K == 0) return st;
-  const int KP = padded(K);
-  const long long k_tiles = ceil_div(KP, kColK);
-  RowLaunch l;
-  const long long col_blocks = ceil_div(rows, kColRows) * k_tiles;
-  if (trans ? col_blocks > INT32_MAX : !row_launch(rows, KP, &l)) return GEMM_ERR_INVALID_DIM;
   int dev = 0, cus = 0;
   st = gemm::host_check_device(&dev, &cus);
   if (st != GEMM_OK) return st;
-  const unsigned *c = static_cast<const unsigned *>(codes);
-  const unsigned char *s = static_cast<const unsigned char *>(scales);
+  const int KP = padded(K);
   with_type(y_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     typename Elem<T>::store *y = static_cast<typename Elem<T>::store *>(Y);
-    if (trans)
-      hipLaunchKernelGGL(dequantize_columns_kernel<T>, dim3(static_cast<unsigned>(col_blocks)),
-                         dim3(kColThreads), 0, stream, c, s, y, ldy, rows, K, KP,
-                         static_cast<int>(k_tiles));
-    else
-      hipLaunchKernelGGL(dequantize_rows_kernel<T>, dim3(l.blocks), dim3(256), 0, stream,
-                         c, s, y, ldy, rows, K, KP, l.map);
+    auto c = [&](long long r) { return static_cast<const unsigned *>(codes) + r * (KP / 8); };
+    auto s = [&](long long r) { return static_cast<const unsigned char *>(scales) + r * (KP / 32); };
+    if (trans) {
+      const ColumnLaunch l = column_launch(KP);
+      st = in_ranges(rows, l.most(), [&](long long r, int n) {
+        hipLaunchKernelGGL(dequantize_columns_kernel<T>, l.grid(n), dim3(kColThreads), 0, stream, c(r), s(r),
+                           y + r, ldy, n, K, KP, l.k_tiles);
+        return launched();
+      });
+    } else {
+      const RowLaunch l = row_launch(KP);
+      st = in_ranges(rows, l.most(), [&](long long r, int n) {
+        hipLaunchKernelGGL(dequantize_rows_kernel<T>, l.grid(n), dim3(256), 0, stream, c(r), s(r),
+                           y + r * ldy, ldy, n, K, KP, l.map);
+        return launched();
+      });
+    }
   });
-  return launched();
+  return st;
 }
 
 size_t gemm_mx_workspace_bytes(int M, int N, int K) {

@@ -6,7 +6,7 @@ import pytest
 import mx_reference as ref
 from fp32_gemm_07_amd import binding as lib
 from gpu_util import say, torch
-from test_mx_gpu import KINDS, bytes_dev, run_layer
+from test_mx_gpu import KINDS, bytes_dev, run_layer, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,84 @@ def test_layer_infinite_hidden_activations(kind, T):
     np.testing.assert_array_equal(got[hot][np.isinf(want[hot])], want[hot][np.isinf(want[hot])])
     rest = np.arange(T) != hot
     assert np.isfinite(got[rest]).all() if kind != "f16" else not np.isnan(got[rest]).any()
+
+
+# ---------------------------------------------------------------------------
+# More workgroups than one launch takes (2^32 threads).
+
+@pytest.fixture
+def room():
+    """The card's memory without what earlier tests left in torch's pool, and given back."""
+    t = torch()
+    t.cuda.empty_cache()
+    yield
+    t.cuda.synchronize()
+    t.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("trans", [False, True], ids=["rows", "columns"])
+def test_conversion_of_more_rows_than_a_launch_takes(trans, room):
+    """2^30 + 130 rows of one value (64 rows of it are a workgroup, 128 down columns):
+    1 to 7 by row, which stand for 1, 2, 3, 4, 4 (a tie, to the even code), 6 and 6."""
+    t = torch()
+    rows = (1 << 30) + 130
+    say(f"conversion of {rows} rows, trans {trans}")
+    x = (t.arange(rows, dtype=t.int32, device="cuda:0") % 7 + 1).to(t.bfloat16)
+    c = t.full((lib.gemm_mx_codes_bytes(rows, 1),), 0xA5, dtype=t.uint8, device="cuda:0")
+    s = t.full((lib.gemm_mx_scales_bytes(rows, 1),), 0xA5, dtype=t.uint8, device="cuda:0")
+    ld = rows if trans else 1
+    lib.gemm_mx_quantize(trans, rows, 1, x, ref.BF16, ld, c, s, stream())
+    codes, scales = ref.quantize(np.arange(1.0, 8.0)[:, None])
+    for first in (0, (1 << 29) - 70, (1 << 30) - 150, rows - 140):   # whole periods of 7 rows
+        first -= first % 7
+        n = min(140, rows - first)
+        got_c = c.view(rows, 64)[first:first + n].cpu().numpy()
+        got_s = s.view(rows, 4)[first:first + n].cpu().numpy()
+        np.testing.assert_array_equal(got_c, codes[np.arange(n) % 7])
+        np.testing.assert_array_equal(got_s, scales[np.arange(n) % 7])
+    y = t.full((rows,), float("nan"), dtype=t.bfloat16, device="cuda:0")
+    lib.gemm_mx_dequantize(trans, rows, 1, c, s, y, ref.BF16, ld, stream())
+    del c, s
+    stands_for = t.tensor([1, 2, 3, 4, 4, 6, 6], dtype=t.bfloat16, device="cuda:0")
+    step = 7 << 24
+    for first in range(0, rows, step):
+        n = min(step, rows - first)
+        want = stands_for.repeat(-(-n // 7))[:n]
+        assert t.equal(y[first:first + n], want), first
+
+
+def test_product_of_more_tiles_than_a_launch_takes(room):
+    """2^31 - 1 rows of A by one of B: 2^24 tiles of 128 x 128, one more than a launch
+    of 256 threads each takes. Every row's value has its own code."""
+    t = torch()
+    M = (1 << 31) - 1
+    say(f"product {M}x1x1")
+    c = t.zeros((M, 64), dtype=t.uint8, device="cuda:0")
+    s = t.full((M, 4), 127, dtype=t.uint8, device="cuda:0")
+    step = 1 << 27
+    for first in range(0, M, step):
+        n = min(step, M - first)
+        c[first:first + n, 0] = (t.arange(first, first + n, dtype=t.int64, device="cuda:0") % 16).to(t.uint8)
+    b = packed(np.full((1, 128), 1.0) * (np.arange(128) == 0), np.full((1, 4), 128))
+    out = t.full((M,), float("nan"), dtype=t.bfloat16, device="cuda:0")
+    lib.gemm_mx(M, 1, 1, 1.0, c, s, b[2], b[3], 0.0, out, ref.BF16, 1, None, 0, stream())
+    table = t.tensor(np.concatenate((2 * ref.E2M1, -2 * ref.E2M1)), dtype=t.bfloat16, device="cuda:0")
+    for first in range(0, M, step):
+        n = min(step, M - first)
+        assert t.equal(out[first:first + n], table.repeat(n // 16 + 1)[:n]), first
+
+
+def test_product_of_more_columns_than_a_launch_takes(room):
+    """The same with the operands exchanged: the columns of C in two launches."""
+    t = torch()
+    N = (1 << 31) - 1
+    say(f"product 3x{N}x1")
+    c = t.zeros((N, 64), dtype=t.uint8, device="cuda:0")
+    s = t.full((N, 4), 127, dtype=t.uint8, device="cuda:0")
+    c[:, 0] = 2                      # 1.0, and the last tile 6.0
+    c[N - 100:, 0] = 7
+    a = packed(np.array([[1.0], [-2.0], [0.5]]) * (np.arange(128) == 0), np.full((3, 4), 127))
+    out = t.full((3, N), float("nan"), dtype=t.bfloat16, device="cuda:0")
+    lib.gemm_mx(3, N, 1, 1.0, a[2], a[3], c, s, 0.0, out, ref.BF16, N, None, 0, stream())
+    for row, v in enumerate((1.0, -2.0, 0.5)):
+        assert (out[row, :N - 100] == v).all().item() and (out[row, N - 100:] == 6 * v).all().item()
