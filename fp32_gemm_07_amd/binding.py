@@ -104,7 +104,7 @@ EXPORTS = (
     "gemm_f32_ex", "gemm_f32_plan", "gemm_f32_plan_cus",
     "gemm_f32_plan_workspace_bytes", "gemm_f32_with_plan", "gemm_f32_general",
     "gemm_f32_general_workspace_bytes", "gemm_mx_codes_bytes", "gemm_mx_scales_bytes",
-    "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_workspace_bytes",
+    "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_workspace_bytes", "gemm_mx_plan",
     "gemm_mx_moe", "gemm_mx_moe_workspace_bytes", "gemm_kernel_name", "gemm_status_string",
     "gemm_last_hip_error",
 )
@@ -126,6 +126,15 @@ class gemm_plan_t(ctypes.Structure):
     def __repr__(self):
         return (f"gemm_plan_t(kernel={gemm_kernel_name(self.kernel)}, split_k={self.split_k}, "
                 f"k_chunk={self.k_chunk}, split_tail={self.split_tail})")
+
+
+class gemm_mx_plan_t(ctypes.Structure):
+    _fields_ = [("tile_m", ctypes.c_int), ("tile_n", ctypes.c_int), ("stages", ctypes.c_int),
+                ("split_k", ctypes.c_int), ("k_chunk", ctypes.c_int)]
+
+    def __repr__(self):
+        return (f"gemm_mx_plan_t(tile_m={self.tile_m}, tile_n={self.tile_n}, stages={self.stages}, "
+                f"split_k={self.split_k}, k_chunk={self.k_chunk})")
 
 
 _lib = None
@@ -199,6 +208,8 @@ def load():
         lib.gemm_mx.restype = i
         lib.gemm_mx_workspace_bytes.argtypes = [i, i, i]
         lib.gemm_mx_workspace_bytes.restype = sz
+        lib.gemm_mx_plan.argtypes = [i, i, i, ctypes.POINTER(gemm_mx_plan_t)]
+        lib.gemm_mx_plan.restype = i
         lib.gemm_mx_moe.argtypes = [i, i, i, i, i, i, vp, i, vp, i, i, vp, vp, vp, vp, vp, i, vp,
                                     sz, vp]
         lib.gemm_mx_moe.restype = i
@@ -328,6 +339,12 @@ def gemm_mx(M: int, N: int, K: int, alpha: float, A_codes, A_scales, B_codes, B_
 
 def gemm_mx_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(load().gemm_mx_workspace_bytes(M, N, K))
+
+
+def gemm_mx_plan(M: int, N: int, K: int) -> gemm_mx_plan_t:
+    p = gemm_mx_plan_t()
+    _check(load().gemm_mx_plan(M, N, K, ctypes.byref(p)), "gemm_mx_plan")
+    return p
 
 
 def gemm_mx_moe(tokens: int, hidden: int, inter: int, experts: int, top_k: int, renormalize: bool,

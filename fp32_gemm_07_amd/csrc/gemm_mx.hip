@@ -125,10 +125,10 @@ struct Product {
   int type, ldc;
 };
 
-// How a product is computed: tiles of bm x bn, or with bm = 0 the kernel for few
-// rows of A; K cut into `splits` ranges of k_chunk.
+// How a product is computed: tiles of bm x bn through a ring of `stages`, or with no
+// stages the kernel for few rows of A; K cut into `splits` ranges of k_chunk.
 struct ProductPlan {
-  int bm, bn;
+  int bm, bn, stages;
   int splits, k_chunk;
 };
 
@@ -169,7 +169,10 @@ ProductPlan plan_product(int M, int N, int K, int cus) {
       if (splits > 1) us += kSumUs + 2 * partial / kSumBytesPerUs;
       if (us < best_us * 0.99) {
         best_us = us;
-        best = ProductPlan{c.bm, c.bn, splits, chunk};
+        // Two workgroups of 128 x 128 share a CU; where there is one for each CU at most
+        // it takes twice the stages instead (512 x 512 x 131072: 34 us against 39).
+        const int stages = c.bm == 64 || (c.bm == 128 && tiles * splits <= cus) ? 4 : 2;
+        best = ProductPlan{c.bm, c.bn, stages, splits, chunk};
       }
     }
   }
@@ -180,7 +183,7 @@ ProductPlan plan_product(int M, int N, int K, int cus) {
   if (M <= 32) {
     const long long rounds = ceil_div(ceil_div(N, 16), cus);
     const double us = rounds * ceil_div(KP / kAlign, kSkinnyWaves * kSkinnyAt) * (M <= 16 ? 2.2 : 4.5) - 0.3;
-    if (us < best_us) best = ProductPlan{0, 0, 1, KP};
+    if (us < best_us) best = ProductPlan{M <= 16 ? 16 : 32, 16, 0, 1, KP};
   }
   return best;
 }
@@ -228,17 +231,14 @@ int launch_product(const Product &p, void *ws, int cus, hipStream_t stream) {
   int st = GEMM_OK;
   if (plan.bn == 256) st = launch_tile<256, 256, 2, 1>(p, plan, ws, stream);
   else if (plan.bm == 256) st = launch_tile<256, 128, 2, 1>(p, plan, ws, stream);
-  // Two workgroups of 128 x 128 share a CU; where there is one for each CU at most it
-  // takes twice the stages instead (512 x 512 x 131072: 34 us against 39).
-  else if (plan.bm == 128 && ceil_div(p.M, 128) * ceil_div(p.N, 128) * plan.splits <= cus)
-    st = launch_tile<128, 128, 4, 1>(p, plan, ws, stream);
+  else if (plan.bm == 128 && plan.stages == 4) st = launch_tile<128, 128, 4, 1>(p, plan, ws, stream);
   else if (plan.bm == 128) st = launch_tile<128, 128, 2, 2>(p, plan, ws, stream);
   else if (plan.bm == 64) st = launch_tile<64, 64, 4, 2>(p, plan, ws, stream);
   else {
     // (One launch: with more workgroups than one takes a tile is always chosen above.)
     with_type(p.type, [&](auto t) {
       constexpr int T = decltype(t)::value;
-      auto *kernel = p.M <= 16 ? skinny_kernel<T, 1> : skinny_kernel<T, 2>;
+      auto *kernel = plan.bm == 16 ? skinny_kernel<T, 1> : skinny_kernel<T, 2>;
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(p.N, 16))),
                          dim3(64 * kSkinnyWaves), 0, stream, p.ac, p.as, p.bc, p.bs,
                          static_cast<typename Elem<T>::store *>(p.C), p.M, p.N, padded(p.K), p.ldc,
@@ -461,6 +461,14 @@ int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void
 size_t gemm_mx_workspace_bytes(int M, int N, int K) {
   if (M <= 0 || N <= 0 || K <= 0 || !valid_operand(M, K) || !valid_operand(N, K)) return 0;
   return product_workspace(M, N, K, gemm::host_planning_cus());
+}
+
+int gemm_mx_plan(int M, int N, int K, gemm_mx_plan_t *out) {
+  if (!out) return GEMM_ERR_NULL_PTR;
+  if (M < 1 || N < 1 || K < 1 || !valid_operand(M, K) || !valid_operand(N, K)) return GEMM_ERR_INVALID_DIM;
+  const ProductPlan plan = plan_product(M, N, K, gemm::host_planning_cus());
+  *out = gemm_mx_plan_t{plan.bm, plan.bn, plan.stages, plan.splits, plan.k_chunk};
+  return GEMM_OK;
 }
 
 int gemm_mx(int M, int N, int K, float alpha, const void *A_codes, const void *A_scales,

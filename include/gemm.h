@@ -336,6 +336,22 @@ int gemm_mx(int M, int N, int K, float alpha, const void *A_codes, const void *A
  * needs none, or for invalid arguments). */
 size_t gemm_mx_workspace_bytes(int M, int N, int K);
 
+/* How gemm_mx computes a product: the block of C that a workgroup makes, the LDS
+ * stages (256 values of K each) its operands pass through (0: the kernel for few
+ * rows of A, which reads them straight into registers), and the ranges of
+ * k_chunk values that K is cut into. */
+typedef struct gemm_mx_plan {
+  int tile_m, tile_n;
+  int stages;
+  int split_k;
+  int k_chunk;
+} gemm_mx_plan_t;
+
+/* The plan for (M, N, K), each at least 1, on the current device, written to
+ * *plan. Returns a status code. (Where gemm_mx can get no workspace from the
+ * library, the same tile runs with K whole.) */
+int gemm_mx_plan(int M, int N, int K, gemm_mx_plan_t *plan);
+
 /* A mixture-of-experts layer for a few tokens, in two kernels. For token t, with
  * the router's logits l (FP32, tokens x experts, row stride ld_logits; the
  * product of the tokens and the router's weights, e.g. by gemm_f32):

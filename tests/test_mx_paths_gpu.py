@@ -6,7 +6,8 @@ import pytest
 import mx_reference as ref
 from fp32_gemm_07_amd import binding as lib
 from gpu_util import say, torch
-from test_mx_gpu import KINDS, bytes_dev, run_layer, stream
+from mx_plans import IDS, PLANS, is_plan
+from test_mx_gpu import KINDS, bytes_dev, dtype, operand, run_layer, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -187,3 +188,93 @@ def test_product_of_more_columns_than_a_launch_takes(room):
     lib.gemm_mx(3, N, 1, 1.0, a[2], a[3], c, s, 0.0, out, ref.BF16, N, None, 0, stream())
     for row, v in enumerate((1.0, -2.0, 0.5)):
         assert (out[row, :N - 100] == v).all().item() and (out[row, N - 100:] == 6 * v).all().item()
+
+
+# ---------------------------------------------------------------------------
+# The product through every kernel it chooses between.
+
+def decode_on_device(codes, scales, K):
+    """An operand as float64 on the device (exact)."""
+    t = torch()
+    table = t.tensor(np.concatenate((ref.E2M1, -ref.E2M1)), dtype=t.float64, device="cuda:0")
+    v = t.stack((table[(codes & 15).long()], table[(codes >> 4).long()]), dim=-1).view(*scales.shape, 32)
+    powers = t.tensor([2.0 ** (n - 127) for n in range(255)] + [float("nan")], dtype=t.float64, device="cuda:0")
+    v *= powers[scales.long()][..., None]
+    return v.view(codes.shape[0], -1)[:, :K].contiguous()
+
+
+@pytest.mark.parametrize("M,N,K,tile,split", PLANS, ids=IDS)
+def test_product_through_every_kernel(M, N, K, tile, split):
+    """Bit for bit in every type, with alpha, beta and row strides, aligned and not. Scales
+    within a factor of 4 of each other: products are multiples of 2^-4, with a root mean
+    square of 15 under random signs, so that sums stay below 100 sqrt(K) 15 < 2^20 and FP32
+    sums of them are exact in any order; so are the powers of two alpha and beta with
+    whole numbers in C, and one rounding to the type is left."""
+    t = torch()
+    plan = lib.gemm_mx_plan(M, N, K)
+    say(f"product {M}x{N}x{K}: {plan}")
+    assert is_plan(plan, tile, split), "other sizes are needed to reach this kernel"
+    rng = np.random.default_rng(M + N + K)
+    a, b = operand(rng, M, K, 126, 128), operand(rng, N, K, 126, 128)
+    s = decode_on_device(a[2], a[3], K) @ decode_on_device(b[2], b[3], K).t().contiguous()
+    assert s.abs().max().item() < 2 ** 20
+    need = lib.gemm_mx_workspace_bytes(M, N, K)
+    ws = t.full((max(need, 16),), 0xff, dtype=t.uint8, device="cuda:0")
+    c0 = t.randint(-99, 100, (M, N), device="cuda:0")
+    for kind in KINDS:
+        # alpha small enough for half's range; strides of 16 bytes, and odd ones one element off
+        for alpha, beta, ldc, off in ((0.125, 0.0, N + -N % 8, 0), (-0.25, 0.5, N + -N % 8 + 8, 0),
+                                      (0.0625, -2.0, N + 1 + N % 2, 1)):
+            C = t.full((off + M * ldc + 8,), 7.0, dtype=dtype(kind), device="cuda:0")
+            view = C[off:off + M * ldc].view(M, ldc)
+            view[:, :N] = c0.to(dtype(kind)) if beta else float("nan")
+            lib.gemm_mx(M, N, K, alpha, a[2], a[3], b[2], b[3], beta, C[off:], ref.TYPES[kind], ldc, ws, need, stream())
+            want = (alpha * s + beta * c0).float().to(dtype(kind))
+            assert t.equal(view[:, :N], want), (kind, alpha, (view[:, :N] != want).sum().item())
+            assert (view[:, N:] == 7).all().item() and (C[off + M * ldc:] == 7).all().item() and (C[:off] == 7).all().item()
+    # a NaN block in the last stretch of a row of A and in the first of B's last row
+    a[3][M // 2, -(-K // 32) - 1] = 255
+    b[3][N - 1, 0] = 255
+    out = t.zeros((M, N), device="cuda:0")
+    lib.gemm_mx(M, N, K, 1.0, a[2], a[3], b[2], b[3], 0.0, out, ref.F32, N, ws, need, stream())
+    want = s.float()
+    want[M // 2], want[:, N - 1] = float("nan"), float("nan")
+    assert t.equal(t.isnan(out), t.isnan(want)) and t.equal(out.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("M,N,K,tile,split", [PLANS[n] for n in (1, 6, 10, 16, 21, 24, 27)],
+                         ids=[IDS[n] for n in (1, 6, 10, 16, 21, 24, 27)])
+def test_product_kernels_captured_and_on_streams(M, N, K, tile, split):
+    """Replays of a captured call with operands changed between them, and calls on three
+    streams at once with the library's workspace, all against the exact product."""
+    t = torch()
+    say(f"product {M}x{N}x{K} captured and on streams")
+    assert is_plan(lib.gemm_mx_plan(M, N, K), tile, split)
+    rng = np.random.default_rng(M * N + K)
+    a, bs = operand(rng, M, K, 126, 128), [operand(rng, N, K, 126, 128) for _ in range(2)]
+    av = decode_on_device(a[2], a[3], K)
+    want = [(av @ decode_on_device(b[2], b[3], K).t().contiguous()).float() for b in bs]
+    del av
+    need = lib.gemm_mx_workspace_bytes(M, N, K)
+    ws = t.empty(max(need, 16), dtype=t.uint8, device="cuda:0")
+    bc, bsc, out = bs[0][2].clone(), bs[0][3].clone(), t.zeros((M, N), device="cuda:0")
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        lib.gemm_mx(M, N, K, 1.0, a[2], a[3], bc, bsc, 0.0, out, ref.F32, N, ws, need, stream())
+    for n in range(4):
+        bc.copy_(bs[n % 2][2])
+        bsc.copy_(bs[n % 2][3])
+        out.fill_(float("nan"))
+        g.replay()
+        t.cuda.synchronize()
+        assert t.equal(out, want[n % 2]), n
+    streams = [t.cuda.Stream() for _ in range(3)]
+    outs = [t.full((M, N), float("nan"), device="cuda:0") for _ in range(6)]
+    t.cuda.synchronize()
+    for i, o in enumerate(outs):
+        b = bs[i % 2]
+        lib.gemm_mx(M, N, K, 1.0, a[2], a[3], b[2], b[3], 0.0, o, ref.F32, N, None, 0, streams[i % 3].cuda_stream)
+    t.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert t.equal(o, want[i % 2]), i
