@@ -7,7 +7,7 @@ import mx_reference as ref
 from fp32_gemm_07_amd import binding as lib
 from gpu_util import say, torch
 from mx_plans import IDS, PLANS, is_plan
-from test_mx_gpu import KINDS, bytes_dev, dtype, operand, run_layer, stream
+from test_mx_gpu import KINDS, bytes_dev, check_layer, dtype, layer_case, operand, run_layer, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -278,3 +278,39 @@ def test_product_kernels_captured_and_on_streams(M, N, K, tile, split):
     t.cuda.synchronize()
     for i, o in enumerate(outs):
         assert t.equal(o, want[i % 2]), i
+
+
+# ---------------------------------------------------------------------------
+# More of the layer.
+
+@pytest.mark.parametrize("renorm", [True, False], ids=["renorm", "plain"])
+@pytest.mark.parametrize("kind,T,H,I,E,k", [
+    # groups of 8 tokens whose activations fill several batches of K in LDS
+    ("bf16", 40, 5120, 48, 8, 2), ("bf16", 64, 7000, 20, 6, 3), ("bf16", 25, 4225, 130, 4, 1),
+    # the same sizes where more parts leave room for groups of 4 only
+    ("f16", 40, 5120, 48, 8, 2), ("f32", 40, 5120, 48, 8, 2),
+    # groups of 8 in one batch, every type
+    ("f16", 30, 1700, 70, 5, 2), ("f32", 30, 1100, 70, 5, 2)])
+def test_layer_with_many_tokens_an_expert(kind, T, H, I, E, k, renorm):
+    say(f"layer {kind} tokens {T} hidden {H} inter {I} experts {E} top {k} renorm {renorm}")
+    x, logits, w1, w2 = layer_case(T + H + E, T, H, I, E, kind)
+    check_layer(run_layer(x, logits, w1, w2, I, k, renorm, kind), x, logits, w1, w2, I, k, renorm, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [4, 30])
+def test_layer_inputs_near_the_largest_value(kind, T):
+    """Inputs near the type's largest value, both signs, under weights that bring the gates
+    back to ordinary size: what the split into parts leaves of them is in the bound."""
+    say(f"layer large inputs {kind}, {T} tokens")
+    H, I, E, k = 260, 64, 4, 2
+    x, logits, w1, w2 = layer_case(T, T, H, I, E, kind)
+    top = torch().finfo(dtype(kind)).max
+    rng = np.random.default_rng(T)
+    big = rng.random(x.shape) < 0.3
+    x[big] = ref.to_type(top * rng.choice([-1.0, -0.75, 0.5, 1.0], big.sum()), ref.TYPES[kind])
+    assert np.isfinite(x).all() and np.abs(x).max() == top
+    w1 = operand(rng, E * 2 * I, H, *((103, 106) if kind == "f16" else (0, 2)))   # from 2^-24 or 2^-127 on
+    got = run_layer(x, logits, w1, w2, I, k, True, kind)
+    want, _ = check_layer(got, x, logits, w1, w2, I, k, True, kind)
+    assert np.isfinite(want).all() and (np.abs(want) > 0).all()
