@@ -15,10 +15,6 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgemm.so")
 SOURCES = [os.path.join(CSRC, "gemm_api.hip"), os.path.join(CSRC, "gemm_dma.hip"),
            os.path.join(CSRC, "gemm_mx.hip")]
-DEPENDS = SOURCES + [os.path.join(CSRC, "host_shared.hpp"), os.path.join(CSRC, "mx_kernels.hpp"),
-                     os.path.join(CSRC, "mx_moe.hpp"),
-                     os.path.join(CSRC, "gemm_kernels.hpp"), os.path.join(CSRC, "ladder_kernels.hpp"),
-                     os.path.join(CSRC, "dma_launch.hpp"), os.path.join(INCLUDE, "gemm.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIPCC_FLAGS = [
