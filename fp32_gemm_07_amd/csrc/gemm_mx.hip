@@ -342,11 +342,14 @@ int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
   int st = GEMM_OK;
   with_type(type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    // Groups of 8 where an expert has more than 2 tokens on average (its weights are
-    // then read once for 8 of them: 64 tokens on 8 of 128 experts, 4096 x 1024,
-    // 243 us against 289 with groups of 4), else of 4 (fewer activations to move:
-    // 32 tokens on 8 of those 128 198 us against 202).
-    if (static_cast<long long>(a.tokens) * a.top_k > 2LL * a.experts && activations_fit<T, 8>(a))
+    // Groups of 8 where an expert has more than 3 tokens on average (its weights are
+    // then read once for 8 of them), else of 4 (fewer activations to move and split):
+    // with 2, 2.5, 3 and 4 tokens for each of 128 experts of 4096 x 1024 (bfloat16) groups
+    // of 4 take 177, 200, 220 and 261 us, of 8 202, 214, 218 and 233; with 2, 3, 4 and 16
+    // for each of 8 of 4096 x 2048 32, 38, 40 and 104 us against 38, 39, 41 and 81; with 3
+    // and 6 for each of 16 of 2048 x 1024 32 and 45 us against 35 and 41 in half, 33 and 46
+    // against 37 and 44 in FP32.
+    if (static_cast<long long>(a.tokens) * a.top_k > 3LL * a.experts && activations_fit<T, 8>(a))
       st = launch_moe_groups<T, 8, true>(a, cus, stream);
     else if (activations_fit<T, 4>(a))
       st = launch_moe_groups<T, 4, true>(a, cus, stream);
