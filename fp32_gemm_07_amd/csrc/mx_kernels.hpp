@@ -404,7 +404,7 @@ __device__ inline intx8 widen(const intx4 v) { return intx8{v[0], v[1], v[2], v[
 // takes 16 rows of B (its instructions' rows; A's rows are the columns), its 8
 // waves share K, a wave taking kSkinnyAt neighbouring chunks of 128 at a time.
 // The waves' sums are added in order. 1 x 4096 x 4096 (8.9 MB, other weights every
-// call) takes 4.7 us, half of it the launch; the tiled kernel with 4 splits and
+// call) takes 4.8 us, half of it the launch; the tiled kernel with 4 splits and
 // their sum takes 2.2 us more.
 constexpr int kSkinnyWaves = 8, kSkinnyAt = 4;
 

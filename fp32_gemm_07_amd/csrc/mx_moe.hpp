@@ -383,7 +383,7 @@ __device__ inline float pair_scale(const uintx2 &s, int b, int g) {
 // next item where this one ends) are on their way meanwhile, in the other of
 // two sets of registers.
 // Bound by the weights' bytes: 32 tokens on 8 of 128 experts of 4096 x 1024 (0.49 GB
-// of G and U) take 123 us, 10 of them routing, so 4.3 TB/s. With activations
+// of G and U) take 118 to 125 us, 10 of them routing, so 4.2 to 4.5 TB/s. With activations
 // loaded anew for each item the vector memory pipe was the bound (155 us, as long
 // with the arithmetic left out).
 constexpr int kUpLds = 160 * 1024;
@@ -628,8 +628,8 @@ __global__ __launch_bounds__(kMoeThreads, 4) void moe_up_kernel(MoeArgs a) {
 // parts are added to the wave's own sums of those tokens, in LDS; at the end
 // the waves' sums are added in order. Where the first part's sum is not finite it is the
 // result: the other parts of an infinity are NaN.
-// 32 tokens on 8 of 128 experts of 4096 x 1024 (0.25 GB of D) take 69 us, 3.6 TB/s;
-// the activations, as many bytes for a workgroup as its weights, cost the rest.
+// 32 tokens on 8 of 128 experts of 4096 x 1024 (0.25 GB of D) take 69 to 73 us, 3.4 to 3.6
+// TB/s; the activations, as many bytes for a workgroup as its weights, cost the rest.
 template <int TYPE, int GROUP>
 __global__ __launch_bounds__(64 * kDownWaves<TYPE>, kDownWaves<TYPE> / 4) void moe_down_kernel(
     MoeArgs a) {

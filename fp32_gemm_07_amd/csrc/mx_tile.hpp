@@ -28,10 +28,14 @@ namespace mx {
 // Rows past M or N and stages past the K range are outside the copies' buffer
 // ranges and read as zeros (a zero scale byte is 2^-127, not NaN).
 //
-// 8192^3 with 256 x 256 tiles takes 284 to 299 us from chip to chip (3.9 to 3.7 PFLOP/s). The
-// instructions alone (no reads, copies or stores) take 195 us on the same data:
-// random operands draw so much power that the chip's matrix rate falls from 8.7 to
-// 6.3 PFLOP/s. With stages of 128 values of K it took 305 us.
+// 8192^3 with 256 x 256 tiles takes 292 to 306 us from chip to chip (3.8 to 3.6 PFLOP/s):
+// 571,000 cycles a CU, in 46% of which the matrix pipe is busy, at a mean 1.9 GHz of 2.4. Its
+// instructions in a loop of their own take 173 us on random operands (6.36 PFLOP/s)
+// and 122 on constant ones (9.0): the difference is power. The cycles beside them
+// are what feeds them: with stages of 128 values of K, when it took 305 us, this
+// kernel without its copies, reads and stores took 195, the copies added 70, the LDS
+// reads 33, and of a tile's 76 us 10 were its start and end. 4096^3 (46 to 51 us, one tile a
+// CU): 95,000 cycles, the pipe busy in 34%, at 1.9 to 2.1 GHz.
 // Smaller tiles are bound by what a CU gets from the L2 cache, about 10 TB/s for the
 // chip in half lines: 4096^3 with 128 x 128 tiles took 54 us, in whole lines 46.
 // 16 bytes of C: alpha * sums + beta * C, or with RAW the sums.

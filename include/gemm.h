@@ -321,7 +321,8 @@ int gemm_mx_dequantize(int trans, int rows, int K, const void *codes, const void
  * (B's columns), both of K values; C is M x N of c_type, row stride ldc >= N.
  * Products and sums are FP32 (products of e2m1 numbers and scales are exact);
  * with a split K the partial sums are added in ascending order, so results
- * are the same from run to run. alpha, beta, K = 0 and the final rounding
+ * are the same from run to run (but for a call that can get no workspace from the
+ * library: it runs unsplit). alpha, beta, K = 0 and the final rounding
  * as in gemm_f32_general (fmaf(alpha, sum, fl(beta * c)), rounded once more
  * when c_type has 16 bits): beta == 0 does not read C; alpha == 0 or K == 0
  * does not read A and B. workspace: null for the library's (not while the
@@ -367,10 +368,13 @@ int gemm_mx_plan(int M, int N, int K, gemm_mx_plan_t *plan);
  * sizes and the choice alone.
  * An expert whose logit is -inf is never chosen (a token with no other is
  * given zeros, one with fewer than top_k others gets those); a NaN or +inf
- * among a token's logits makes its row of Y NaN.
+ * among a token's logits makes its row of Y NaN. Weights are the values that
+ * gemm_mx_dequantize gives in FP32 (infinite from 2^128 on); FP32 inputs and hidden
+ * activations below 2^-110 in magnitude are cut off to a multiple of 2^-133.
  * 1 <= tokens <= GEMM_MX_MOE_MAX_TOKENS (0 does nothing), experts <=
  * GEMM_MX_MOE_MAX_EXPERTS, top_k <= GEMM_MX_MOE_MAX_TOP_K and <= experts.
- * workspace: as gemm_mx, gemm_mx_moe_workspace_bytes(...) bytes. */
+ * workspace: as gemm_mx, gemm_mx_moe_workspace_bytes(...) bytes; GEMM_ERR_WORKSPACE
+ * also where the library can get none. */
 enum {
   GEMM_MX_MOE_MAX_TOKENS = 64,
   GEMM_MX_MOE_MAX_EXPERTS = 512,
