@@ -37,6 +37,12 @@ GEMM_MX_MOE_MAX_TOKENS = 64
 GEMM_MX_MOE_MAX_EXPERTS = 512
 GEMM_MX_MOE_MAX_TOP_K = 16
 
+GEMM_ROUTE_SOFTMAX = 0
+GEMM_ROUTE_SIGMOID = 1
+GEMM_ROUTE_MAX_EXPERTS = 512
+GEMM_ROUTE_MAX_TOP_K = 16
+GEMM_ROUTE_MAX_GROUPS = 64
+
 GEMM_KERNEL_AUTO = 0
 GEMM_KERNEL_MFMA_256x256 = 1
 GEMM_KERNEL_MFMA_256x128 = 2
@@ -105,7 +111,8 @@ EXPORTS = (
     "gemm_f32_plan_workspace_bytes", "gemm_f32_with_plan", "gemm_f32_general",
     "gemm_f32_general_workspace_bytes", "gemm_mx_codes_bytes", "gemm_mx_scales_bytes",
     "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_workspace_bytes", "gemm_mx_plan",
-    "gemm_mx_moe", "gemm_mx_moe_workspace_bytes", "gemm_kernel_name", "gemm_status_string",
+    "gemm_mx_moe", "gemm_mx_moe_workspace_bytes", "gemm_mx_moe_routed", "gemm_route",
+    "gemm_route_backward", "gemm_kernel_name", "gemm_status_string",
     "gemm_last_hip_error",
 )
 
@@ -135,6 +142,24 @@ class gemm_mx_plan_t(ctypes.Structure):
     def __repr__(self):
         return (f"gemm_mx_plan_t(tile_m={self.tile_m}, tile_n={self.tile_n}, stages={self.stages}, "
                 f"split_k={self.split_k}, k_chunk={self.k_chunk})")
+
+
+class gemm_route_t(ctypes.Structure):
+    """A router: how many experts, how many of them a token chooses, and how."""
+    _fields_ = [("experts", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int),
+                ("groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("group_top", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+    def __init__(self, experts: int, top_k: int, score: int = GEMM_ROUTE_SOFTMAX, groups: int = 1,
+                 top_groups: int = 1, group_top: int = 1, renormalize: bool = False,
+                 scale: float = 1.0):
+        super().__init__(experts, top_k, score, groups, top_groups, group_top,
+                         int(bool(renormalize)), scale)
+
+    def __repr__(self):
+        return (f"gemm_route_t(experts={self.experts}, top_k={self.top_k}, score={self.score}, "
+                f"groups={self.groups}, top_groups={self.top_groups}, group_top={self.group_top}, "
+                f"renormalize={self.renormalize}, scale={self.scale})")
 
 
 _lib = None
@@ -215,6 +240,14 @@ def load():
         lib.gemm_mx_moe.restype = i
         lib.gemm_mx_moe_workspace_bytes.argtypes = [i, i, i, i]
         lib.gemm_mx_moe_workspace_bytes.restype = sz
+        lib.gemm_mx_moe_routed.argtypes = [i, i, i, i, i, vp, vp, vp, i, i, vp, vp, vp, vp, vp, i,
+                                           vp, sz, vp]
+        lib.gemm_mx_moe_routed.restype = i
+        route_p = ctypes.POINTER(gemm_route_t)
+        lib.gemm_route.argtypes = [i, route_p, vp, i, i, vp, vp, vp, vp, vp]
+        lib.gemm_route.restype = i
+        lib.gemm_route_backward.argtypes = [i, route_p, vp, i, i, vp, vp, vp, i, vp]
+        lib.gemm_route_backward.restype = i
         lib.gemm_kernel_name.argtypes = [i]
         lib.gemm_kernel_name.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [i]
@@ -361,6 +394,35 @@ def gemm_mx_moe(tokens: int, hidden: int, inter: int, experts: int, top_k: int, 
 
 def gemm_mx_moe_workspace_bytes(tokens: int, inter: int, top_k: int, x_type: int) -> int:
     return int(load().gemm_mx_moe_workspace_bytes(tokens, inter, top_k, x_type))
+
+
+def gemm_mx_moe_routed(tokens: int, hidden: int, inter: int, experts: int, top_k: int, chosen,
+                       weights, X, x_type: int, ldx: int, W1_codes, W1_scales, W2_codes, W2_scales,
+                       Y, ldy: int, workspace=None, workspace_bytes: int = 0,
+                       stream: int = 0) -> None:
+    _check(load().gemm_mx_moe_routed(tokens, hidden, inter, experts, top_k, _addr(chosen) or None,
+                                     _addr(weights) or None, _addr(X) or None, x_type, ldx,
+                                     _addr(W1_codes) or None, _addr(W1_scales) or None,
+                                     _addr(W2_codes) or None, _addr(W2_scales) or None,
+                                     _addr(Y) or None, ldy, _addr(workspace) or None,
+                                     workspace_bytes, stream or None), "gemm_mx_moe_routed")
+
+
+def gemm_route(tokens: int, router: gemm_route_t, logits, logits_type: int, ld_logits: int, bias,
+               chosen, weights, counts=None, stream: int = 0) -> None:
+    _check(load().gemm_route(tokens, ctypes.byref(router), _addr(logits) or None, logits_type,
+                             ld_logits, _addr(bias) or None, _addr(chosen) or None,
+                             _addr(weights) or None, _addr(counts) or None, stream or None),
+           "gemm_route")
+
+
+def gemm_route_backward(tokens: int, router: gemm_route_t, logits, logits_type: int,
+                        ld_logits: int, chosen, dweights, dlogits, ld_dlogits: int,
+                        stream: int = 0) -> None:
+    _check(load().gemm_route_backward(tokens, ctypes.byref(router), _addr(logits) or None,
+                                      logits_type, ld_logits, _addr(chosen) or None,
+                                      _addr(dweights) or None, _addr(dlogits) or None, ld_dlogits,
+                                      stream or None), "gemm_route_backward")
 
 
 def gemm_kernel_name(kernel: int) -> str:

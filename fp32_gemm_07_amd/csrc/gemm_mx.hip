@@ -4,9 +4,8 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <initializer_list>
-#include <type_traits>
 
+#include "host_checks.hpp"
 #include "host_shared.hpp"
 #include "mx_kernels.hpp"
 #include "mx_moe.hpp"
@@ -15,6 +14,7 @@
 namespace {
 
 using namespace gemm::mx;
+using namespace gemm::host;
 
 static_assert(kF32 == GEMM_TYPE_F32 && kBf16 == GEMM_TYPE_BF16 && kF16 == GEMM_TYPE_F16,
               "element types");
@@ -22,52 +22,12 @@ static_assert(kMaxTokens == GEMM_MX_MOE_MAX_TOKENS && kMaxExperts == GEMM_MX_MOE
                   kMaxTopK == GEMM_MX_MOE_MAX_TOP_K,
               "layer limits");
 
-constexpr long long kMaxElements = 1LL << 40;
-
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 int padded(int K) { return static_cast<int>(ceil_div(K, kAlign) * kAlign); }
 size_t codes_bytes(long long rows, int K) { return static_cast<size_t>(rows) * (padded(K) / 2); }
 size_t scales_bytes(long long rows, int K) { return static_cast<size_t>(rows) * (padded(K) / 32); }
-bool valid_type(int t) { return t == kF32 || t == kBf16 || t == kF16; }
-size_t elem_size(int t) { return t == kF32 ? 4 : 2; }
-bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
-
 // Rows and K of an operand.
 bool valid_operand(long long rows, int K) {
   return rows >= 0 && K >= 0 && K <= GEMM_MX_MAX_K && rows * static_cast<long long>(padded(K)) <= kMaxElements;
-}
-
-// Bytes from the first to the last element of a stored matrix.
-size_t extent(long long rows, long long cols, long long ld, int type) {
-  return rows > 0 && cols > 0 ? elem_size(type) * static_cast<size_t>((rows - 1) * ld + cols) : 0;
-}
-
-int launched() {
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? GEMM_OK : gemm::host_fail(e);
-}
-
-// A launch takes fewer than 2^32 threads, so at most this many workgroups.
-constexpr long long max_blocks(long long threads) { return ((1LL << 32) - 1) / threads; }
-
-// launch(at, count), which returns a status, for successive ranges of at most `most`
-// of `total`.
-template <class F>
-int in_ranges(long long total, long long most, F &&launch) {
-  int st = GEMM_OK;
-  for (long long at = 0; at < total && st == GEMM_OK; at += most)
-    st = launch(at, static_cast<int>(std::min(most, total - at)));
-  return st;
-}
-
-// Calls f.template operator()<TYPE>() for a valid element type.
-template <class F>
-void with_type(int type, F &&f) {
-  switch (type) {
-    case kF32: f(std::integral_constant<int, kF32>()); break;
-    case kBf16: f(std::integral_constant<int, kBf16>()); break;
-    default: f(std::integral_constant<int, kF16>()); break;
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -292,23 +252,6 @@ int check_product(const Product &p) {
   return GEMM_OK;
 }
 
-// A range that a call reads or writes.
-struct Range {
-  const void *p;
-  size_t bytes;
-};
-
-// A caller's workspace (null: the library's) of `need` bytes: large enough,
-// aligned, and apart from everything else that the call touches.
-int check_workspace(const void *workspace, size_t bytes, size_t need, std::initializer_list<Range> others) {
-  if (!workspace || need == 0) return GEMM_OK;
-  if (bytes < need) return GEMM_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return GEMM_ERR_ALIGNMENT;
-  for (const Range &r : others)
-    if (gemm::host_overlaps(workspace, need, r.p, r.bytes)) return GEMM_ERR_ALIAS;
-  return GEMM_OK;
-}
-
 // ---------------------------------------------------------------------------
 // The mixture-of-experts layer.
 constexpr size_t kGroupBytes = (kMaxGroups + 1) * sizeof(Group) / 16 * 16 + 16;   // the workspace's head
@@ -359,22 +302,25 @@ int launch_moe(const MoeArgs &a, int type, int cus, hipStream_t stream) {
   return st;
 }
 
-int check_moe(const MoeArgs &a, int type) {
+int check_moe(const MoeArgs &a, int type, bool routed) {
   if (a.tokens < 0 || a.tokens > kMaxTokens || a.hidden < 1 || a.inter < 1 || a.experts < 1 ||
       a.experts > kMaxExperts || a.top_k < 1 || a.top_k > std::min(kMaxTopK, a.experts) ||
-      a.ld_logits < a.experts || a.ldx < a.hidden || a.ldy < a.hidden)
+      (!routed && a.ld_logits < a.experts) || a.ldx < a.hidden || a.ldy < a.hidden)
     return GEMM_ERR_INVALID_DIM;
   const long long rows1 = 2LL * a.experts * a.inter, rows2 = static_cast<long long>(a.experts) * a.hidden;
   if (!valid_operand(rows1, a.hidden) || !valid_operand(rows2, a.inter)) return GEMM_ERR_INVALID_DIM;
   if (!valid_type(type)) return GEMM_ERR_INVALID_TYPE;
   if (a.tokens == 0) return GEMM_OK;
-  if (!a.logits || !a.x || !a.y || !a.w1c || !a.w1s || !a.w2c || !a.w2s) return GEMM_ERR_NULL_PTR;
+  if ((routed ? !a.chosen || !a.weights : !a.logits) || !a.x || !a.y || !a.w1c || !a.w1s || !a.w2c || !a.w2s) return GEMM_ERR_NULL_PTR;
   const size_t es = elem_size(type);
-  if (!aligned(a.logits, 4) || !aligned(a.x, es) || !aligned(a.y, es) || !aligned(a.w1c, 16) ||
+  if (!aligned(a.logits, 4) || !aligned(a.chosen, 4) || !aligned(a.weights, 4) || !aligned(a.x, es) || !aligned(a.y, es) || !aligned(a.w1c, 16) ||
       !aligned(a.w2c, 16) || !aligned(a.w1s, 4) || !aligned(a.w2s, 4))
     return GEMM_ERR_ALIGNMENT;
   const size_t y = extent(a.tokens, a.hidden, a.ldy, type);
-  if (gemm::host_overlaps(a.y, y, a.logits, extent(a.tokens, a.experts, a.ld_logits, kF32)) ||
+  const size_t logits = routed ? 0 : extent(a.tokens, a.experts, a.ld_logits, kF32);
+  const size_t choices = routed ? 4 * static_cast<size_t>(a.tokens) * a.top_k : 0;
+  if (gemm::host_overlaps(a.y, y, a.logits, logits) || gemm::host_overlaps(a.y, y, a.chosen, choices) ||
+      gemm::host_overlaps(a.y, y, a.weights, choices) ||
       gemm::host_overlaps(a.y, y, a.x, extent(a.tokens, a.hidden, a.ldx, type)) ||
       gemm::host_overlaps(a.y, y, a.w1c, codes_bytes(rows1, a.hidden)) ||
       gemm::host_overlaps(a.y, y, a.w1s, scales_bytes(rows1, a.hidden)) ||
@@ -382,6 +328,38 @@ int check_moe(const MoeArgs &a, int type) {
       gemm::host_overlaps(a.y, y, a.w2s, scales_bytes(rows2, a.inter)))
     return GEMM_ERR_ALIAS;
   return GEMM_OK;
+}
+
+int run_moe(MoeArgs a, int type, bool routed, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  int st = check_moe(a, type, routed);
+  if (st != GEMM_OK || a.tokens == 0) return st;
+  const size_t need = moe_workspace(a.tokens, a.inter, a.top_k, type);
+  const long long rows1 = 2LL * a.experts * a.inter, rows2 = static_cast<long long>(a.experts) * a.hidden;
+  const size_t choices = routed ? 4 * static_cast<size_t>(a.tokens) * a.top_k : 0;
+  st = check_workspace(workspace, workspace_bytes, need,
+                       {{a.y, extent(a.tokens, a.hidden, a.ldy, type)}, {a.x, extent(a.tokens, a.hidden, a.ldx, type)},
+                        {a.logits, routed ? 0 : extent(a.tokens, a.experts, a.ld_logits, kF32)},
+                        {a.chosen, choices}, {a.weights, choices},
+                        {a.w1c, codes_bytes(rows1, a.hidden)}, {a.w1s, scales_bytes(rows1, a.hidden)},
+                        {a.w2c, codes_bytes(rows2, a.inter)}, {a.w2s, scales_bytes(rows2, a.inter)}});
+  if (st != GEMM_OK) return st;
+  int dev = 0, cus = 0;
+  st = gemm::host_check_device(&dev, &cus);
+  if (st != GEMM_OK) return st;
+  struct Call {
+    MoeArgs *a;
+    int type, cus;
+    hipStream_t stream;
+  } call{&a, type, cus, stream};
+  auto body = [](void *c, void *ws) {
+    const Call *k = static_cast<const Call *>(c);
+    if (!ws) return static_cast<int>(GEMM_ERR_WORKSPACE);
+    k->a->groups = static_cast<Group *>(ws);
+    k->a->h = reinterpret_cast<u16 *>(static_cast<char *>(ws) + kGroupBytes);
+    return launch_moe(*k->a, k->type, k->cus, k->stream);
+  };
+  if (workspace) return body(&call, workspace);
+  return gemm::host_with_library_workspace(dev, need, stream, body, &call);
 }
 
 }  // namespace
@@ -522,37 +500,23 @@ int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int r
                 const void *W1_codes, const void *W1_scales, const void *W2_codes,
                 const void *W2_scales, void *Y, int ldy, void *workspace, size_t workspace_bytes,
                 hipStream_t stream) {
-  MoeArgs a{tokens, hidden, inter, experts, top_k, renormalize != 0, logits, ld_logits, X, ldx,
-            static_cast<const unsigned char *>(W1_codes), static_cast<const unsigned char *>(W1_scales),
-            static_cast<const unsigned char *>(W2_codes), static_cast<const unsigned char *>(W2_scales),
-            Y, ldy, nullptr, nullptr};
-  int st = check_moe(a, x_type);
-  if (st != GEMM_OK || tokens == 0) return st;
-  const size_t need = moe_workspace(tokens, inter, top_k, x_type);
-  const long long rows1 = 2LL * experts * inter, rows2 = static_cast<long long>(experts) * hidden;
-  st = check_workspace(workspace, workspace_bytes, need,
-                       {{Y, extent(tokens, hidden, ldy, x_type)}, {X, extent(tokens, hidden, ldx, x_type)},
-                        {logits, extent(tokens, experts, ld_logits, kF32)},
-                        {W1_codes, codes_bytes(rows1, hidden)}, {W1_scales, scales_bytes(rows1, hidden)},
-                        {W2_codes, codes_bytes(rows2, inter)}, {W2_scales, scales_bytes(rows2, inter)}});
-  if (st != GEMM_OK) return st;
-  int dev = 0, cus = 0;
-  st = gemm::host_check_device(&dev, &cus);
-  if (st != GEMM_OK) return st;
-  struct Call {
-    MoeArgs *a;
-    int type, cus;
-    hipStream_t stream;
-  } call{&a, x_type, cus, stream};
-  auto body = [](void *c, void *ws) {
-    const Call *k = static_cast<const Call *>(c);
-    if (!ws) return static_cast<int>(GEMM_ERR_WORKSPACE);
-    k->a->groups = static_cast<Group *>(ws);
-    k->a->h = reinterpret_cast<u16 *>(static_cast<char *>(ws) + kGroupBytes);
-    return launch_moe(*k->a, k->type, k->cus, k->stream);
-  };
-  if (workspace) return body(&call, workspace);
-  return gemm::host_with_library_workspace(dev, need, stream, body, &call);
+  const MoeArgs a{tokens, hidden, inter, experts, top_k, renormalize != 0, logits, ld_logits, nullptr, nullptr, X, ldx,
+                  static_cast<const unsigned char *>(W1_codes), static_cast<const unsigned char *>(W1_scales),
+                  static_cast<const unsigned char *>(W2_codes), static_cast<const unsigned char *>(W2_scales),
+                  Y, ldy, nullptr, nullptr};
+  return run_moe(a, x_type, false, workspace, workspace_bytes, stream);
+}
+
+int gemm_mx_moe_routed(int tokens, int hidden, int inter, int experts, int top_k,
+                       const int *chosen, const float *weights, const void *X, int x_type, int ldx,
+                       const void *W1_codes, const void *W1_scales, const void *W2_codes,
+                       const void *W2_scales, void *Y, int ldy, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  const MoeArgs a{tokens, hidden, inter, experts, top_k, 0, nullptr, 0, chosen, weights, X, ldx,
+                  static_cast<const unsigned char *>(W1_codes), static_cast<const unsigned char *>(W1_scales),
+                  static_cast<const unsigned char *>(W2_codes), static_cast<const unsigned char *>(W2_scales),
+                  Y, ldy, nullptr, nullptr};
+  return run_moe(a, x_type, true, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

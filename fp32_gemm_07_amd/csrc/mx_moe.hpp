@@ -23,6 +23,7 @@
 #pragma once
 
 #include "gemm_kernels.hpp"
+#include "lanes.hpp"
 #include "mx_kernels.hpp"
 
 namespace gemm {
@@ -51,7 +52,8 @@ constexpr int kDownWaves = TYPE == kF32 ? 8 : 16;
 // pair and the tokens (a byte each, the first one again where there are fewer).
 // Pairs (token, expert) are numbered by expert, then token; pair numbers index the
 // rows of the hidden activations. Entry 0 of the workspace's list holds how many
-// follow and the tokens whose logits hold a NaN or +inf, one bit each.
+// follow and the tokens whose logits hold a NaN or +inf (or whose
+// given weights a NaN), one bit each.
 struct Group {
   unsigned packed;   // expert | count << 9 | first pair << 13
   unsigned lo, hi;
@@ -68,8 +70,10 @@ __device__ inline Group uniform(const Group &g) {
 
 struct MoeArgs {
   int tokens, hidden, inter, experts, top_k, renormalize;
-  const float *logits;
+  const float *logits;   // null: the choice is given
   int ld_logits;
+  const int *chosen;     // tokens x top_k, and the weights
+  const float *weights;
   const void *x;
   int ldx;
   const unsigned char *w1c, *w1s, *w2c, *w2s;
@@ -94,47 +98,6 @@ struct RoutingScratch {
   u16 chosen[kMaxTokens * kMaxTopK];           // token t's experts at t * kMaxTopK, 0xffff: none
   float chosen_weight[kMaxTokens * kMaxTopK];
 };
-
-template <int CTRL, int ROWS>
-__device__ inline int dpp(int identity, int v) {
-  return __builtin_amdgcn_update_dpp(identity, v, CTRL, ROWS, 0xf, false);
-}
-// v of the lane N further on in its row of 16 (0 past the row).
-template <int N>
-__device__ inline float from_lane(float v) {
-  return __builtin_bit_cast(float, dpp<0x100 + N, 0xf>(0, __builtin_bit_cast(int, v)));
-}
-// op over the 16 lanes of a row (rotations by 1, 2, 4, 8), in every lane.
-template <class OP>
-__device__ inline int row_all(int v, OP &&op) {
-  v = op(v, dpp<0x121, 0xf>(0, v));
-  v = op(v, dpp<0x122, 0xf>(0, v));
-  v = op(v, dpp<0x124, 0xf>(0, v));
-  return op(v, dpp<0x128, 0xf>(0, v));
-}
-__device__ inline unsigned row_max(unsigned v) {
-  return static_cast<unsigned>(row_all(static_cast<int>(v), [](int a, int b) {
-    return static_cast<int>(max(static_cast<unsigned>(a), static_cast<unsigned>(b)));
-  }));
-}
-__device__ inline int row_min(int v) {
-  return row_all(v, [](int a, int b) { return min(a, b); });
-}
-__device__ inline float row_sum(float v) {
-  return __builtin_bit_cast(float, row_all(__builtin_bit_cast(int, v), [](int a, int b) {
-    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
-  }));
-}
-// Running sums over a wave: shifts within rows, then the last lane of each row
-// and of the first half handed on (row_bcast 15, 31).
-__device__ inline int wave_running_sum(int v) {
-  v += dpp<0x111, 0xf>(0, v);
-  v += dpp<0x112, 0xf>(0, v);
-  v += dpp<0x114, 0xf>(0, v);
-  v += dpp<0x118, 0xf>(0, v);
-  v += dpp<0x142, 0xa>(0, v);
-  return v + dpp<0x143, 0xc>(0, v);
-}
 
 // The choice of 4 tokens, one to each row of 16 lanes, whose lanes hold the
 // experts l, l + 16, ..: top_k rounds of a maximum over the row. Logits are
@@ -208,6 +171,36 @@ __device__ inline void choose(const MoeArgs &a, int t, Routing &r, RoutingScratc
   }
 }
 
+// The given choice of 4 tokens, a lane of a row of 16 for each entry. An expert named
+// again counts with its first entry, which takes the sum of the weights in order.
+__device__ inline void take_choice(const MoeArgs &a, int t, Routing &r, RoutingScratch &s) {
+  const int l16 = threadIdx.x & 15;
+  const bool ok = t < a.tokens && l16 < a.top_k;
+  int expert = -1;
+  float w = 0.0f;
+  if (ok) {
+    expert = a.chosen[t * a.top_k + l16];
+    w = a.weights[t * a.top_k + l16];
+  }
+  const bool bad = row_max(w != w ? 1u : 0u) != 0;
+  bool live = ok && !bad && expert >= 0 && expert < a.experts;
+  if (!live) expert = -1;
+  const float own = w;
+  for (int n = 1; n < a.top_k; ++n) {
+    const int e = __shfl(expert, n, 16);
+    const float v = __shfl(own, n, 16);
+    if (e == expert && n > l16) w += v;
+  }
+  for (int n = 0; n < a.top_k - 1; ++n)
+    if (__shfl(expert, n, 16) == expert && n < l16) live = false;
+  if (t < a.tokens) {
+    s.chosen[t * kMaxTopK + l16] = static_cast<u16>(live ? expert : 0xffff);
+    s.chosen_weight[t * kMaxTopK + l16] = w;
+    if (live) atomicOr(t < 32 ? &s.lo[expert] : &s.hi[expert], 1u << (t & 31));
+    if (bad && l16 == 0) atomicOr(t < 32 ? &r.nan_lo : &r.nan_hi, 1u << (t & 31));
+  }
+}
+
 // Routes all tokens; ends with a barrier.
 template <int GROUP>
 __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
@@ -218,7 +211,8 @@ __device__ inline void route(const MoeArgs &a, Routing &r, RoutingScratch &s) {
   __syncthreads();
   for (int t0 = wave * 4; t0 < a.tokens; t0 += kMoeWaves * 4) {
     const int t = t0 + (lane >> 4);
-    if (a.experts <= 64) choose<4>(a, t, r, s);
+    if (!a.logits) take_choice(a, t, r, s);
+    else if (a.experts <= 64) choose<4>(a, t, r, s);
     else if (a.experts <= 128) choose<8>(a, t, r, s);
     else if (a.experts <= 256) choose<16>(a, t, r, s);
     else choose<32>(a, t, r, s);

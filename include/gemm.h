@@ -59,8 +59,9 @@ enum {
   GEMM_ERR_INVALID_DIM = 1,      /* M, N or K negative, or a size too large to index */
   GEMM_ERR_NULL_PTR = 2,         /* null A, B or C that the call would access
                                     (A, B when M, N, K > 0; C when M, N > 0) */
-  GEMM_ERR_ALIAS = 3,            /* C overlaps A or B (gemm_mx*: an output or the
-                                    workspace overlaps something else of the call) */
+  GEMM_ERR_ALIAS = 3,            /* C overlaps A or B (gemm_mx*, gemm_route*, gemm_lora*: an
+                                    output or the workspace overlaps something else
+                                    of the call) */
   GEMM_ERR_WORKSPACE = 4,        /* workspace missing or smaller than required */
   GEMM_ERR_INVALID_PLAN = 5,     /* unknown kernel id, split count < 1 or unusable split_tail */
   GEMM_ERR_HIP = 6,              /* a HIP call failed; see gemm_last_hip_error() */
@@ -71,9 +72,10 @@ enum {
                                      gemm_f32_general) */
   GEMM_ERR_SCRATCH_LIMIT = 9,     /* gemm_f32_noalloc: the plan's partial sums need
                                      more than its static scratch buffer */
-  GEMM_ERR_INVALID_TYPE = 10,     /* gemm_mx*: not a GEMM_TYPE_* */
-  GEMM_ERR_ALIGNMENT = 11         /* gemm_mx*: a pointer without the alignment that
-                                     its operand needs */
+  GEMM_ERR_INVALID_TYPE = 10,     /* gemm_mx*, gemm_route*, gemm_lora*: not a GEMM_TYPE_*
+                                     (gemm_route_t: not a GEMM_ROUTE_*) */
+  GEMM_ERR_ALIGNMENT = 11         /* gemm_mx*, gemm_route*, gemm_lora*: a pointer without the
+                                     alignment that its operand needs */
 };
 
 /* Element types of the float matrices that the gemm_mx* entry points take. */
@@ -389,6 +391,77 @@ int gemm_mx_moe(int tokens, int hidden, int inter, int experts, int top_k, int r
 /* Workspace bytes gemm_mx_moe needs for these sizes and the type of X
  * (always some for tokens > 0; 0 for invalid arguments). */
 size_t gemm_mx_moe_workspace_bytes(int tokens, int inter, int top_k, int x_type);
+
+/* gemm_mx_moe on a choice made elsewhere, by gemm_route or otherwise:
+ *   Y[t] = sum over i < top_k of w_i D_e a_e,  e = chosen[t*top_k + i],
+ *                                              w_i = weights[t*top_k + i]
+ * Everything else is as gemm_mx_moe describes it, the workspace too. An entry whose
+ * expert lies outside 0 .. experts - 1 counts nothing (a token with no other is
+ * given zeros); an expert named twice counts with the sum of its weights; a NaN among a
+ * token's weights makes its row of Y NaN, whatever expert it stands with. */
+int gemm_mx_moe_routed(int tokens, int hidden, int inter, int experts, int top_k,
+                       const int *chosen, const float *weights, const void *X, int x_type, int ldx,
+                       const void *W1_codes, const void *W1_scales, const void *W2_codes,
+                       const void *W2_scales, void *Y, int ldy, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing of tokens to experts: what a mixture-of-experts layer chooses by
+ * (gemm_mx_moe_routed takes the result as it is), and the gradient of its logits.
+ *
+ * For a token with logits l (one for each expert, of logits_type):
+ *   s = softmax(l)  (GEMM_ROUTE_SOFTMAX)  or  s_e = 1 / (1 + exp(-l_e))
+ *       (GEMM_ROUTE_SIGMOID);
+ *   v_e = s_e + bias_e; the bias (null: none) is for the choice alone;
+ *   with top_groups < groups the experts are `groups` groups of consecutive ones of
+ *       the same number; a group is worth the sum of its group_top (1 or 2) largest
+ *       v (of those that there are), and only the experts of the top_groups groups that
+ *       are worth most stay;
+ *   S = the top_k experts of largest v that are left, all ties to the lowest index;
+ *   w_e = scale * s_e, or scale * s_e / sum_S s when renormalize.
+ * Where neither a bias nor sums of scores come in, the choice compares the logits
+ * themselves (s rises with l); else v is computed and compared in 64 bits. Weights
+ * are FP32; renormalised ones are taken as ratios, so they are right also where every
+ * score underflows.
+ * An expert whose logit or bias is -inf is never chosen. A token with a NaN among its
+ * logits (softmax: or +inf) is given no experts and NaN weights; so is every token
+ * where the bias holds a NaN. */
+enum { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 };
+enum {
+  GEMM_ROUTE_MAX_EXPERTS = 512,
+  GEMM_ROUTE_MAX_TOP_K = 16,
+  GEMM_ROUTE_MAX_GROUPS = 64
+};
+
+/* 1 <= experts <= GEMM_ROUTE_MAX_EXPERTS; 1 <= top_k <= GEMM_ROUTE_MAX_TOP_K; groups
+ * (1: none) <= GEMM_ROUTE_MAX_GROUPS divides experts; 1 <= top_groups <= groups;
+ * top_k <= top_groups * experts / groups. */
+typedef struct gemm_route {
+  int experts, top_k;
+  int score;        /* GEMM_ROUTE_* */
+  int groups, top_groups, group_top;
+  int renormalize;
+  float scale;
+} gemm_route_t;
+
+/* Routes `tokens` tokens: logits tokens x experts, row stride ld_logits >= experts.
+ * chosen (tokens x top_k, dense) and weights (the same) are written in descending
+ * order of v; where a token has fewer than top_k experts to choose from, -1 and 0 fill
+ * up. counts (experts of them; null: not wanted) gets how often each expert was chosen,
+ * by all tokens together: what a bias that balances the experts is adjusted by. */
+int gemm_route(int tokens, const gemm_route_t *router, const void *logits, int logits_type,
+               int ld_logits, const float *bias, int *chosen, float *weights, int *counts,
+               hipStream_t stream);
+
+/* The gradient of the logits from that of the weights (dweights: tokens x top_k, dense),
+ * the choice fixed: dlogits, tokens x experts of logits_type, row stride ld_dlogits, is
+ * overwritten. For softmax without renormalising it reaches every expert, else the chosen
+ * ones. `chosen` as gemm_route left it; entries outside 0 .. experts - 1 count
+ * nothing, a token without any other gets zeros. The router's groups have been
+ * used for the choice and are only checked. */
+int gemm_route_backward(int tokens, const gemm_route_t *router, const void *logits,
+                        int logits_type, int ld_logits, const int *chosen, const float *dweights,
+                        void *dlogits, int ld_dlogits, hipStream_t stream);
 
 /* Static, human-readable name of a kernel id ("unknown" otherwise). */
 const char *gemm_kernel_name(int kernel);
