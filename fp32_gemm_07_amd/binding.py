@@ -43,6 +43,11 @@ GEMM_ROUTE_MAX_EXPERTS = 512
 GEMM_ROUTE_MAX_TOP_K = 16
 GEMM_ROUTE_MAX_GROUPS = 64
 
+GEMM_LORA_MAX_ROWS = 1 << 20
+GEMM_LORA_MAX_DIM = 1 << 18
+GEMM_LORA_MAX_RANK = 128
+GEMM_LORA_MAX_ADAPTERS = 1024
+
 GEMM_KERNEL_AUTO = 0
 GEMM_KERNEL_MFMA_256x256 = 1
 GEMM_KERNEL_MFMA_256x128 = 2
@@ -112,7 +117,8 @@ EXPORTS = (
     "gemm_f32_general_workspace_bytes", "gemm_mx_codes_bytes", "gemm_mx_scales_bytes",
     "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_workspace_bytes", "gemm_mx_plan",
     "gemm_mx_moe", "gemm_mx_moe_workspace_bytes", "gemm_mx_moe_routed", "gemm_route",
-    "gemm_route_backward", "gemm_kernel_name", "gemm_status_string",
+    "gemm_route_backward", "gemm_lora", "gemm_lora_workspace_bytes", "gemm_lora_backward",
+    "gemm_lora_backward_workspace_bytes", "gemm_kernel_name", "gemm_status_string",
     "gemm_last_hip_error",
 )
 
@@ -160,6 +166,23 @@ class gemm_route_t(ctypes.Structure):
         return (f"gemm_route_t(experts={self.experts}, top_k={self.top_k}, score={self.score}, "
                 f"groups={self.groups}, top_groups={self.top_groups}, group_top={self.group_top}, "
                 f"renormalize={self.renormalize}, scale={self.scale})")
+
+
+class gemm_lora_t(ctypes.Structure):
+    """A set of low-rank adapters. Device pointers as everywhere (tensors or ints); the set
+    keeps no tensor alive."""
+    _fields_ = [("type", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("rank", ctypes.c_int), ("adapters", ctypes.c_int), ("A", ctypes.c_void_p),
+                ("B", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+    def __init__(self, type: int, N: int, K: int, rank: int, adapters: int, A, B, ranks=None,
+                 scales=None):
+        super().__init__(type, N, K, rank, adapters, _addr(A) or None, _addr(B) or None,
+                         _addr(ranks) or None, _addr(scales) or None)
+
+    def __repr__(self):
+        return (f"gemm_lora_t(type={self.type}, N={self.N}, K={self.K}, rank={self.rank}, "
+                f"adapters={self.adapters})")
 
 
 _lib = None
@@ -248,6 +271,16 @@ def load():
         lib.gemm_route.restype = i
         lib.gemm_route_backward.argtypes = [i, route_p, vp, i, i, vp, vp, vp, i, vp]
         lib.gemm_route_backward.restype = i
+        lora_p = ctypes.POINTER(gemm_lora_t)
+        lib.gemm_lora.argtypes = [i, lora_p, vp, vp, i, vp, i, vp, i, vp, sz, vp]
+        lib.gemm_lora.restype = i
+        lib.gemm_lora_workspace_bytes.argtypes = [i, lora_p]
+        lib.gemm_lora_workspace_bytes.restype = sz
+        lib.gemm_lora_backward.argtypes = [i, lora_p, vp, vp, i, vp, i, vp, i, vp, i, vp, vp, vp, sz,
+                                           vp]
+        lib.gemm_lora_backward.restype = i
+        lib.gemm_lora_backward_workspace_bytes.argtypes = [i, lora_p]
+        lib.gemm_lora_backward_workspace_bytes.restype = sz
         lib.gemm_kernel_name.argtypes = [i]
         lib.gemm_kernel_name.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [i]
@@ -423,6 +456,31 @@ def gemm_route_backward(tokens: int, router: gemm_route_t, logits, logits_type: 
                                       logits_type, ld_logits, _addr(chosen) or None,
                                       _addr(dweights) or None, _addr(dlogits) or None, ld_dlogits,
                                       stream or None), "gemm_route_backward")
+
+
+def gemm_lora(rows: int, set: gemm_lora_t, ids, X, ldx: int, C, ldc: int, Y, ldy: int,
+              workspace=None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_lora(rows, ctypes.byref(set), _addr(ids) or None, _addr(X) or None, ldx,
+                            _addr(C) or None, ldc, _addr(Y) or None, ldy, _addr(workspace) or None,
+                            workspace_bytes, stream or None), "gemm_lora")
+
+
+def gemm_lora_workspace_bytes(rows: int, set: gemm_lora_t) -> int:
+    return int(load().gemm_lora_workspace_bytes(rows, ctypes.byref(set)))
+
+
+def gemm_lora_backward(rows: int, set: gemm_lora_t, ids, X, ldx: int, dY, lddy: int, C, ldc: int,
+                       dX, lddx: int, dA, dB, workspace=None, workspace_bytes: int = 0,
+                       stream: int = 0) -> None:
+    _check(load().gemm_lora_backward(rows, ctypes.byref(set), _addr(ids) or None, _addr(X) or None,
+                                     ldx, _addr(dY) or None, lddy, _addr(C) or None, ldc,
+                                     _addr(dX) or None, lddx, _addr(dA) or None, _addr(dB) or None,
+                                     _addr(workspace) or None, workspace_bytes, stream or None),
+           "gemm_lora_backward")
+
+
+def gemm_lora_backward_workspace_bytes(rows: int, set: gemm_lora_t) -> int:
+    return int(load().gemm_lora_backward_workspace_bytes(rows, ctypes.byref(set)))
 
 
 def gemm_kernel_name(kernel: int) -> str:

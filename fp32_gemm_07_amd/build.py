@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgemm.so")
 SOURCES = [os.path.join(CSRC, "gemm_api.hip"), os.path.join(CSRC, "gemm_dma.hip"),
-           os.path.join(CSRC, "gemm_mx.hip"), os.path.join(CSRC, "gemm_route.hip")]
+           os.path.join(CSRC, "gemm_mx.hip"), os.path.join(CSRC, "gemm_route.hip"),
+           os.path.join(CSRC, "gemm_lora.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIPCC_FLAGS = [

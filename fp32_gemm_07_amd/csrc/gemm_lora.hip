@@ -1,0 +1,313 @@
+// The gemm_lora* entry points (declared and documented in gemm.h): argument checks,
+// choice of kernel, launches.
+#include "gemm.h"
+
+#include "host_checks.hpp"
+#include "host_shared.hpp"
+#include "lora_kernels.hpp"
+
+namespace {
+
+using namespace gemm::mx;
+using namespace gemm::host;
+
+static_assert(kLoraMaxRank == GEMM_LORA_MAX_RANK && kLoraMaxAdapters == GEMM_LORA_MAX_ADAPTERS, "adapter limits");
+
+// 16-column tiles of H for a rank: 1, 2, 4 or 8.
+int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+template <class F>
+void with_rank(int rank, F &&f) {
+  switch (rank_tiles(rank)) {
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    default: f(std::integral_constant<int, 8>()); break;
+  }
+}
+size_t up16(size_t bytes) { return (bytes + 15) / 16 * 16; }
+
+int check_set(int rows, const gemm_lora_t *s) {
+  if (!s) return GEMM_ERR_NULL_PTR;
+  if (rows < 0 || rows > GEMM_LORA_MAX_ROWS || s->K < 1 || s->K > GEMM_LORA_MAX_DIM || s->N < 1 ||
+      s->N > GEMM_LORA_MAX_DIM || s->rank < 1 || s->rank > kLoraMaxRank || s->adapters < 1 ||
+      s->adapters > kLoraMaxAdapters)
+    return GEMM_ERR_INVALID_DIM;
+  if (!valid_type(s->type)) return GEMM_ERR_INVALID_TYPE;
+  return GEMM_OK;
+}
+Range range_a(const gemm_lora_t &s) {
+  return {s.A, elem_size(s.type) * static_cast<size_t>(s.adapters) * s.rank * s.K};
+}
+Range range_b(const gemm_lora_t &s) {
+  return {s.B, elem_size(s.type) * static_cast<size_t>(s.adapters) * s.rank * s.N};
+}
+Range range_ranks(const gemm_lora_t &s) { return {s.ranks, s.ranks ? 4 * static_cast<size_t>(s.adapters) : 0}; }
+Range range_scales(const gemm_lora_t &s) { return {s.scales, s.scales ? 4 * static_cast<size_t>(s.adapters) : 0}; }
+bool aligned_set(const gemm_lora_t &s, const int *ids) {
+  return aligned(s.A, elem_size(s.type)) && aligned(s.B, elem_size(s.type)) && aligned(s.ranks, 4) &&
+         aligned(s.scales, 4) && aligned(ids, 4);
+}
+LoraRows rows_of(int rows, const gemm_lora_t &s, const int *ids) {
+  return LoraRows{rows, s.rank, s.adapters, ids, s.ranks, s.scales};
+}
+
+// Ranges that the columns of a shrink are cut into: workgroups of 16 rows alone would leave
+// most CUs idle below 16 * cus rows. At most 16, each of 256 columns at least; the expand adds
+// their sums up.
+int shrink_splits(int rows, int K, int cus) {
+  const long long tiles = std::max<long long>(1, ceil_div(rows, 16));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({2LL * cus / tiles, K / 256, 16})));
+}
+Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, int splits, float *h, void *parts) {
+  const int k_split = static_cast<int>(ceil_div(ceil_div(K, splits), 64) * 64);
+  return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, parts};
+}
+
+int launch_shrink(ShrinkArgs a, int problems, int type, hipStream_t stream) {
+  const long long tiles = ceil_div(a.r.rows, 16);
+  a.blocks0 = static_cast<int>(tiles * a.p[0].splits);
+  const long long blocks = a.blocks0 + (problems > 1 ? tiles * a.p[1].splits : 0);
+  with_type(type, [&](auto t) {
+    with_rank(a.r.rank, [&](auto rt) {
+      hipLaunchKernelGGL((shrink_kernel<decltype(t)::value, decltype(rt)::value, 1, 4>), dim3(static_cast<unsigned>(blocks)),
+                         dim3(256), 0, stream, a);
+    });
+  });
+  return launched();
+}
+
+template <int TYPE, int RT, bool TRANS, int J>
+void launch_expand_columns(ExpandArgs a, int cus, hipStream_t stream) {
+  const long long columns = ceil_div(a.N, 64 * J), tiles = ceil_div(a.r.rows, 16);
+  // Four workgroups a CU, then more row tiles for each: an adapter's columns stay in registers.
+  a.tiles = static_cast<int>(std::max<long long>(1, columns * tiles / (4LL * cus)));
+  hipLaunchKernelGGL((expand_kernel<TYPE, RT, TRANS, J>), dim3(static_cast<unsigned>(columns * ceil_div(tiles, a.tiles))),
+                     dim3(256), 0, stream, a);
+}
+template <bool TRANS>
+int launch_expand(const ExpandArgs &a, int type, int cus, hipStream_t stream) {
+  with_type(type, [&](auto t) {
+    with_rank(a.r.rank, [&](auto rt) {
+      constexpr int T = decltype(t)::value, RT = decltype(rt)::value, MOST = kExpandMost<T, TRANS>;
+      if constexpr (!TRANS) {
+        if (ceil_div(a.N, 64 * MOST) * ceil_div(a.r.rows, 16) < cus)
+          return launch_expand_columns<T, RT, false, 1>(a, cus, stream);
+      }
+      launch_expand_columns<T, RT, TRANS, MOST>(a, cus, stream);
+    });
+  });
+  return launched();
+}
+
+size_t forward_workspace(int rows, const gemm_lora_t &s, int cus) {
+  return up16(sizeof(float) * static_cast<size_t>(shrink_splits(rows, s.K, cus)) * rows * 16 * rank_tiles(s.rank));
+}
+
+// Runs body(workspace) on the caller's workspace or the library's.
+template <class F>
+int with_workspace(void *workspace, size_t need, int dev, hipStream_t stream, F &&body) {
+  if (workspace) return body(workspace);
+  return gemm::host_with_library_workspace(
+      dev, need, stream,
+      [](void *f, void *ws) { return ws ? (*static_cast<F *>(f))(ws) : static_cast<int>(GEMM_ERR_WORKSPACE); }, &body);
+}
+
+// ---------------------------------------------------------------------------
+// Backward.
+
+// Rows of a slot, the stretch of an adapter's rows that one workgroup sums over: as few as
+// fill the CUs twice (a slot's sums are written and read once more), 128 at least.
+int slot_rows(int rows, const gemm_lora_t &s, int cus) {
+  const int lane = s.type == GEMM_TYPE_F32 ? 4 : 8;
+  const long long blocks = ceil_div(s.K, 16 * lane) + ceil_div(s.N, 16 * lane);
+  int n = 128;
+  while (n < rows && ceil_div(rows, n) * blocks > 4LL * cus) n *= 2;
+  return n;
+}
+
+struct Backward {
+  size_t plan, slots, sums, order, position, g, parts_h, parts_g, bt, partial_a, partial_b, bytes;
+  int slot_rows, most_slots, positions;
+};
+Backward backward_layout(int rows, const gemm_lora_t &s, int cus) {
+  Backward l{};
+  const size_t rp = 16 * rank_tiles(s.rank), used = std::min(rows, s.adapters);
+  l.slot_rows = slot_rows(rows, s, cus);
+  l.most_slots = static_cast<int>(rows / l.slot_rows + used);
+  l.positions = static_cast<int>((rows + 31 * used + 31) / 32 * 32);
+  // partial sums of adapters with more rows than a slot
+  const size_t partials = 2 * static_cast<size_t>(rows) / l.slot_rows;
+  const size_t part = s.type == GEMM_TYPE_F32 ? 4 : 6;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up16(bytes);
+    return here;
+  };
+  l.plan = take(sizeof(LoraPlan));
+  l.slots = take(sizeof(Slot) * l.most_slots);
+  l.sums = take(sizeof(int2) * s.adapters);
+  l.order = take(sizeof(int) * l.positions);
+  l.position = take(sizeof(int) * rows);
+  l.g = take(sizeof(float) * rows * rp);
+  l.parts_h = take(part * rp * l.positions);
+  l.parts_g = take(part * rp * l.positions);
+  l.bt = take(range_b(s).bytes);
+  l.partial_a = take(sizeof(float) * partials * s.rank * s.K);
+  l.partial_b = take(sizeof(float) * partials * s.rank * s.N);
+  l.bytes = at;
+  return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set) {
+  if (check_set(rows, set) != GEMM_OK || rows == 0) return 0;
+  return forward_workspace(rows, *set, gemm::host_planning_cus());
+}
+
+int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
+              const void *C, int ldc, void *Y, int ldy, void *workspace, size_t workspace_bytes,
+              hipStream_t stream) {
+  int st = check_set(rows, set);
+  if (st != GEMM_OK) return st;
+  const gemm_lora_t &s = *set;
+  if (ldx < s.K || (C && ldc < s.N) || ldy < s.N) return GEMM_ERR_INVALID_DIM;
+  if (rows == 0) return GEMM_OK;
+  if (!s.A || !s.B || !ids || !X || !Y) return GEMM_ERR_NULL_PTR;
+  const size_t es = elem_size(s.type);
+  if (!aligned_set(s, ids) || !aligned(X, es) || !aligned(C, es) || !aligned(Y, es)) return GEMM_ERR_ALIGNMENT;
+  const bool in_place = C == Y && ldc == ldy;
+  const Range x = {X, extent(rows, s.K, ldx, s.type)}, c = {C, C ? extent(rows, s.N, ldc, s.type) : 0};
+  const Range y = {Y, extent(rows, s.N, ldy, s.type)}, id = {ids, 4 * static_cast<size_t>(rows)};
+  const Range in[] = {x, range_a(s), range_b(s), range_ranks(s), range_scales(s), id, {C, in_place ? 0 : c.bytes}};
+  const Range out[] = {y};
+  st = check_outputs(out, in);
+  if (st != GEMM_OK) return st;
+  const int cus = gemm::host_planning_cus();
+  const size_t need = forward_workspace(rows, s, cus);
+  st = check_workspace(workspace, workspace_bytes, need,
+                       {x, c, y, id, range_a(s), range_b(s), range_ranks(s), range_scales(s)});
+  if (st != GEMM_OK) return st;
+  int dev = 0, dev_cus = 0;
+  st = gemm::host_check_device(&dev, &dev_cus);
+  if (st != GEMM_OK) return st;
+  return with_workspace(workspace, need, dev, stream, [&](void *ws) {
+    const LoraRows r = rows_of(rows, s, ids);
+    const int splits = shrink_splits(rows, s.K, cus);
+    ShrinkArgs sa{};
+    sa.r = r;
+    sa.p[0] = shrink_of(X, ldx, s.A, s.rank, s.K, splits, static_cast<float *>(ws), nullptr);
+    const int launch_st = launch_shrink(sa, 1, s.type, stream);
+    if (launch_st != GEMM_OK) return launch_st;
+    const ExpandArgs ea{r, static_cast<const float *>(ws), splits, s.B, static_cast<long long>(s.rank) * s.N, s.rank,
+                        C, ldc, Y, ldy, s.N, 1, in_place};
+    return launch_expand<false>(ea, s.type, cus, stream);
+  });
+}
+
+size_t gemm_lora_backward_workspace_bytes(int rows, const gemm_lora_t *set) {
+  if (check_set(rows, set) != GEMM_OK) return 0;
+  return backward_layout(rows, *set, gemm::host_planning_cus()).bytes;
+}
+
+int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
+                       const void *dY, int lddy, const void *C, int ldc, void *dX, int lddx,
+                       float *dA, float *dB, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream) {
+  int st = check_set(rows, set);
+  if (st != GEMM_OK) return st;
+  const gemm_lora_t &s = *set;
+  if (ldx < s.K || lddy < s.N || (dX && C && ldc < s.K) || (dX && lddx < s.K)) return GEMM_ERR_INVALID_DIM;
+  if (!dX && !dA && !dB) return GEMM_OK;
+  if (!dA != !dB) return GEMM_ERR_NULL_PTR;
+  if (rows == 0 && !dA) return GEMM_OK;
+  if (rows > 0 && (!s.A || !s.B || !ids || !X || !dY)) return GEMM_ERR_NULL_PTR;
+  const size_t es = elem_size(s.type);
+  if (!aligned_set(s, ids) || !aligned(X, es) || !aligned(dY, es) || !aligned(C, es) || !aligned(dX, es) ||
+      !aligned(dA, 4) || !aligned(dB, 4))
+    return GEMM_ERR_ALIGNMENT;
+  const bool in_place = C == dX && ldc == lddx;
+  const Range x = {X, extent(rows, s.K, ldx, s.type)}, dy = {dY, extent(rows, s.N, lddy, s.type)};
+  const Range c = {C, dX && C ? extent(rows, s.K, ldc, s.type) : 0}, dx = {dX, dX ? extent(rows, s.K, lddx, s.type) : 0};
+  const Range id = {ids, 4 * static_cast<size_t>(rows)};
+  const size_t weights = sizeof(float) * static_cast<size_t>(s.adapters) * s.rank;
+  const Range da = {dA, dA ? weights * s.K : 0}, db = {dB, dB ? weights * s.N : 0};
+  const Range in[] = {x, dy, range_a(s), range_b(s), range_ranks(s), range_scales(s), id, {C, in_place ? 0 : c.bytes}};
+  const Range out[] = {dx, da, db};
+  st = check_outputs(out, in);
+  if (st != GEMM_OK) return st;
+  if (in_place && (gemm::host_overlaps(C, c.bytes, dA, da.bytes) || gemm::host_overlaps(C, c.bytes, dB, db.bytes)))
+    return GEMM_ERR_ALIAS;
+  const int cus = gemm::host_planning_cus();
+  const Backward l = backward_layout(rows, s, cus);
+  st = check_workspace(workspace, workspace_bytes, l.bytes,
+                       {x, dy, c, dx, da, db, id, range_a(s), range_b(s), range_ranks(s), range_scales(s)});
+  if (st != GEMM_OK) return st;
+  int dev = 0, dev_cus = 0;
+  st = gemm::host_check_device(&dev, &dev_cus);
+  if (st != GEMM_OK) return st;
+  return with_workspace(workspace, l.bytes, dev, stream, [&](void *ws) {
+    char *w = static_cast<char *>(ws);
+    const LoraRows r = rows_of(rows, s, ids);
+    LoraPlan *plan = reinterpret_cast<LoraPlan *>(w + l.plan);
+    Slot *slots = reinterpret_cast<Slot *>(w + l.slots);
+    int2 *sums = reinterpret_cast<int2 *>(w + l.sums);
+    int *order = reinterpret_cast<int *>(w + l.order), *position = reinterpret_cast<int *>(w + l.position);
+    const int bt_tiles = static_cast<int>(std::min<long long>(ceil_div(s.N, kTransRows), 256));
+    const PrepareArgs pa{r, l.slot_rows, s.N, plan, slots, sums, order, position, s.B, w + l.bt, bt_tiles};
+    with_type(s.type, [&](auto t) {
+      hipLaunchKernelGGL(prepare_kernel<decltype(t)::value>,
+                         dim3(static_cast<unsigned>(1 + (rows ? s.adapters * bt_tiles : 0))), dim3(1024), 0, stream, pa);
+    });
+    int launch_st = launched();
+    if (launch_st != GEMM_OK) return launch_st;
+    float *g = reinterpret_cast<float *>(w + l.g);
+    if (rows > 0) {
+      ShrinkArgs sa{};
+      sa.r = r;
+      sa.position = position;
+      sa.positions = l.positions;
+      sa.p[0] = shrink_of(dY, lddy, w + l.bt, s.rank, s.N, 1, dX ? g : nullptr, dA ? w + l.parts_g : nullptr);
+      if (dA) sa.p[1] = shrink_of(X, ldx, s.A, s.rank, s.K, 1, nullptr, w + l.parts_h);
+      launch_st = launch_shrink(sa, dA ? 2 : 1, s.type, stream);
+      if (launch_st != GEMM_OK) return launch_st;
+      if (dX) {
+        const ExpandArgs ea{r, g, 1, s.A, static_cast<long long>(s.rank) * s.K, s.K, C, ldc, dX, lddx, s.K, 1, in_place};
+        launch_st = launch_expand<true>(ea, s.type, cus, stream);
+        if (launch_st != GEMM_OK) return launch_st;
+      }
+    }
+    if (!dA) return launch_st;
+    float *partial_a = reinterpret_cast<float *>(w + l.partial_a), *partial_b = reinterpret_cast<float *>(w + l.partial_b);
+    if (rows > 0) {
+      const int lane = s.type == kF32 ? 4 : 8;
+      const int blocks0 = static_cast<int>(ceil_div(s.K, 16 * lane)), blocks = blocks0 + static_cast<int>(ceil_div(s.N, 16 * lane));
+      GradArgs ga{r, plan, slots, order, l.positions,
+                  {{X, ldx, s.K, w + l.parts_g, partial_a, dA}, {dY, lddy, s.N, w + l.parts_h, partial_b, dB}},
+                  blocks0, blocks, 0, 16 * rank_tiles(s.rank), s.rank > 64 ? 2 : 1};
+      const long long slot_blocks = static_cast<long long>(blocks) * ga.rank_blocks;
+      launch_st = in_ranges(l.most_slots, max_blocks(256) / slot_blocks, [&](long long slot0, int count) {
+        ga.slot0 = static_cast<int>(slot0);
+        with_type(s.type, [&](auto t) {
+          with_rank(std::min(s.rank, 64), [&](auto rt) {
+            if constexpr (decltype(rt)::value <= 4)
+              hipLaunchKernelGGL((grad_kernel<decltype(t)::value, decltype(rt)::value>),
+                                 dim3(static_cast<unsigned>(count * slot_blocks)), dim3(256), 0, stream, ga);
+          });
+        });
+        return launched();
+      });
+      if (launch_st != GEMM_OK) return launch_st;
+    }
+    const long long size_a = static_cast<long long>(s.rank) * s.K, size_b = static_cast<long long>(s.rank) * s.N;
+    const int blocks = static_cast<int>(std::min<long long>(ceil_div(std::max(size_a, size_b), 1024), 64));
+    const GradSumArgs ga{sums, {partial_a, partial_b}, {dA, dB}, {size_a, size_b}, blocks};
+    hipLaunchKernelGGL(grad_sum_kernel, dim3(static_cast<unsigned>(2 * blocks * s.adapters)), dim3(256), 0, stream, ga);
+    return launched();
+  });
+}
+
+}  // extern "C"

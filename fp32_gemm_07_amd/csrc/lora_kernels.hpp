@@ -1,0 +1,761 @@
+// Low-rank adapters beside a shared projection: every row of X has an adapter of its own
+// (the operations are described in gemm.h at gemm_lora and gemm_lora_backward).
+//   shrink:  H = s X A^T          rows x rank, FP32
+//   expand:  Y = C + H B^T
+// and backward, with B transposed once (few bytes) so that shrink serves both ways:
+//   shrink:  H = s X A^T,  G = s dY B
+//   expand:  dX = C' + G A
+//   grads:   dA = G^T X,  dB = dY^T H, sums over the rows of one adapter.
+// A rank is far below the balance of the matrix units, so all of these are bound by the
+// bytes of X, C and Y (dY, dX): each is read or written once a kernel, straight
+// between memory and registers. What is small (adapters, H, G) comes from L2.
+//
+// Rows are taken 16 at a time, the columns of 16x16 matrix instructions. The rows of a tile
+// mostly have one adapter (prompts packed one behind the other); where they have
+// several, the tile is worked out for each and every row keeps its own. An
+// instruction's columns do not mix, so what another adapter holds, NaN included,
+// never reaches a row.
+//
+// Precision: products of 16-bit inputs are exact and summed in FP32. H and G stay FP32:
+// they enter the second products as three bfloat16 parts whose sum is exact. FP32
+// inputs go through FP32 matrix instructions throughout.
+#pragma once
+
+#include "gemm_kernels.hpp"
+#include "mx_moe.hpp"
+
+namespace gemm {
+namespace mx {
+
+constexpr int kLoraMaxRank = 128, kLoraMaxAdapters = 1024;   // GEMM_LORA_MAX_*
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// What every kernel knows of the adapters: each row's, its rank and its scale.
+struct LoraRows {
+  int rows, rank, adapters;
+  const int *ids;
+  const int *ranks;      // null: all `rank`
+  const float *scales;   // null: all 1
+  __device__ inline int id(int row) const {   // -1: none
+    if (row >= rows) return -1;
+    const int a = ids[row];
+    return a >= 0 && a < adapters ? a : -1;
+  }
+  __device__ inline int rank_of(int a) const { return ranks ? max(0, min(rank, ranks[a])) : rank; }
+};
+
+// 16 bytes of a row as an operand of a matrix instruction: 8 values of 16 bits (k = 8g ..
+// 8g + 7 of 32), or 4 floats, one for each of 4 instructions (k = 4g .. 4g + 3 of 16).
+template <int TYPE>
+constexpr int kLaneK = TYPE == kF32 ? 4 : 8;
+
+template <int TYPE>
+__device__ inline uintx4 load_k(const typename Elem<TYPE>::store *p) {
+  return *reinterpret_cast<const uintx4_any *>(p);
+}
+// The same at a row's end: `left` values (may be negative), zeros behind them.
+template <int TYPE>
+__device__ inline uintx4 load_k(const typename Elem<TYPE>::store *p, int left) {
+  if (left >= kLaneK<TYPE>) return load_k<TYPE>(p);
+  uintx4 v = {};
+  if constexpr (TYPE == kF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) v[i] = __builtin_bit_cast(unsigned, p[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) v[i / 2] |= static_cast<unsigned>(p[i]) << (16 * (i % 2));
+  }
+  return v;
+}
+template <int TYPE>
+__device__ inline f32x4 multiply(const uintx4 &a, const uintx4 &b, f32x4 acc) {
+  if constexpr (TYPE == kBf16) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  } else if constexpr (TYPE == kF16) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned x = a[i], y = b[i];
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y), acc, 0, 0, 0);
+    }
+  }
+  return acc;
+}
+
+// 8 floats, 4 to a register quad, as operands of a kind that multiplies them with TYPE.
+__device__ inline void floats8(const f32x4 &a, const f32x4 &b, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+// 8 halfs as two bfloat16 parts (exact: 11 bits in 8 and 8).
+__device__ inline void split_halfs(const uintx4 &h, bf16x8 (&out)[2]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned w = h[i];
+    v[2 * i] = Elem<kF16>::get(static_cast<u16>(w));
+    v[2 * i + 1] = Elem<kF16>::get(static_cast<u16>(w >> 16));
+  }
+  split8<2>(v, out);
+}
+
+// ---------------------------------------------------------------------------
+// shrink.
+struct Shrink {
+  const void *z;       // rows x K
+  long long ldz;
+  const void *w;       // adapter a's rank x K at w + a * w_adapter, row stride ldw
+  long long w_adapter, ldw;
+  int K, k_split;      // columns of a workgroup's range, a multiple of 64
+  int splits;
+  float *h;            // [split][rows][RP] sums of each range, or null
+  void *parts;         // for the gradients: [3][RP][positions] bfloat16 parts ([RP][positions] floats), or null
+};
+struct ShrinkArgs {
+  LoraRows r;
+  Shrink p[2];         // blocks of p[0] first
+  int blocks0;
+  const int *position; // of each row among the rows sorted by adapter (with parts)
+  int positions;
+};
+
+// One workgroup: 16 MT rows, a range of K. With S ranges for each of the D adapters that
+// its rows have (S = W / D), wave d S + s sums range s for adapter d; where there are more
+// adapters than waves a wave takes several.
+template <int TYPE, int RT, int MT, int W>
+__global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
+  typedef typename Elem<TYPE>::store store;
+  constexpr int RP = 16 * RT, kLane = kLaneK<TYPE>, kChunk = 4 * kLane;
+  constexpr int U = RT * MT >= 8 ? 2 : 4;   // chunks at a time
+  __shared__ __attribute__((aligned(16))) f32x4 sums[W * MT * RT * 64];
+  const bool second = static_cast<int>(blockIdx.x) >= a.blocks0;
+  const Shrink p = second ? a.p[1] : a.p[0];
+  const int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
+  const int split = block % p.splits;
+  const int row0 = block / p.splits * (16 * MT);
+  const int k0 = split * p.k_split, k1 = min(p.K, k0 + p.k_split);
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Lane l < 16 MT knows row l's adapter.
+  const int my_id = lane < 16 * MT ? a.r.id(row0 + lane) : -1;
+  const unsigned long long live = __ballot(my_id >= 0);
+  int D = 0, my_d = 0;
+  for (unsigned long long todo = live; todo; ++D) {
+    const int id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
+    const unsigned long long same = __ballot(my_id == id);
+    if (my_id == id) my_d = D;
+    todo &= ~same;
+  }
+  if (D == 0) return;
+  const int S = D >= W ? 1 : W / D;
+  const int k_slice = ((k1 - k0 + S - 1) / S + 63) / 64 * 64;
+
+  // Sums of a range of K for one adapter, in the layout of the instruction: value v of lane
+  // (g, i16) is column 4g + v of H for row i16.
+  auto sum_range = [&](int id, unsigned long long mask, int ka, int kb, f32x4 (&acc)[MT][RT]) __attribute__((always_inline)) {
+    const int rank = a.r.rank_of(id);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[m][t] = f32x4{};
+    if (rank == 0) return;
+    const store *w = static_cast<const store *>(p.w) + id * p.w_adapter + g * kLane;
+    const store *wr[RT], *zr[MT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) wr[t] = w + min(t * 16 + i16, rank - 1) * p.ldw;   // (past the rank: not kept)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      zr[m] = static_cast<const store *>(p.z) + static_cast<long long>(min(row0 + m * 16 + i16, a.r.rows - 1)) * p.ldz + g * kLane;
+    int k = ka;
+    for (; k + U * kChunk <= kb; k += U * kChunk) {
+      uintx4 wv[U][RT], zv[U][MT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) zv[u][m] = load_k<TYPE>(zr[m] + k + u * kChunk);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) wv[u][t] = load_k<TYPE>(wr[t] + k + u * kChunk);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(wv[u][t], zv[u][m], acc[m][t]);
+    }
+    for (; k < kb; k += kChunk) {
+      const int left = kb - k - g * kLane;
+      uintx4 wv[RT], zv[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) zv[m] = load_k<TYPE>(zr[m] + k, left);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) wv[t] = load_k<TYPE>(wr[t] + k, left);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(wv[t], zv[m], acc[m][t]);
+    }
+  };
+  // 4 neighbouring columns of H for one row, scaled, zeros past the rank.
+  auto keep = [&](int id, int row, int t, f32x4 v) __attribute__((always_inline)) {
+    const int rank = a.r.rank_of(id);
+    const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = t * 16 + 4 * g + i < rank ? v[i] * scale : 0.0f;
+    if (p.h)
+      *reinterpret_cast<f32x4 *>(p.h + (static_cast<long long>(split) * a.r.rows + row) * RP + t * 16 + 4 * g) = v;
+    if (p.parts) {
+      const int at = a.position[row];
+      const long long plane = static_cast<long long>(RP) * a.positions;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long to = static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at;
+        if constexpr (TYPE == kF32) {
+          static_cast<float *>(p.parts)[to] = v[i];
+        } else {
+          float rest = v[i];
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const u16 part = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
+            static_cast<u16 *>(p.parts)[q * plane + to] = part;
+            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
+          }
+        }
+      }
+    }
+  };
+
+  int d = 0;
+  for (unsigned long long todo = live; todo; ++d) {
+    const int id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
+    const unsigned long long same = __ballot(my_id == id);
+    todo &= ~same;
+    if (S == 1 ? d % W != wave : d != wave / S) continue;
+    const int s = S == 1 ? 0 : wave % S;
+    f32x4 acc[MT][RT];
+    sum_range(id, same, min(k1, k0 + s * k_slice), min(k1, k0 + (s + 1) * k_slice), acc);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (S > 1) sums[((wave * MT + m) * RT + t) * 64 + lane] = acc[m][t];
+        else if (same >> (m * 16 + i16) & 1) keep(id, row0 + m * 16 + i16, t, acc[m][t]);
+      }
+  }
+  if (S == 1) return;
+  __syncthreads();
+  for (int n = wave; n < MT * RT; n += W) {
+    const int m = n / RT, t = n % RT;
+    const int id = __shfl(my_id, m * 16 + i16), at = __shfl(my_d, m * 16 + i16);
+    if (id < 0) continue;
+    f32x4 v = sums[((at * S * MT + m) * RT + t) * 64 + lane];
+    for (int s = 1; s < S; ++s) v += sums[(((at * S + s) * MT + m) * RT + t) * 64 + lane];
+    keep(id, row0 + m * 16 + i16, t, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// expand.
+struct ExpandArgs {
+  LoraRows r;
+  const float *h;          // [splits][rows][RP]
+  int splits;
+  const void *w;           // adapter a's matrix at w + a * w_adapter: N x rank, row stride ldw;
+  long long w_adapter, ldw;   // rank x N for TRANS
+  const void *c;           // null: zeros
+  long long ldc;
+  void *y;
+  long long ldy;
+  int N, tiles;            // row tiles of a workgroup
+  bool in_place;           // c is y
+};
+
+// Columns of Y that a wave has at one time: 16 J, and consecutive ones of a lane.
+template <int TYPE, bool TRANS>
+constexpr int kExpandMost = TRANS && TYPE != kF32 ? 8 : 4;
+
+// A wave keeps 16 J rows of an adapter's B (columns of its A) in registers and takes row
+// tile after row tile; they are loaded again where the adapter changes. Row m of
+// instruction j is column 4 J (m / 4) + 4 j + m % 4 of the wave's, or for TRANS, where a lane loads
+// J neighbouring columns of several ranks, column J m + j: either way the results
+// of a lane are 4 J neighbouring columns of one row of Y.
+template <int TYPE, int RT, bool TRANS, int J>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
+  typedef typename Elem<TYPE>::store store;
+  constexpr int RP = 16 * RT, COLS = 4 * J;
+  constexpr int KS = TYPE == kF32 ? RT : (RT + 1) / 2;   // operands along the rank: of 16 or 32
+  constexpr int PB = TYPE == kF16 ? 2 : 1;               // parts of B
+  constexpr int PH = TYPE == kF32 ? 1 : 3;               // parts of H
+  static_assert(!TRANS || J == kExpandMost<TYPE, TRANS>, "a lane's load");
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col_blocks = (a.N + 64 * J - 1) / (64 * J);
+  const int nb = (blockIdx.x % col_blocks * 4 + wave) * 16 * J;
+  if (nb >= a.N) return;
+  const int tile0 = blockIdx.x / col_blocks * a.tiles;
+  const int n_lane = nb + COLS * g, left = a.N - n_lane;
+
+  uintx4 b[J][KS][PB];
+  int have = -1;
+  auto load_adapter = [&](int id) __attribute__((always_inline)) {
+    const int rank = a.r.rank_of(id);
+    const store *w = static_cast<const store *>(a.w) + id * a.w_adapter;
+    constexpr int kLane = kLaneK<TYPE>;
+    if constexpr (!TRANS) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int n = min(nb + COLS * (i16 >> 2) + 4 * j + (i16 & 3), a.N - 1);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int r = s * 4 * kLane + g * kLane;
+          b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, rank - r);
+        }
+      }
+    } else {
+      // kLane ranks, J neighbouring columns of each
+      const int n = nb + J * i16;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uintx4 x[kLane];
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+          const int r = s * 4 * kLane + g * kLane + i;
+          x[i] = load_k<TYPE>(w + r * a.ldw + n, r < rank ? a.N - n : 0);
+        }
+        if constexpr (TYPE == kF32) {
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[j][s][0][i] = x[i][j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              b[j][s][0][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302 : 0x05040100);
+        }
+      }
+    }
+    if constexpr (PB == 2) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          bf16x8 parts[2];
+          split_halfs(b[j][s][0], parts);
+          b[j][s][0] = __builtin_bit_cast(uintx4, parts[0]);
+          b[j][s][1] = __builtin_bit_cast(uintx4, parts[1]);
+        }
+    }
+  };
+
+  for (int tile = tile0; tile < tile0 + a.tiles && tile * 16 < a.r.rows; ++tile) {
+    const int row = tile * 16 + i16;
+    const int id = a.r.id(row);
+    unsigned long long todo = __ballot(id >= 0) & 0xffff;
+    if (!todo && a.in_place) continue;
+    float out[COLS];
+    const store *c = static_cast<const store *>(a.c) + static_cast<long long>(min(row, a.r.rows - 1)) * a.ldc + n_lane;
+    if (a.c) {
+      if constexpr (COLS >= 8) {
+#pragma unroll
+        for (int q = 0; q < COLS; q += 8) load8<TYPE>(c + q, left - q, reinterpret_cast<float(&)[8]>(out[q]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) out[q] = q < left ? Elem<TYPE>::get(c[q]) : 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) out[q] = 0.0f;
+    }
+    if (todo) {
+      // H of the row, in operands.
+      uintx4 h[KS][PH];
+      const float *hr = a.h + static_cast<long long>(min(row, a.r.rows - 1)) * RP;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        constexpr int kLane = kLaneK<TYPE>;
+        const int r = s * 4 * kLane + g * kLane;
+        f32x4 v[2] = {};
+        if (r < RP) {   // (the upper half of 32 where RP is 16: zeros)
+          for (int q = 0; q < a.splits; ++q) {
+            const float *part = hr + static_cast<long long>(q) * a.r.rows * RP + r;
+#pragma unroll
+            for (int i = 0; i < kLane / 4; ++i) v[i] += reinterpret_cast<const f32x4 *>(part)[i];
+          }
+        }
+        if constexpr (TYPE == kF32) {
+          h[s][0] = __builtin_bit_cast(uintx4, v[0]);
+        } else {
+          float x[8];
+          floats8(v[0], v[1], x);
+          bf16x8 parts[3];
+          split8<3>(x, parts);
+#pragma unroll
+          for (int q = 0; q < PH; ++q) h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
+        }
+      }
+      while (todo) {
+        const int which = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        todo &= ~__ballot(id == which);
+        if (which != have) {
+          load_adapter(which);
+          have = which;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          // first: the products of the first parts; where their sum is not finite it is
+          // the result (the other parts of an infinity, or its products with zeros, are NaN)
+          f32x4 first = {}, rest = {};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if constexpr (TYPE == kF32) {
+              first = multiply<kF32>(b[j][s][0], h[s][0], first);
+            } else {
+              first = multiply<kBf16>(b[j][s][0], h[s][0], first);
+#pragma unroll
+              for (int q = 1; q < PH; ++q) rest = multiply<kBf16>(b[j][s][0], h[s][q], rest);
+              if constexpr (PB == 2) {   // (the third part of H times the second of B is below 2^-24)
+                rest = multiply<kBf16>(b[j][s][1], h[s][0], rest);
+                rest = multiply<kBf16>(b[j][s][1], h[s][1], rest);
+              }
+            }
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int q = TRANS ? J * v + j : 4 * j + v;
+            const float sum = TYPE == kF32 || !__builtin_isfinite(first[v]) ? first[v] : first[v] + rest[v];
+            out[q] = id == which ? out[q] + sum : out[q];   // (adding zero would lose -0)
+          }
+        }
+      }
+    }
+    if (row < a.r.rows && (id >= 0 || !a.in_place)) {
+      store *y = static_cast<store *>(a.y) + static_cast<long long>(row) * a.ldy + n_lane;
+      if constexpr (COLS >= 8) {
+#pragma unroll
+        for (int q = 0; q < COLS; q += 8) store8<TYPE>(y + q, left - q, reinterpret_cast<float(&)[8]>(out[q]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < COLS; ++q)
+          if (q < left) y[q] = Elem<TYPE>::put(out[q]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: the rows sorted by adapter, and B transposed.
+
+// A stretch of up to `slot_rows` rows of one adapter, in the sorted order.
+struct Slot {
+  int adapter, first, count;   // positions
+  int partial;                 // where its sums go: -1 straight to the gradient, else a partial sum
+};
+struct LoraPlan {
+  int slots, pad[3];
+};
+struct PrepareArgs {
+  LoraRows r;
+  int slot_rows, N;
+  LoraPlan *plan;
+  Slot *slots;
+  int2 *sums;           // adapter: its first partial sum, how many (-1: written straight)
+  int *order;           // position -> row
+  int *position;        // row -> position
+  const void *b;        // N x rank for each adapter
+  void *bt;             // rank x N for each
+  int bt_tiles;         // workgroups for each adapter's
+};
+constexpr int kTransRows = 64;   // rows of B of a transposing workgroup
+
+// Lanes of the wave that have the same id (valid ones).
+__device__ inline unsigned long long same_id(int id, bool valid, int bits) {
+  unsigned long long m = __ballot(valid);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (id >> b) & 1;
+    const unsigned long long ones = __ballot(one);
+    m &= one ? ones : ~ones;
+  }
+  return m;
+}
+
+// Workgroup 0 sorts the rows by adapter, keeping their order (so that sums over them do not
+// depend on timing): every wave counts a stretch of rows, running sums over adapters and
+// waves say where each wave's rows of an adapter go, and each wave puts its
+// rows there. An adapter's positions begin at a multiple of 32. The other workgroups transpose 64
+// rows of one adapter's B each, if any row has that adapter.
+template <int TYPE>
+__global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
+  typedef typename Elem<TYPE>::store store;
+  constexpr int W = 16;
+  __shared__ int lds[W * kLoraMaxAdapters + 3 * 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.x > 0) {
+    const int id = (blockIdx.x - 1) / a.bt_tiles;
+    int n0 = (blockIdx.x - 1) % a.bt_tiles * kTransRows;
+    bool used = false;
+    for (int row = threadIdx.x; row < a.r.rows; row += 1024) used |= a.r.ids[row] == id;
+    if (!__syncthreads_or(used)) return;
+    store *tile = reinterpret_cast<store *>(lds);
+    const int rank = a.r.rank;
+    for (; n0 < a.N; n0 += a.bt_tiles * kTransRows) {
+      const store *b = static_cast<const store *>(a.b) + (static_cast<long long>(id) * a.N + n0) * rank;
+      store *bt = static_cast<store *>(a.bt) + static_cast<long long>(id) * rank * a.N + n0;
+      const int many = min(kTransRows, a.N - n0);
+      for (int i = threadIdx.x; i < many * rank; i += 1024) tile[(i % rank) * (kTransRows + 1) + i / rank] = b[i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < kTransRows * rank; i += 1024) {
+        const int n = i % kTransRows, r = i / kTransRows;
+        if (n < many) bt[static_cast<long long>(r) * a.N + n] = tile[r * (kTransRows + 1) + n];
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  int *count = lds, *across = lds + W * kLoraMaxAdapters;   // [wave][adapter]; sums over the waves' adapters
+  const int bits = 32 - __builtin_clz(max(a.r.adapters - 1, 1));
+  for (int i = threadIdx.x; i < W * kLoraMaxAdapters; i += 1024) count[i] = 0;
+  __syncthreads();
+  const int per = ((a.r.rows + W - 1) / W + 63) / 64 * 64;
+  const int from = min(a.r.rows, wave * per), to = min(a.r.rows, from + per);
+  for (int row0 = from; row0 < to; row0 += 64) {
+    const int id = row0 + lane < to ? a.r.id(row0 + lane) : -1;
+    const unsigned long long same = same_id(id, id >= 0, bits);
+    if (id >= 0 && (same & ((1ull << lane) - 1)) == 0) count[wave * kLoraMaxAdapters + id] += __popcll(same);
+    wave_order();
+  }
+  __syncthreads();
+  // Thread t has adapter t: its rows, positions (rounded up to 32), slots and partial sums,
+  // and running sums of the last three over all adapters.
+  const int id = threadIdx.x;
+  int rows = 0;
+  if (id < a.r.adapters) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int n = count[w * kLoraMaxAdapters + id];
+      count[w * kLoraMaxAdapters + id] = rows;
+      rows += n;
+    }
+  }
+  const int slots = (rows + a.slot_rows - 1) / a.slot_rows;
+  int v[3] = {(rows + 31) / 32 * 32, slots, slots > 1 ? slots : 0}, before[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int upto = wave_running_sum(v[i]);
+    before[i] = upto - v[i];
+    if (lane == 63) across[i * W + wave] = upto;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    for (int w = 0; w < wave; ++w) before[i] += across[i * W + w];
+  if (threadIdx.x == 1023) a.plan->slots = before[1] + v[1];
+  if (id < a.r.adapters) {
+    for (int s = 0; s < slots; ++s)
+      a.slots[before[1] + s] = Slot{id, before[0] + s * a.slot_rows, min(a.slot_rows, rows - s * a.slot_rows),
+                                    slots > 1 ? before[2] + s : -1};
+    a.sums[id] = make_int2(before[2], slots == 1 ? -1 : slots);
+#pragma unroll
+    for (int w = 0; w < W; ++w) count[w * kLoraMaxAdapters + id] += before[0];
+  }
+  __syncthreads();
+  for (int row0 = from; row0 < to; row0 += 64) {
+    const int row = row0 + lane;
+    const int mine = row < to ? a.r.id(row) : -1;
+    const unsigned long long same = same_id(mine, mine >= 0, bits);
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    if (mine >= 0) {
+      const int at = count[wave * kLoraMaxAdapters + mine] + rank;
+      a.order[at] = row;
+      a.position[row] = at;
+    }
+    wave_order();
+    if (mine >= 0 && rank == 0) count[wave * kLoraMaxAdapters + mine] += __popcll(same);
+    wave_order();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// grads.
+struct Grad {
+  const void *z;         // rows x cols: X, or dY
+  long long ldz;
+  int cols;
+  const void *parts;     // of G, or H
+  float *partial;        // [partial sum][cols x rank or rank x cols]
+  float *out;            // the same for each adapter
+};
+struct GradArgs {
+  LoraRows r;
+  const LoraPlan *plan;
+  const Slot *slots;
+  const int *order;
+  int positions;
+  Grad p[2];             // dA: rank x cols; dB: cols x rank
+  int blocks0, blocks;   // column blocks of the first, of both
+  int slot0;             // of the launch
+  int rp, rank_blocks;   // ranks of `parts`, and the stretches of 16 RT that they are taken in
+};
+
+// One workgroup: a slot's rows, 16 CL columns (CL of a lane) and 16 RT ranks (128 ranks
+// would not fit the registers: two workgroups share them). Its waves take 32 rows (16 of
+// FP32) in turn, and their sums are added in order at the end. A lane loads CL neighbouring columns of 8 rows
+// (4 of FP32): turned in its registers, these are the operands of CL instructions, whose
+// column i16 is column CL i16 + j.
+template <int TYPE, int RT>
+__global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
+  typedef typename Elem<TYPE>::store store;
+  constexpr int CL = kLaneK<TYPE>, kRows = kLaneK<TYPE>, kStep = 4 * kRows;
+  constexpr int PZ = TYPE == kF16 ? 2 : 1, PP = TYPE == kF32 ? 1 : 3;
+  __shared__ __attribute__((aligned(16))) f32x4 sums[CL * RT * 64];
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slot_at = a.slot0 + blockIdx.x / (a.blocks * a.rank_blocks);
+  const int rank0 = blockIdx.x % a.rank_blocks * (16 * RT);
+  int block = blockIdx.x / a.rank_blocks % a.blocks;
+  if (slot_at >= a.plan->slots) return;
+  const bool second = block >= a.blocks0;
+  const Grad p = second ? a.p[1] : a.p[0];
+  if (second) block -= a.blocks0;
+  const Slot slot = a.slots[slot_at];
+  const int n = (block * 16 + i16) * CL, left = p.cols - n;
+  const long long plane = static_cast<long long>(a.rp) * a.positions;
+  f32x4 acc[CL][RT] = {};
+  for (int at = wave * kStep; at < slot.count; at += 4 * kStep) {
+    const int first = at + g * kRows;   // of the lane's rows
+    uintx4 x[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      // (rows past the last: zeros on both sides)
+      const bool real = first + i < slot.count;
+      const int row = a.order[slot.first + min(first + i, slot.count - 1)];
+      x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + row * p.ldz + n, real ? left : 0);
+    }
+    uintx4 pv[RT][PP];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int q = 0; q < PP; ++q) {
+        const long long from = (rank0 + t * 16 + i16) * static_cast<long long>(a.positions) + slot.first + first;
+        const int real = slot.count - first;
+        uintx4 v;
+        if constexpr (TYPE == kF32) {
+          v = *reinterpret_cast<const uintx4 *>(static_cast<const float *>(p.parts) + from);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = i < real ? v[i] : 0;
+        } else {
+          v = *reinterpret_cast<const uintx4 *>(static_cast<const u16 *>(p.parts) + q * plane + from);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < real ? v[i] : 2 * i < real ? v[i] & 0xffff : 0;
+        }
+        pv[t][q] = v;
+      }
+#pragma unroll
+    for (int j = 0; j < CL; ++j) {
+      uintx4 z[PZ];
+      if constexpr (TYPE == kF32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[0][i] = x[i][j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[0][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302 : 0x05040100);
+        if constexpr (PZ == 2) {
+          bf16x8 parts[2];
+          split_halfs(z[0], parts);
+          z[0] = __builtin_bit_cast(uintx4, parts[0]);
+          z[1] = __builtin_bit_cast(uintx4, parts[1]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if constexpr (TYPE == kF32) {
+          acc[j][t] = multiply<kF32>(pv[t][0], z[0], acc[j][t]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < PP; ++q) acc[j][t] = multiply<kBf16>(pv[t][q], z[0], acc[j][t]);
+          if constexpr (PZ == 2) {   // (the third part times the second is below 2^-24)
+            acc[j][t] = multiply<kBf16>(pv[t][0], z[1], acc[j][t]);
+            acc[j][t] = multiply<kBf16>(pv[t][1], z[1], acc[j][t]);
+          }
+        }
+      }
+    }
+  }
+  // The waves' sums in order.
+  for (int w = 3; w > 0; --w) {
+    __syncthreads();
+    if (wave == w) {
+#pragma unroll
+      for (int j = 0; j < CL; ++j)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) sums[(j * RT + t) * 64 + lane] = acc[j][t];
+    }
+    __syncthreads();
+    if (wave == w - 1) {
+#pragma unroll
+      for (int j = 0; j < CL; ++j)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[j][t] += sums[(j * RT + t) * 64 + lane];
+    }
+  }
+  if (wave != 0) return;
+  const long long size = static_cast<long long>(a.r.rank) * p.cols;
+  float *out = slot.partial < 0 ? p.out + slot.adapter * size : p.partial + slot.partial * size;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = rank0 + t * 16 + 4 * g + v;
+      if (r >= a.r.rank) continue;
+#pragma unroll
+      for (int j = 0; j < CL; ++j)
+        if (j < left) out[second ? static_cast<long long>(n + j) * a.r.rank + r : static_cast<long long>(r) * p.cols + n + j] = acc[j][t][v];
+    }
+}
+
+// Gradients of the adapters with several slots, whose partial sums are added in order, and
+// zeros for those that no row has.
+struct GradSumArgs {
+  const int2 *sums;
+  const float *partial[2];
+  float *out[2];
+  long long size[2];     // of one adapter's
+  int blocks;            // workgroups for each adapter's, of each of the two
+};
+__global__ __launch_bounds__(256) void grad_sum_kernel(GradSumArgs a) {
+  const int id = blockIdx.x / (2 * a.blocks), block = blockIdx.x % (2 * a.blocks);
+  const int2 s = a.sums[id];
+  if (s.y < 0) return;
+  const bool second = block >= a.blocks;
+  const long long size = second ? a.size[1] : a.size[0];
+  const float *partial = (second ? a.partial[1] : a.partial[0]) + s.x * size;
+  float *out = (second ? a.out[1] : a.out[0]) + id * size;
+  const long long first = (static_cast<long long>(second ? block - a.blocks : block) * 256 + threadIdx.x) * 4;
+  for (long long at = first; at < size; at += a.blocks * 1024LL) {
+    if (at + 4 <= size) {
+      typedef f32x4 f32x4_any __attribute__((aligned(4)));
+      f32x4 v = {};
+      for (int i = 0; i < s.y; ++i) v += *reinterpret_cast<const f32x4_any *>(partial + i * size + at);
+      *reinterpret_cast<f32x4_any *>(out + at) = v;
+    } else {
+      for (long long k = at; k < size; ++k) {
+        float v = 0.0f;
+        for (int i = 0; i < s.y; ++i) v += partial[i * size + k];
+        out[k] = v;
+      }
+    }
+  }
+}
+
+}  // namespace mx
+}  // namespace gemm

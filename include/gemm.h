@@ -463,6 +463,64 @@ int gemm_route_backward(int tokens, const gemm_route_t *router, const void *logi
                         int logits_type, int ld_logits, const int *chosen, const float *dweights,
                         void *dlogits, int ld_dlogits, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters beside a shared projection: every row has an adapter of its own, so that
+ * one call serves (or trains on) the rows of many requests.
+ *
+ *   Y[i] = C[i] + s_a B_a (A_a X[i]),   a = ids[i]
+ *
+ * C is what the shared projection gives (gemm_f32, gemm_mx, ...). A_a is rank x K and
+ * B_a N x rank, stored one adapter after the other:
+ *   element (r, k) of A_a at A[(a*rank + r)*K + k], (n, r) of B_a at B[(a*N + n)*rank + r].
+ * ranks (null: all `rank`; else `adapters` of them in device memory, each taken as at least 0
+ * and at most `rank`) says how many of the stored ranks an adapter has: what is
+ * stored behind them is not used. scales (null: all 1; else `adapters` floats in
+ * device memory) holds the s_a. A row whose id lies outside 0 .. adapters - 1 has no
+ * adapter: Y[i] = C[i].
+ * X, C, Y, A and B have the same type; sums and the products A_a X[i] are FP32 (with
+ * 16-bit types they enter the second product as three bfloat16 parts, which cut values
+ * below 2^-110 off to a multiple of 2^-133), rounded once at the end. A row's result does not
+ * depend on the other rows, and is the same from run to run.
+ */
+enum {
+  GEMM_LORA_MAX_ROWS = 1 << 20,
+  GEMM_LORA_MAX_DIM = 1 << 18,      /* K, N */
+  GEMM_LORA_MAX_RANK = 128,
+  GEMM_LORA_MAX_ADAPTERS = 1024
+};
+typedef struct gemm_lora {
+  int type;                /* GEMM_TYPE_* */
+  int N, K, rank, adapters;
+  const void *A, *B;
+  const int *ranks;
+  const float *scales;
+} gemm_lora_t;
+
+/* X rows x K, C and Y rows x N, with row strides. C null: zeros. C may be Y with the same
+ * stride (rows without an adapter are then left as they are); otherwise Y overlaps
+ * nothing else. workspace: as gemm_mx, gemm_lora_workspace_bytes(...) bytes;
+ * GEMM_ERR_WORKSPACE also where the library can get none. */
+int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
+              const void *C, int ldc, void *Y, int ldy, void *workspace, size_t workspace_bytes,
+              hipStream_t stream);
+size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set);
+
+/* The gradients of gemm_lora from dY (rows x N):
+ *   dX[i] = C[i] + s_a A_a^T (B_a^T dY[i]),  C (rows x K) being the shared projection's own
+ *           gradient (null: zeros; it may be dX, as above);
+ *   dA_a = sum over a's rows of (s_a B_a^T dY[i]) X[i]^T      dense FP32 arrays of the
+ *   dB_a = sum over a's rows of dY[i] (s_a A_a X[i])^T        shapes of A and B
+ * dA and dB are overwritten whole, with zeros where an adapter has no rows and behind
+ * its rank. dX may be null, and dA and dB together. Sums over rows are FP32, in an
+ * order that depends on the sizes and ids alone. Where an input is not finite, a
+ * gradient that it enters may be NaN instead of infinite. workspace: as above
+ * (it holds B once more, so it grows with the number of adapters). */
+int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
+                       const void *dY, int lddy, const void *C, int ldc, void *dX, int lddx,
+                       float *dA, float *dB, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+size_t gemm_lora_backward_workspace_bytes(int rows, const gemm_lora_t *set);
+
 /* Static, human-readable name of a kernel id ("unknown" otherwise). */
 const char *gemm_kernel_name(int kernel);
 
