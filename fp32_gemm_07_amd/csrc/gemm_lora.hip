@@ -51,22 +51,25 @@ LoraRows rows_of(int rows, const gemm_lora_t &s, const int *ids) {
   return LoraRows{rows, s.rank, s.adapters, ids, s.ranks, s.scales};
 }
 
-// Ranges that the columns of a shrink are cut into: workgroups of 16 rows alone would leave
-// most CUs idle below 16 * cus rows. At most 16, each of 256 columns at least; the expand adds
-// their sums up.
+// Ranges that the columns of a shrink are cut into, where workgroups of 16 rows alone would
+// leave most CUs idle: at most 16, each of 256 columns at least; the expand adds their sums up.
 int shrink_splits(int rows, int K, int cus) {
-  const long long tiles = std::max<long long>(1, ceil_div(rows, 16));
-  return static_cast<int>(std::max<long long>(1, std::min<long long>({2LL * cus / tiles, K / 256, 16})));
+  const long long units = ceil_div(std::max(rows, 1), 16);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({2LL * cus / units, K / 256, 16})));
 }
+// Workgroups among which the units of a window are dealt out. A window has from 4 (one
+// adapter) to 64 (all different): with few rows as many as it can have.
+int shrink_units(int rows, int cus) { return rows >= 16 * cus ? 4 : std::min(rows, 64); }
 Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, int splits, float *h, void *parts) {
   const int k_split = static_cast<int>(ceil_div(ceil_div(K, splits), 64) * 64);
   return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, parts};
 }
 
-int launch_shrink(ShrinkArgs a, int problems, int type, hipStream_t stream) {
-  const long long tiles = ceil_div(a.r.rows, 16);
-  a.blocks0 = static_cast<int>(tiles * a.p[0].splits);
-  const long long blocks = a.blocks0 + (problems > 1 ? tiles * a.p[1].splits : 0);
+int launch_shrink(ShrinkArgs a, int problems, int type, int cus, hipStream_t stream) {
+  a.units_by = shrink_units(a.r.rows, cus);
+  const long long units = ceil_div(a.r.rows, 64) * a.units_by;
+  a.blocks0 = static_cast<int>(units * a.p[0].splits);
+  const long long blocks = a.blocks0 + (problems > 1 ? units * a.p[1].splits : 0);
   with_type(type, [&](auto t) {
     with_rank(a.r.rank, [&](auto rt) {
       hipLaunchKernelGGL((shrink_kernel<decltype(t)::value, decltype(rt)::value, 1, 4>), dim3(static_cast<unsigned>(blocks)),
@@ -76,24 +79,23 @@ int launch_shrink(ShrinkArgs a, int problems, int type, hipStream_t stream) {
   return launched();
 }
 
-template <int TYPE, int RT, bool TRANS, int J>
+template <int TYPE, int RT, int J>
 void launch_expand_columns(ExpandArgs a, int cus, hipStream_t stream) {
-  const long long columns = ceil_div(a.N, 64 * J), tiles = ceil_div(a.r.rows, 16);
-  // Four workgroups a CU, then more row tiles for each: an adapter's columns stay in registers.
-  a.tiles = static_cast<int>(std::max<long long>(1, columns * tiles / (4LL * cus)));
-  hipLaunchKernelGGL((expand_kernel<TYPE, RT, TRANS, J>), dim3(static_cast<unsigned>(columns * ceil_div(tiles, a.tiles))),
-                     dim3(256), 0, stream, a);
+  const long long columns = ceil_div(a.N, 64 * J), windows = ceil_div(a.r.rows, 64);
+  // Four workgroups a CU, then more windows for each: an adapter's columns stay in registers.
+  // With fewer, the units of a window are dealt out among several.
+  a.windows = static_cast<int>(std::max<long long>(1, columns * windows / (4LL * cus)));
+  const long long blocks = columns * ceil_div(windows, a.windows);
+  a.units_by = static_cast<int>(std::max<long long>(1, std::min<long long>({4LL * cus / blocks, a.r.rows, 64})));
+  hipLaunchKernelGGL((expand_kernel<TYPE, RT, J>), dim3(static_cast<unsigned>(blocks * a.units_by)), dim3(256), 0,
+                     stream, a);
 }
-template <bool TRANS>
 int launch_expand(const ExpandArgs &a, int type, int cus, hipStream_t stream) {
   with_type(type, [&](auto t) {
     with_rank(a.r.rank, [&](auto rt) {
-      constexpr int T = decltype(t)::value, RT = decltype(rt)::value, MOST = kExpandMost<T, TRANS>;
-      if constexpr (!TRANS) {
-        if (ceil_div(a.N, 64 * MOST) * ceil_div(a.r.rows, 16) < cus)
-          return launch_expand_columns<T, RT, false, 1>(a, cus, stream);
-      }
-      launch_expand_columns<T, RT, TRANS, MOST>(a, cus, stream);
+      constexpr int T = decltype(t)::value, RT = decltype(rt)::value;
+      if (ceil_div(a.N, 256) * ceil_div(a.r.rows, 16) < cus) launch_expand_columns<T, RT, 1>(a, cus, stream);
+      else launch_expand_columns<T, RT, 4>(a, cus, stream);
     });
   });
   return launched();
@@ -126,7 +128,7 @@ int slot_rows(int rows, const gemm_lora_t &s, int cus) {
 }
 
 struct Backward {
-  size_t plan, slots, sums, order, position, g, parts_h, parts_g, bt, partial_a, partial_b, bytes;
+  size_t plan, slots, sums, order, position, g, parts_h, parts_g, at, bt, partial_a, partial_b, bytes;
   int slot_rows, most_slots, positions;
 };
 Backward backward_layout(int rows, const gemm_lora_t &s, int cus) {
@@ -152,6 +154,7 @@ Backward backward_layout(int rows, const gemm_lora_t &s, int cus) {
   l.g = take(sizeof(float) * rows * rp);
   l.parts_h = take(part * rp * l.positions);
   l.parts_g = take(part * rp * l.positions);
+  l.at = take(range_a(s).bytes);
   l.bt = take(range_b(s).bytes);
   l.partial_a = take(sizeof(float) * partials * s.rank * s.K);
   l.partial_b = take(sizeof(float) * partials * s.rank * s.N);
@@ -200,11 +203,11 @@ int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, i
     ShrinkArgs sa{};
     sa.r = r;
     sa.p[0] = shrink_of(X, ldx, s.A, s.rank, s.K, splits, static_cast<float *>(ws), nullptr);
-    const int launch_st = launch_shrink(sa, 1, s.type, stream);
+    const int launch_st = launch_shrink(sa, 1, s.type, cus, stream);
     if (launch_st != GEMM_OK) return launch_st;
     const ExpandArgs ea{r, static_cast<const float *>(ws), splits, s.B, static_cast<long long>(s.rank) * s.N, s.rank,
-                        C, ldc, Y, ldy, s.N, 1, in_place};
-    return launch_expand<false>(ea, s.type, cus, stream);
+                        C, ldc, Y, ldy, s.N, 1, 1, in_place};
+    return launch_expand(ea, s.type, cus, stream);
   });
 }
 
@@ -256,11 +259,13 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
     Slot *slots = reinterpret_cast<Slot *>(w + l.slots);
     int2 *sums = reinterpret_cast<int2 *>(w + l.sums);
     int *order = reinterpret_cast<int *>(w + l.order), *position = reinterpret_cast<int *>(w + l.position);
-    const int bt_tiles = static_cast<int>(std::min<long long>(ceil_div(s.N, kTransRows), 256));
-    const PrepareArgs pa{r, l.slot_rows, s.N, plan, slots, sums, order, position, s.B, w + l.bt, bt_tiles};
+    const int a_tiles = dX ? static_cast<int>(std::min<long long>(ceil_div(s.K, kTransRows), 256)) : 0;
+    const int b_tiles = static_cast<int>(std::min<long long>(ceil_div(s.N, kTransRows), 256));
+    const PrepareArgs pa{r, l.slot_rows, s.N, plan, slots, sums, order, position, s.A, s.B, w + l.at, w + l.bt,
+                         s.K, a_tiles, b_tiles};
     with_type(s.type, [&](auto t) {
       hipLaunchKernelGGL(prepare_kernel<decltype(t)::value>,
-                         dim3(static_cast<unsigned>(1 + (rows ? s.adapters * bt_tiles : 0))), dim3(1024), 0, stream, pa);
+                         dim3(static_cast<unsigned>(1 + (rows ? s.adapters * (a_tiles + b_tiles) : 0))), dim3(1024), 0, stream, pa);
     });
     int launch_st = launched();
     if (launch_st != GEMM_OK) return launch_st;
@@ -272,11 +277,12 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
       sa.positions = l.positions;
       sa.p[0] = shrink_of(dY, lddy, w + l.bt, s.rank, s.N, 1, dX ? g : nullptr, dA ? w + l.parts_g : nullptr);
       if (dA) sa.p[1] = shrink_of(X, ldx, s.A, s.rank, s.K, 1, nullptr, w + l.parts_h);
-      launch_st = launch_shrink(sa, dA ? 2 : 1, s.type, stream);
+      launch_st = launch_shrink(sa, dA ? 2 : 1, s.type, cus, stream);
       if (launch_st != GEMM_OK) return launch_st;
       if (dX) {
-        const ExpandArgs ea{r, g, 1, s.A, static_cast<long long>(s.rank) * s.K, s.K, C, ldc, dX, lddx, s.K, 1, in_place};
-        launch_st = launch_expand<true>(ea, s.type, cus, stream);
+        const ExpandArgs ea{r, g, 1, w + l.at, static_cast<long long>(s.rank) * s.K, s.rank, C, ldc, dX, lddx, s.K, 1, 1,
+                            in_place};
+        launch_st = launch_expand(ea, s.type, cus, stream);
         if (launch_st != GEMM_OK) return launch_st;
       }
     }

@@ -2,7 +2,7 @@
 // (the operations are described in gemm.h at gemm_lora and gemm_lora_backward).
 //   shrink:  H = s X A^T          rows x rank, FP32
 //   expand:  Y = C + H B^T
-// and backward, with B transposed once (few bytes) so that shrink serves both ways:
+// and backward, with A and B transposed first (few bytes) so that both serve again:
 //   shrink:  H = s X A^T,  G = s dY B
 //   expand:  dX = C' + G A
 //   grads:   dA = G^T X,  dB = dY^T H, sums over the rows of one adapter.
@@ -10,16 +10,18 @@
 // bytes of X, C and Y (dY, dX): each is read or written once a kernel, straight
 // between memory and registers. What is small (adapters, H, G) comes from L2.
 //
-// Rows are taken 16 at a time, the columns of 16x16 matrix instructions. The rows of a tile
-// mostly have one adapter (prompts packed one behind the other); where they have
-// several, the tile is worked out for each and every row keeps its own. An
-// instruction's columns do not mix, so what another adapter holds, NaN included,
-// never reaches a row.
+// Rows are looked at 64 at a time (a window: a lane each). Those of one adapter, up to 16
+// or some times 16, make a unit, wherever they lie in the window: they are the columns of
+// 16x16 matrix instructions, so an adapter is read once for all of its rows there, be they
+// a prompt's or single tokens between those of other requests. An instruction's columns do
+// not mix: what another row or adapter holds, NaN included, never reaches a row.
 //
 // Precision: products of 16-bit inputs are exact and summed in FP32. H and G stay FP32:
 // they enter the second products as three bfloat16 parts whose sum is exact. FP32
 // inputs go through FP32 matrix instructions throughout.
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_kernels.hpp"
 #include "mx_moe.hpp"
@@ -106,6 +108,61 @@ __device__ inline void split_halfs(const uintx4 &h, bf16x8 (&out)[2]) {
   split8<2>(v, out);
 }
 
+// The units of a range of windows in order: rows of one adapter (of none for id -1, where those
+// count too), up to 16 MT of them. Everything but `row` is uniform over the wave.
+template <int MT>
+struct Units {
+  const LoraRows &r;
+  const bool with_none;      // rows without an adapter make units too
+  int window, end;
+  int my_id, next_id;        // of this lane's row in the window, and in the next one
+  unsigned long long todo = 0, same = 0;
+  int base = 0;
+  // The current unit.
+  int id;
+  int row[MT];               // of column i16; rows - 1 past the unit's last
+  bool real[MT];
+
+  __device__ inline Units(const LoraRows &rows, bool none, int first, int last)
+      : r(rows), with_none(none), window(first - 1), end(last) {
+    next_id = fetch(first);
+  }
+  // (-2: past the last row)
+  __device__ inline int fetch(int w) const {
+    const int at = w * 64 + (threadIdx.x & 63);
+    return w < end && at < r.rows ? r.id(at) : -2;
+  }
+  __device__ inline bool next() {
+    if (!same) {
+      while (!todo) {
+        if (++window >= end) return false;
+        my_id = next_id;
+        next_id = fetch(window + 1);
+        todo = __ballot(with_none ? my_id >= -1 : my_id >= 0);
+      }
+      id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
+      same = __ballot(my_id == id);
+      todo &= ~same;
+      base = 0;
+    }
+    // Lane l's row of the window goes to the lane of its number among the unit's.
+    const int lane = threadIdx.x & 63, i16 = lane & 15;
+    const int count = __popcll(same);
+    const int number = __popcll(same & ((1ull << lane) - 1)) - base;
+    const bool mine = (same >> lane & 1) && number >= 0 && number < 64;
+    const int from = __builtin_amdgcn_ds_permute((mine ? number : 63) * 4, mine ? lane : 0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      real[m] = m * 16 + i16 < count - base;
+      const int at = window * 64 + __shfl(from, m * 16 + i16);
+      row[m] = real[m] ? at : r.rows - 1;
+    }
+    base += 16 * MT;
+    if (base >= count) same = 0;
+    return true;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // shrink.
 struct Shrink {
@@ -121,143 +178,134 @@ struct Shrink {
 struct ShrinkArgs {
   LoraRows r;
   Shrink p[2];         // blocks of p[0] first
-  int blocks0;
+  int blocks0, units_by;
   const int *position; // of each row among the rows sorted by adapter (with parts)
   int positions;
 };
 
-// One workgroup: 16 MT rows, a range of K. With S ranges for each of the D adapters that
-// its rows have (S = W / D), wave d S + s sums range s for adapter d; where there are more
-// adapters than waves a wave takes several.
+// One workgroup: every units_by-th unit of a window, over a range of K that its W waves share;
+// their sums are added in order through LDS. A wave's operands of the next U chunks are
+// on their way while those of the last are multiplied.
 template <int TYPE, int RT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
   typedef typename Elem<TYPE>::store store;
   constexpr int RP = 16 * RT, kLane = kLaneK<TYPE>, kChunk = 4 * kLane;
-  constexpr int U = RT * MT >= 8 ? 2 : 4;   // chunks at a time
-  __shared__ __attribute__((aligned(16))) f32x4 sums[W * MT * RT * 64];
+  constexpr int U = RT + MT > 8 ? 1 : RT + MT > 3 ? 2 : 4;   // chunks at a time
+  __shared__ __attribute__((aligned(16))) f32x4 sums[2][W * MT * RT * 64];
   const bool second = static_cast<int>(blockIdx.x) >= a.blocks0;
   const Shrink p = second ? a.p[1] : a.p[0];
-  const int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
+  int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
   const int split = block % p.splits;
-  const int row0 = block / p.splits * (16 * MT);
-  const int k0 = split * p.k_split, k1 = min(p.K, k0 + p.k_split);
+  block /= p.splits;
+  const int group = block % a.units_by, window = block / a.units_by;
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Lane l < 16 MT knows row l's adapter.
-  const int my_id = lane < 16 * MT ? a.r.id(row0 + lane) : -1;
-  const unsigned long long live = __ballot(my_id >= 0);
-  int D = 0, my_d = 0;
-  for (unsigned long long todo = live; todo; ++D) {
-    const int id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
-    const unsigned long long same = __ballot(my_id == id);
-    if (my_id == id) my_d = D;
-    todo &= ~same;
-  }
-  if (D == 0) return;
-  const int S = D >= W ? 1 : W / D;
-  const int k_slice = ((k1 - k0 + S - 1) / S + 63) / 64 * 64;
+  const int k_wave = (p.k_split / W + 63) / 64 * 64;
+  const int k1 = min(p.K, (split + 1) * p.k_split);
+  const int ka = min(k1, split * p.k_split + wave * k_wave), kb = wave == W - 1 ? k1 : min(k1, ka + k_wave);
 
-  // Sums of a range of K for one adapter, in the layout of the instruction: value v of lane
-  // (g, i16) is column 4g + v of H for row i16.
-  auto sum_range = [&](int id, unsigned long long mask, int ka, int kb, f32x4 (&acc)[MT][RT]) __attribute__((always_inline)) {
-    const int rank = a.r.rank_of(id);
+  Units<MT> unit(a.r, false, window, window + 1);
+  int turn = 0;
+  for (int n = 0; unit.next(); ++n) {
+    if (n % a.units_by != group) continue;
+    const int id = unit.id, rank = a.r.rank_of(id);
+    f32x4 acc[MT][RT] = {};
+    if (rank > 0) {
+      const store *w = static_cast<const store *>(p.w) + id * p.w_adapter + g * kLane;
+      const store *wr[RT], *zr[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int t = 0; t < RT; ++t) wr[t] = w + min(t * 16 + i16, rank - 1) * p.ldw;   // (past the rank: not kept)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) acc[m][t] = f32x4{};
-    if (rank == 0) return;
-    const store *w = static_cast<const store *>(p.w) + id * p.w_adapter + g * kLane;
-    const store *wr[RT], *zr[MT];
+      for (int m = 0; m < MT; ++m) zr[m] = static_cast<const store *>(p.z) + unit.row[m] * p.ldz + g * kLane;
+      struct Fetched {
+        uintx4 w[U][RT], z[U][MT];
+      };
+      auto fetch = [&](Fetched &f, int k) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) wr[t] = w + min(t * 16 + i16, rank - 1) * p.ldw;   // (past the rank: not kept)
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      zr[m] = static_cast<const store *>(p.z) + static_cast<long long>(min(row0 + m * 16 + i16, a.r.rows - 1)) * p.ldz + g * kLane;
-    int k = ka;
-    for (; k + U * kChunk <= kb; k += U * kChunk) {
-      uintx4 wv[U][RT], zv[U][MT];
+          for (int m = 0; m < MT; ++m) f.z[u][m] = load_k<TYPE>(zr[m] + k + u * kChunk);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+          for (int t = 0; t < RT; ++t) f.w[u][t] = load_k<TYPE>(wr[t] + k + u * kChunk);
+        }
+      };
+      int k = ka;
+      const int batches = (kb - ka) / (U * kChunk);
+      int left = batches;
+      auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
+        // (after the last batch the same again: a branch around loads would wait for them)
+        fetch(next, --left ? k + U * kChunk : k);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) zv[u][m] = load_k<TYPE>(zr[m] + k + u * kChunk);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) wv[u][t] = load_k<TYPE>(wr[t] + k + u * kChunk);
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(cur.w[u][t], cur.z[u][m], acc[m][t]);
+        k += U * kChunk;
+      };
+      if (batches > 0) {
+        Fetched even, odd;
+        fetch(even, ka);
+        in_turn(batches, even, odd, step);
       }
+      for (; k < kb; k += kChunk) {
+        const int rest = kb - k - g * kLane;
+        uintx4 wv[RT], zv[MT];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int m = 0; m < MT; ++m) zv[m] = load_k<TYPE>(zr[m] + k, rest);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) wv[t] = load_k<TYPE>(wr[t] + k, rest);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(wv[u][t], zv[u][m], acc[m][t]);
-    }
-    for (; k < kb; k += kChunk) {
-      const int left = kb - k - g * kLane;
-      uintx4 wv[RT], zv[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) zv[m] = load_k<TYPE>(zr[m] + k, left);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) wv[t] = load_k<TYPE>(wr[t] + k, left);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(wv[t], zv[m], acc[m][t]);
-    }
-  };
-  // 4 neighbouring columns of H for one row, scaled, zeros past the rank.
-  auto keep = [&](int id, int row, int t, f32x4 v) __attribute__((always_inline)) {
-    const int rank = a.r.rank_of(id);
-    const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = t * 16 + 4 * g + i < rank ? v[i] * scale : 0.0f;
-    if (p.h)
-      *reinterpret_cast<f32x4 *>(p.h + (static_cast<long long>(split) * a.r.rows + row) * RP + t * 16 + 4 * g) = v;
-    if (p.parts) {
-      const int at = a.position[row];
-      const long long plane = static_cast<long long>(RP) * a.positions;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long to = static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at;
-        if constexpr (TYPE == kF32) {
-          static_cast<float *>(p.parts)[to] = v[i];
-        } else {
-          float rest = v[i];
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            const u16 part = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
-            static_cast<u16 *>(p.parts)[q * plane + to] = part;
-            rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
-          }
-        }
+          for (int t = 0; t < RT; ++t) acc[m][t] = multiply<TYPE>(wv[t], zv[m], acc[m][t]);
       }
     }
-  };
-
-  int d = 0;
-  for (unsigned long long todo = live; todo; ++d) {
-    const int id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
-    const unsigned long long same = __ballot(my_id == id);
-    todo &= ~same;
-    if (S == 1 ? d % W != wave : d != wave / S) continue;
-    const int s = S == 1 ? 0 : wave % S;
-    f32x4 acc[MT][RT];
-    sum_range(id, same, min(k1, k0 + s * k_slice), min(k1, k0 + (s + 1) * k_slice), acc);
+    // One barrier a unit: the next one's sums go to the other half.
+    f32x4 *half = sums[turn & 1];
+    ++turn;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) half[((wave * MT + m) * RT + t) * 64 + lane] = acc[m][t];
+    __syncthreads();
+    const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        if (S > 1) sums[((wave * MT + m) * RT + t) * 64 + lane] = acc[m][t];
-        else if (same >> (m * 16 + i16) & 1) keep(id, row0 + m * 16 + i16, t, acc[m][t]);
+        if ((m * RT + t) % W != wave) continue;
+        f32x4 v = half[(m * RT + t) * 64 + lane];
+#pragma unroll
+        for (int s = 1; s < W; ++s) v += half[((s * MT + m) * RT + t) * 64 + lane];
+        // 4 neighbouring columns of H for one row, scaled, zeros past the rank
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = t * 16 + 4 * g + i < rank ? v[i] * scale : 0.0f;
+        const int row = unit.row[m];
+        if (!unit.real[m]) continue;
+        if (p.h)
+          *reinterpret_cast<f32x4 *>(p.h + (static_cast<long long>(split) * a.r.rows + row) * RP + t * 16 + 4 * g) = v;
+        if (p.parts) {
+          const int at = a.position[row];
+          const long long plane = static_cast<long long>(RP) * a.positions;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long to = static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at;
+            if constexpr (TYPE == kF32) {
+              static_cast<float *>(p.parts)[to] = v[i];
+            } else {
+              float rest = v[i];
+#pragma unroll
+              for (int q = 0; q < 3; ++q) {
+                const u16 part = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
+                static_cast<u16 *>(p.parts)[q * plane + to] = part;
+                rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
+              }
+            }
+          }
+        }
       }
-  }
-  if (S == 1) return;
-  __syncthreads();
-  for (int n = wave; n < MT * RT; n += W) {
-    const int m = n / RT, t = n % RT;
-    const int id = __shfl(my_id, m * 16 + i16), at = __shfl(my_d, m * 16 + i16);
-    if (id < 0) continue;
-    f32x4 v = sums[((at * S * MT + m) * RT + t) * 64 + lane];
-    for (int s = 1; s < S; ++s) v += sums[(((at * S + s) * MT + m) * RT + t) * 64 + lane];
-    keep(id, row0 + m * 16 + i16, t, v);
   }
 }
 
@@ -267,39 +315,37 @@ struct ExpandArgs {
   LoraRows r;
   const float *h;          // [splits][rows][RP]
   int splits;
-  const void *w;           // adapter a's matrix at w + a * w_adapter: N x rank, row stride ldw;
-  long long w_adapter, ldw;   // rank x N for TRANS
+  const void *w;           // adapter a's N x rank at w + a * w_adapter, row stride ldw
+  long long w_adapter, ldw;
   const void *c;           // null: zeros
   long long ldc;
   void *y;
   long long ldy;
-  int N, tiles;            // row tiles of a workgroup
+  int N, windows;          // of a workgroup
+  int units_by;
   bool in_place;           // c is y
 };
 
-// Columns of Y that a wave has at one time: 16 J, and consecutive ones of a lane.
-template <int TYPE, bool TRANS>
-constexpr int kExpandMost = TRANS && TYPE != kF32 ? 8 : 4;
-
-// A wave keeps 16 J rows of an adapter's B (columns of its A) in registers and takes row
-// tile after row tile; they are loaded again where the adapter changes. Row m of
-// instruction j is column 4 J (m / 4) + 4 j + m % 4 of the wave's, or for TRANS, where a lane loads
-// J neighbouring columns of several ranks, column J m + j: either way the results
-// of a lane are 4 J neighbouring columns of one row of Y.
-template <int TYPE, int RT, bool TRANS, int J>
+// A wave keeps 16 J rows of an adapter's B in registers and takes unit after unit, every
+// units_by-th of its windows'; they are loaded again where the adapter changes. C and H of
+// the next unit are on their way meanwhile. Row m of instruction j is column 4 J (m / 4) +
+// 4 j + m % 4 of the wave's, so that a lane's results are 4 J neighbouring columns of
+// one row of Y.
+template <int TYPE, int RT, int J>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   typedef typename Elem<TYPE>::store store;
-  constexpr int RP = 16 * RT, COLS = 4 * J;
+  constexpr int RP = 16 * RT, COLS = 4 * J, kLane = kLaneK<TYPE>, CW = (COLS + kLane - 1) / kLane;
   constexpr int KS = TYPE == kF32 ? RT : (RT + 1) / 2;   // operands along the rank: of 16 or 32
   constexpr int PB = TYPE == kF16 ? 2 : 1;               // parts of B
   constexpr int PH = TYPE == kF32 ? 1 : 3;               // parts of H
-  static_assert(!TRANS || J == kExpandMost<TYPE, TRANS>, "a lane's load");
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col_blocks = (a.N + 64 * J - 1) / (64 * J);
   const int nb = (blockIdx.x % col_blocks * 4 + wave) * 16 * J;
   if (nb >= a.N) return;
-  const int tile0 = blockIdx.x / col_blocks * a.tiles;
+  const int group = blockIdx.x / col_blocks % a.units_by;
+  const int window0 = blockIdx.x / col_blocks / a.units_by * a.windows;
+  const int window1 = min(window0 + a.windows, (a.r.rows + 63) / 64);
   const int n_lane = nb + COLS * g, left = a.N - n_lane;
 
   uintx4 b[J][KS][PB];
@@ -307,40 +353,13 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   auto load_adapter = [&](int id) __attribute__((always_inline)) {
     const int rank = a.r.rank_of(id);
     const store *w = static_cast<const store *>(a.w) + id * a.w_adapter;
-    constexpr int kLane = kLaneK<TYPE>;
-    if constexpr (!TRANS) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int n = min(nb + COLS * (i16 >> 2) + 4 * j + (i16 & 3), a.N - 1);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const int r = s * 4 * kLane + g * kLane;
-          b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, rank - r);
-        }
-      }
-    } else {
-      // kLane ranks, J neighbouring columns of each
-      const int n = nb + J * i16;
+    for (int j = 0; j < J; ++j) {
+      const int n = min(nb + COLS * (i16 >> 2) + 4 * j + (i16 & 3), a.N - 1);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        uintx4 x[kLane];
-#pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-          const int r = s * 4 * kLane + g * kLane + i;
-          x[i] = load_k<TYPE>(w + r * a.ldw + n, r < rank ? a.N - n : 0);
-        }
-        if constexpr (TYPE == kF32) {
-#pragma unroll
-          for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[j][s][0][i] = x[i][j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              b[j][s][0][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302 : 0x05040100);
-        }
+        const int r = s * 4 * kLane + g * kLane;
+        b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, rank - r);
       }
     }
     if constexpr (PB == 2) {
@@ -356,58 +375,92 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
     }
   };
 
-  for (int tile = tile0; tile < tile0 + a.tiles && tile * 16 < a.r.rows; ++tile) {
-    const int row = tile * 16 + i16;
-    const int id = a.r.id(row);
-    unsigned long long todo = __ballot(id >= 0) & 0xffff;
-    if (!todo && a.in_place) continue;
-    float out[COLS];
-    const store *c = static_cast<const store *>(a.c) + static_cast<long long>(min(row, a.r.rows - 1)) * a.ldc + n_lane;
-    if (a.c) {
-      if constexpr (COLS >= 8) {
+  struct Fetched {
+    int id, row;
+    bool real;
+    uintx4 c[CW];
+    f32x4 h[KS][kLane / 4];
+  };
+  Units<1> unit(a.r, !a.in_place, window0, window1);
+  int n = -1;
+  auto advance = [&]() __attribute__((always_inline)) {
+    bool more;
+    do {
+      more = unit.next();
+      ++n;
+    } while (more && n % a.units_by != group);
+    return more;
+  };
+  // WHOLE: all of the wave's columns exist.
+  auto run = [&](auto whole) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    auto fetch = [&](Fetched &f) __attribute__((always_inline)) {
+      f.id = unit.id;
+      f.row = unit.row[0];
+      f.real = unit.real[0];
+      if (a.c) {
+        const store *c = static_cast<const store *>(a.c) + f.row * a.ldc + n_lane;
 #pragma unroll
-        for (int q = 0; q < COLS; q += 8) load8<TYPE>(c + q, left - q, reinterpret_cast<float(&)[8]>(out[q]));
-      } else {
-#pragma unroll
-        for (int q = 0; q < COLS; ++q) out[q] = q < left ? Elem<TYPE>::get(c[q]) : 0.0f;
+        for (int q = 0; q < CW; ++q) {
+          if constexpr (COLS < kLane) f.c[q] = load_k<TYPE>(c, WHOLE ? COLS : min(COLS, left));
+          else if constexpr (WHOLE) f.c[q] = load_k<TYPE>(c + q * kLane);
+          else f.c[q] = load_k<TYPE>(c + q * kLane, left - q * kLane);
+        }
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < COLS; ++q) out[q] = 0.0f;
-    }
-    if (todo) {
-      // H of the row, in operands.
-      uintx4 h[KS][PH];
-      const float *hr = a.h + static_cast<long long>(min(row, a.r.rows - 1)) * RP;
+      const float *h = a.h + static_cast<long long>(f.row) * RP;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        constexpr int kLane = kLaneK<TYPE>;
-        const int r = s * 4 * kLane + g * kLane;
-        f32x4 v[2] = {};
-        if (r < RP) {   // (the upper half of 32 where RP is 16: zeros)
-          for (int q = 0; q < a.splits; ++q) {
-            const float *part = hr + static_cast<long long>(q) * a.r.rows * RP + r;
+        // (the upper half of 32 ranks where RP is 16: the lower again, not used)
+        const int r = (s * 4 * kLane + g * kLane) % RP;
 #pragma unroll
-            for (int i = 0; i < kLane / 4; ++i) v[i] += reinterpret_cast<const f32x4 *>(part)[i];
-          }
-        }
-        if constexpr (TYPE == kF32) {
-          h[s][0] = __builtin_bit_cast(uintx4, v[0]);
-        } else {
-          float x[8];
-          floats8(v[0], v[1], x);
-          bf16x8 parts[3];
-          split8<3>(x, parts);
+        for (int i = 0; i < kLane / 4; ++i) f.h[s][i] = reinterpret_cast<const f32x4 *>(h + r)[i];
+      }
+      for (int q = 1; q < a.splits; ++q) {
+        const float *part = h + static_cast<long long>(q) * a.r.rows * RP;
 #pragma unroll
-          for (int q = 0; q < PH; ++q) h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
+        for (int s = 0; s < KS; ++s) {
+          const int r = (s * 4 * kLane + g * kLane) % RP;
+#pragma unroll
+          for (int i = 0; i < kLane / 4; ++i) f.h[s][i] += reinterpret_cast<const f32x4 *>(part + r)[i];
         }
       }
-      while (todo) {
-        const int which = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= ~__ballot(id == which);
-        if (which != have) {
-          load_adapter(which);
-          have = which;
+    };
+    auto finish = [&](const Fetched &f) __attribute__((always_inline)) {
+      float out[COLS];
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) {
+        if (!a.c) {
+          out[q] = 0.0f;
+        } else if constexpr (TYPE == kF32) {
+          const unsigned w = f.c[q / 4][q % 4];
+          out[q] = __builtin_bit_cast(float, w);
+        } else {
+          const unsigned w = f.c[q / 8][q % 8 / 2];
+          out[q] = Elem<TYPE>::get(static_cast<u16>(q % 2 ? w >> 16 : w));
+        }
+      }
+      if (f.id >= 0) {
+        if (f.id != have) {
+          load_adapter(f.id);
+          have = f.id;
+        }
+        uintx4 h[KS][PH];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          if constexpr (TYPE == kF32) {
+            h[s][0] = __builtin_bit_cast(uintx4, f.h[s][0]);
+          } else {
+            float x[8];
+            floats8(f.h[s][0], f.h[s][1], x);
+            if (s * 32 + g * 8 >= RP) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            }
+            bf16x8 parts[3];
+            split8<3>(x, parts);
+#pragma unroll
+            for (int q = 0; q < PH; ++q) h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
+          }
         }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -430,29 +483,41 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
           }
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int q = TRANS ? J * v + j : 4 * j + v;
-            const float sum = TYPE == kF32 || !__builtin_isfinite(first[v]) ? first[v] : first[v] + rest[v];
-            out[q] = id == which ? out[q] + sum : out[q];   // (adding zero would lose -0)
+            out[4 * j + v] += TYPE == kF32 || !__builtin_isfinite(first[v]) ? first[v] : first[v] + rest[v];
           }
         }
       }
-    }
-    if (row < a.r.rows && (id >= 0 || !a.in_place)) {
-      store *y = static_cast<store *>(a.y) + static_cast<long long>(row) * a.ldy + n_lane;
+      if (!f.real) return;
+      store *y = static_cast<store *>(a.y) + f.row * a.ldy + n_lane;
       if constexpr (COLS >= 8) {
 #pragma unroll
-        for (int q = 0; q < COLS; q += 8) store8<TYPE>(y + q, left - q, reinterpret_cast<float(&)[8]>(out[q]));
+        for (int q = 0; q < COLS; q += 8) store8<TYPE>(y + q, WHOLE ? 8 : left - q, reinterpret_cast<float(&)[8]>(out[q]));
       } else {
 #pragma unroll
         for (int q = 0; q < COLS; ++q)
-          if (q < left) y[q] = Elem<TYPE>::put(out[q]);
+          if (WHOLE || q < left) y[q] = Elem<TYPE>::put(out[q]);
       }
+    };
+    if (!advance()) return;
+    Fetched even, odd;
+    fetch(even);
+    while (true) {
+      bool more = advance();
+      fetch(odd);   // (after the last unit the same again: a branch around loads would wait for them)
+      finish(even);
+      if (!more) break;
+      more = advance();
+      fetch(even);
+      finish(odd);
+      if (!more) break;
     }
-  }
+  };
+  if (nb + 16 * J <= a.N) run(std::true_type());
+  else run(std::false_type());
 }
 
 // ---------------------------------------------------------------------------
-// Backward: the rows sorted by adapter, and B transposed.
+// Backward: the rows sorted by adapter, A and B transposed.
 
 // A stretch of up to `slot_rows` rows of one adapter, in the sorted order.
 struct Slot {
@@ -470,11 +535,12 @@ struct PrepareArgs {
   int2 *sums;           // adapter: its first partial sum, how many (-1: written straight)
   int *order;           // position -> row
   int *position;        // row -> position
-  const void *b;        // N x rank for each adapter
-  void *bt;             // rank x N for each
-  int bt_tiles;         // workgroups for each adapter's
+  const void *a, *b;    // rank x K and N x rank for each adapter
+  void *at, *bt;        // K x rank and rank x N for each
+  int K;
+  int a_tiles, b_tiles; // workgroups for each adapter's
 };
-constexpr int kTransRows = 64;   // rows of B of a transposing workgroup
+constexpr int kTransRows = 64;   // columns of A, rows of B that a workgroup transposes at a time
 
 // Lanes of the wave that have the same id (valid ones).
 __device__ inline unsigned long long same_id(int id, bool valid, int bits) {
@@ -490,8 +556,8 @@ __device__ inline unsigned long long same_id(int id, bool valid, int bits) {
 // Workgroup 0 sorts the rows by adapter, keeping their order (so that sums over them do not
 // depend on timing): every wave counts a stretch of rows, running sums over adapters and
 // waves say where each wave's rows of an adapter go, and each wave puts its
-// rows there. An adapter's positions begin at a multiple of 32. The other workgroups transpose 64
-// rows of one adapter's B each, if any row has that adapter.
+// rows there. An adapter's positions begin at a multiple of 32. The other workgroups transpose
+// one adapter's A or B, if any row has that adapter.
 template <int TYPE>
 __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
   typedef typename Elem<TYPE>::store store;
@@ -500,23 +566,40 @@ __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (blockIdx.x > 0) {
-    const int id = (blockIdx.x - 1) / a.bt_tiles;
-    int n0 = (blockIdx.x - 1) % a.bt_tiles * kTransRows;
+    const int tiles = a.a_tiles + a.b_tiles, id = (blockIdx.x - 1) / tiles, rank = a.r.rank;
     bool used = false;
     for (int row = threadIdx.x; row < a.r.rows; row += 1024) used |= a.r.ids[row] == id;
     if (!__syncthreads_or(used)) return;
-    store *tile = reinterpret_cast<store *>(lds);
-    const int rank = a.r.rank;
-    for (; n0 < a.N; n0 += a.bt_tiles * kTransRows) {
-      const store *b = static_cast<const store *>(a.b) + (static_cast<long long>(id) * a.N + n0) * rank;
-      store *bt = static_cast<store *>(a.bt) + static_cast<long long>(id) * rank * a.N + n0;
-      const int many = min(kTransRows, a.N - n0);
-      for (int i = threadIdx.x; i < many * rank; i += 1024) tile[(i % rank) * (kTransRows + 1) + i / rank] = b[i];
+    store *tile = reinterpret_cast<store *>(lds);   // [rank][64], a row of 65
+    const int at = (blockIdx.x - 1) % tiles;
+    const bool second = at >= a.a_tiles;
+    const int size = second ? a.N : a.K;            // across the ranks
+    const long long adapter = static_cast<long long>(id) * rank * size;
+    const store *from = static_cast<const store *>(second ? a.b : a.a) + adapter;
+    store *to = static_cast<store *>(second ? a.bt : a.at) + adapter;
+    const int step = (second ? a.b_tiles : a.a_tiles) * kTransRows;
+    for (int n0 = (second ? at - a.a_tiles : at) * kTransRows; n0 < size; n0 += step) {
+      const int many = min(kTransRows, size - n0);
+      // the ranks along a row (B, A transposed), or 64 neighbours of one rank (A, B transposed)
+      auto along = [&](bool load) {
+        for (int i = threadIdx.x; i < many * rank; i += 1024) {
+          store &v = tile[i % rank * (kTransRows + 1) + i / rank];
+          if (load) v = from[static_cast<long long>(n0) * rank + i];
+          else to[static_cast<long long>(n0) * rank + i] = v;
+        }
+      };
+      auto across = [&](bool load) {
+        for (int i = threadIdx.x; i < kTransRows * rank; i += 1024) {
+          const int n = i % kTransRows, r = i / kTransRows;
+          if (n >= many) continue;
+          store &v = tile[r * (kTransRows + 1) + n];
+          if (load) v = from[static_cast<long long>(r) * size + n0 + n];
+          else to[static_cast<long long>(r) * size + n0 + n] = v;
+        }
+      };
+      if (second) along(true); else across(true);
       __syncthreads();
-      for (int i = threadIdx.x; i < kTransRows * rank; i += 1024) {
-        const int n = i % kTransRows, r = i / kTransRows;
-        if (n < many) bt[static_cast<long long>(r) * a.N + n] = tile[r * (kTransRows + 1) + n];
-      }
+      if (second) across(false); else along(false);
       __syncthreads();
     }
     return;
@@ -630,45 +713,60 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
   const int n = (block * 16 + i16) * CL, left = p.cols - n;
   const long long plane = static_cast<long long>(a.rp) * a.positions;
   f32x4 acc[CL][RT] = {};
-  for (int at = wave * kStep; at < slot.count; at += 4 * kStep) {
-    const int first = at + g * kRows;   // of the lane's rows
-    uintx4 x[kRows];
+  struct Fetched {
+    uintx4 x[kRows], p[RT][PP];
+  };
+  // The lane's rows of a step; past the slot's last the last again.
+  auto rows_of = [&](int at, int (&rows)[kRows]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      // (rows past the last: zeros on both sides)
-      const bool real = first + i < slot.count;
-      const int row = a.order[slot.first + min(first + i, slot.count - 1)];
-      x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + row * p.ldz + n, real ? left : 0);
+    for (int i = 0; i < kRows; ++i) rows[i] = a.order[slot.first + min(at + g * kRows + i, slot.count - 1)];
+  };
+  const bool whole = (block * 16 + 16) * CL <= p.cols;
+  auto fetch = [&](Fetched &f, int at, const int (&rows)[kRows]) __attribute__((always_inline)) {
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) f.x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + rows[i] * p.ldz + n);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) f.x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + rows[i] * p.ldz + n, left);
     }
-    uintx4 pv[RT][PP];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int q = 0; q < PP; ++q) {
-        const long long from = (rank0 + t * 16 + i16) * static_cast<long long>(a.positions) + slot.first + first;
-        const int real = slot.count - first;
-        uintx4 v;
-        if constexpr (TYPE == kF32) {
-          v = *reinterpret_cast<const uintx4 *>(static_cast<const float *>(p.parts) + from);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = i < real ? v[i] : 0;
-        } else {
-          v = *reinterpret_cast<const uintx4 *>(static_cast<const u16 *>(p.parts) + q * plane + from);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < real ? v[i] : 2 * i < real ? v[i] & 0xffff : 0;
-        }
-        pv[t][q] = v;
+        const long long from = (rank0 + t * 16 + i16) * static_cast<long long>(a.positions) + slot.first + at + g * kRows;
+        if constexpr (TYPE == kF32) f.p[t][q] = *reinterpret_cast<const uintx4 *>(static_cast<const float *>(p.parts) + from);
+        else f.p[t][q] = *reinterpret_cast<const uintx4 *>(static_cast<const u16 *>(p.parts) + q * plane + from);
       }
+  };
+  // Rows past the slot's last: zeros on both sides.
+  auto cut = [&](Fetched &f, int at) __attribute__((always_inline)) {
+    const int real = slot.count - at - g * kRows;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f.x[i][c] = i < real ? f.x[i][c] : 0;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int q = 0; q < PP; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (TYPE == kF32) f.p[t][q][i] = i < real ? f.p[t][q][i] : 0;
+          else f.p[t][q][i] = 2 * i + 1 < real ? f.p[t][q][i] : 2 * i < real ? f.p[t][q][i] & 0xffff : 0;
+        }
+  };
+  auto add = [&](const Fetched &f) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < CL; ++j) {
       uintx4 z[PZ];
       if constexpr (TYPE == kF32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[0][i] = x[i][j];
+        for (int i = 0; i < 4; ++i) z[0][i] = f.x[i][j];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          z[0][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302 : 0x05040100);
+          z[0][i] = __builtin_amdgcn_perm(f.x[2 * i + 1][j / 2], f.x[2 * i][j / 2], j % 2 ? 0x07060302 : 0x05040100);
         if constexpr (PZ == 2) {
           bf16x8 parts[2];
           split_halfs(z[0], parts);
@@ -679,17 +777,39 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         if constexpr (TYPE == kF32) {
-          acc[j][t] = multiply<kF32>(pv[t][0], z[0], acc[j][t]);
+          acc[j][t] = multiply<kF32>(f.p[t][0], z[0], acc[j][t]);
         } else {
 #pragma unroll
-          for (int q = 0; q < PP; ++q) acc[j][t] = multiply<kBf16>(pv[t][q], z[0], acc[j][t]);
+          for (int q = 0; q < PP; ++q) acc[j][t] = multiply<kBf16>(f.p[t][q], z[0], acc[j][t]);
           if constexpr (PZ == 2) {   // (the third part times the second is below 2^-24)
-            acc[j][t] = multiply<kBf16>(pv[t][0], z[1], acc[j][t]);
-            acc[j][t] = multiply<kBf16>(pv[t][1], z[1], acc[j][t]);
+            acc[j][t] = multiply<kBf16>(f.p[t][0], z[1], acc[j][t]);
+            acc[j][t] = multiply<kBf16>(f.p[t][1], z[1], acc[j][t]);
           }
         }
       }
     }
+  };
+  // The rows of the step after the next and the operands of the next are on their way while
+  // one is multiplied.
+  int at = wave * kStep;
+  const int steps = (slot.count - at + 4 * kStep - 1) / (4 * kStep);
+  if (steps > 0) {
+    int rows[kRows];
+    auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
+      // (past the last step: its rows, and positions that exist, once more)
+      const int then = min(at + 4 * kStep, wave * kStep + (steps - 1) * 4 * kStep);
+      fetch(next, then, rows);
+      rows_of(then + 4 * kStep, rows);
+      __builtin_amdgcn_sched_barrier(0);
+      if (at + kStep > slot.count) cut(cur, at);
+      add(cur);
+      at += 4 * kStep;
+    };
+    Fetched even, odd;
+    rows_of(at, rows);
+    fetch(even, at, rows);
+    rows_of(min(at + 4 * kStep, wave * kStep + (steps - 1) * 4 * kStep), rows);
+    in_turn(steps, even, odd, step);
   }
   // The waves' sums in order.
   for (int w = 3; w > 0; --w) {

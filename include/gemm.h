@@ -479,8 +479,9 @@ int gemm_route_backward(int tokens, const gemm_route_t *router, const void *logi
  * adapter: Y[i] = C[i].
  * X, C, Y, A and B have the same type; sums and the products A_a X[i] are FP32 (with
  * 16-bit types they enter the second product as three bfloat16 parts, which cut values
- * below 2^-110 off to a multiple of 2^-133), rounded once at the end. A row's result does not
- * depend on the other rows, and is the same from run to run.
+ * below 2^-110 off to a multiple of 2^-133), rounded once at the end. What
+ * another row or its adapter holds never reaches a row, NaN included; results are the same
+ * from run to run.
  */
 enum {
   GEMM_LORA_MAX_ROWS = 1 << 20,
@@ -514,7 +515,7 @@ size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set);
  * its rank. dX may be null, and dA and dB together. Sums over rows are FP32, in an
  * order that depends on the sizes and ids alone. Where an input is not finite, a
  * gradient that it enters may be NaN instead of infinite. workspace: as above
- * (it holds B once more, so it grows with the number of adapters). */
+ * (it holds A and B once more, so it grows with the number of adapters). */
 int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
                        const void *dY, int lddy, const void *C, int ldc, void *dX, int lddx,
                        float *dA, float *dB, void *workspace, size_t workspace_bytes,
