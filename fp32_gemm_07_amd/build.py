@@ -13,9 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgemm.so")
-SOURCES = [os.path.join(CSRC, "gemm_api.hip"), os.path.join(CSRC, "gemm_dma.hip"),
-           os.path.join(CSRC, "gemm_mx.hip"), os.path.join(CSRC, "gemm_route.hip"),
-           os.path.join(CSRC, "gemm_lora.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in (
+    "gemm_api.hip", "gemm_dma.hip", "gemm_mx.hip", "gemm_route.hip", "gemm_lora.hip",
+    "lora_f32.hip", "lora_bf16.hip", "lora_f16.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIPCC_FLAGS = [

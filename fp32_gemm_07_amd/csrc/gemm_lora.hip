@@ -4,7 +4,7 @@
 
 #include "host_checks.hpp"
 #include "host_shared.hpp"
-#include "lora_kernels.hpp"
+#include "lora_launch.hpp"
 
 namespace {
 
@@ -13,17 +13,6 @@ using namespace gemm::host;
 
 static_assert(kLoraMaxRank == GEMM_LORA_MAX_RANK && kLoraMaxAdapters == GEMM_LORA_MAX_ADAPTERS, "adapter limits");
 
-// 16-column tiles of H for a rank: 1, 2, 4 or 8.
-int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
-template <class F>
-void with_rank(int rank, F &&f) {
-  switch (rank_tiles(rank)) {
-    case 1: f(std::integral_constant<int, 1>()); break;
-    case 2: f(std::integral_constant<int, 2>()); break;
-    case 4: f(std::integral_constant<int, 4>()); break;
-    default: f(std::integral_constant<int, 8>()); break;
-  }
-}
 size_t up16(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
 int check_set(int rows, const gemm_lora_t *s) {
@@ -51,58 +40,32 @@ LoraRows rows_of(int rows, const gemm_lora_t &s, const int *ids) {
   return LoraRows{rows, s.rank, s.adapters, ids, s.ranks, s.scales};
 }
 
-// Ranges that the columns of a shrink are cut into, where workgroups of 16 rows alone would
-// leave most CUs idle: at most 16, each of 256 columns at least; the expand adds their sums up.
-int shrink_splits(int rows, int K, int cus) {
-  const long long units = ceil_div(std::max(rows, 1), 16);
-  return static_cast<int>(std::max<long long>(1, std::min<long long>({2LL * cus / units, K / 256, 16})));
+// How shrink is launched: 16-row tiles of a unit, waves of a workgroup, workgroups among
+// which the units of a window are dealt out, and ranges that the columns are cut into. A
+// window has from 4 / tiles units (one adapter) to 64 (all different).
+// Many rows: units of two tiles, which halve the reads of A (8192 x 4096 bfloat16, rank 32: 20 us,
+// of one tile 29; rank 16: 18 and 21), dealt out among 4 for the windows where one adapter's
+// rows end and another's begin. Fewer rows: one tile, dealt out among 8. Up to 64 rows (a
+// window, `few`): as many workgroups as there may be units, of 8 waves (4 above rank 64, whose
+// operands take the registers), and where that leaves CUs idle ranges of 512 columns at least,
+// whose sums the expand adds up (48 rows on 32 adapters of rank 64, 4096 columns: 8 ranges 11
+// us, 4 14, one 25).
+ShrinkPlan shrink_plan(int rows, const gemm_lora_t &s, int cus) {
+  if (rows >= 16 * cus) return {2, 4, 4, 1, false};
+  if (rows > 64) return {1, 4, 8, 1, false};
+  const int units = std::max(1, std::min(rows, 32));
+  const int splits = static_cast<int>(std::max<long long>(1, std::min<long long>({4LL * cus / units, s.K / 512, 8})));
+  return {1, s.rank > 64 ? 4 : 8, units, splits, true};
 }
-// Workgroups among which the units of a window are dealt out. A window has from 4 (one
-// adapter) to 64 (all different): with few rows as many as it can have.
-int shrink_units(int rows, int cus) { return rows >= 16 * cus ? 4 : std::min(rows, 64); }
-Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, int splits, float *h, void *parts) {
+Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, int splits, void *h, bool floats, void *parts) {
   const int k_split = static_cast<int>(ceil_div(ceil_div(K, splits), 64) * 64);
-  return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, parts};
+  return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, floats, parts};
 }
 
-int launch_shrink(ShrinkArgs a, int problems, int type, int cus, hipStream_t stream) {
-  a.units_by = shrink_units(a.r.rows, cus);
-  const long long units = ceil_div(a.r.rows, 64) * a.units_by;
-  a.blocks0 = static_cast<int>(units * a.p[0].splits);
-  const long long blocks = a.blocks0 + (problems > 1 ? units * a.p[1].splits : 0);
-  with_type(type, [&](auto t) {
-    with_rank(a.r.rank, [&](auto rt) {
-      hipLaunchKernelGGL((shrink_kernel<decltype(t)::value, decltype(rt)::value, 1, 4>), dim3(static_cast<unsigned>(blocks)),
-                         dim3(256), 0, stream, a);
-    });
-  });
-  return launched();
-}
-
-template <int TYPE, int RT, int J>
-void launch_expand_columns(ExpandArgs a, int cus, hipStream_t stream) {
-  const long long columns = ceil_div(a.N, 64 * J), windows = ceil_div(a.r.rows, 64);
-  // Four workgroups a CU, then more windows for each: an adapter's columns stay in registers.
-  // With fewer, the units of a window are dealt out among several.
-  a.windows = static_cast<int>(std::max<long long>(1, columns * windows / (4LL * cus)));
-  const long long blocks = columns * ceil_div(windows, a.windows);
-  a.units_by = static_cast<int>(std::max<long long>(1, std::min<long long>({4LL * cus / blocks, a.r.rows, 64})));
-  hipLaunchKernelGGL((expand_kernel<TYPE, RT, J>), dim3(static_cast<unsigned>(blocks * a.units_by)), dim3(256), 0,
-                     stream, a);
-}
-int launch_expand(const ExpandArgs &a, int type, int cus, hipStream_t stream) {
-  with_type(type, [&](auto t) {
-    with_rank(a.r.rank, [&](auto rt) {
-      constexpr int T = decltype(t)::value, RT = decltype(rt)::value;
-      if (ceil_div(a.N, 256) * ceil_div(a.r.rows, 16) < cus) launch_expand_columns<T, RT, 1>(a, cus, stream);
-      else launch_expand_columns<T, RT, 4>(a, cus, stream);
-    });
-  });
-  return launched();
-}
-
-size_t forward_workspace(int rows, const gemm_lora_t &s, int cus) {
-  return up16(sizeof(float) * static_cast<size_t>(shrink_splits(rows, s.K, cus)) * rows * 16 * rank_tiles(s.rank));
+// Bytes of what shrink leaves for expand.
+size_t hidden_bytes(int rows, const gemm_lora_t &s, const ShrinkPlan &plan) {
+  const size_t each = s.type != GEMM_TYPE_F32 && !plan.few ? 6 : 4 * static_cast<size_t>(plan.splits);
+  return up16(each * rows * 16 * rank_tiles(s.rank));
 }
 
 // Runs body(workspace) on the caller's workspace or the library's.
@@ -118,12 +81,12 @@ int with_workspace(void *workspace, size_t need, int dev, hipStream_t stream, F 
 // Backward.
 
 // Rows of a slot, the stretch of an adapter's rows that one workgroup sums over: as few as
-// fill the CUs twice (a slot's sums are written and read once more), 128 at least.
+// give each CU two workgroups (a slot's sums are written and read once more), 128 at least.
 int slot_rows(int rows, const gemm_lora_t &s, int cus) {
   const int lane = s.type == GEMM_TYPE_F32 ? 4 : 8;
   const long long blocks = ceil_div(s.K, 16 * lane) + ceil_div(s.N, 16 * lane);
   int n = 128;
-  while (n < rows && ceil_div(rows, n) * blocks > 4LL * cus) n *= 2;
+  while (n < rows && ceil_div(rows, n) * blocks > 2LL * cus) n *= 2;
   return n;
 }
 
@@ -151,7 +114,9 @@ Backward backward_layout(int rows, const gemm_lora_t &s, int cus) {
   l.sums = take(sizeof(int2) * s.adapters);
   l.order = take(sizeof(int) * l.positions);
   l.position = take(sizeof(int) * rows);
-  l.g = take(sizeof(float) * rows * rp);
+  ShrinkPlan whole = shrink_plan(rows, s, cus);
+  whole.splits = 1;
+  l.g = take(hidden_bytes(rows, s, whole));
   l.parts_h = take(part * rp * l.positions);
   l.parts_g = take(part * rp * l.positions);
   l.at = take(range_a(s).bytes);
@@ -162,13 +127,17 @@ Backward backward_layout(int rows, const gemm_lora_t &s, int cus) {
   return l;
 }
 
+const LoraLaunches &lora_launches(int type) {
+  return type == kF32 ? lora_launches_f32() : type == kBf16 ? lora_launches_bf16() : lora_launches_f16();
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set) {
   if (check_set(rows, set) != GEMM_OK || rows == 0) return 0;
-  return forward_workspace(rows, *set, gemm::host_planning_cus());
+  return hidden_bytes(rows, *set, shrink_plan(rows, *set, gemm::host_planning_cus()));
 }
 
 int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
@@ -190,24 +159,25 @@ int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, i
   st = check_outputs(out, in);
   if (st != GEMM_OK) return st;
   const int cus = gemm::host_planning_cus();
-  const size_t need = forward_workspace(rows, s, cus);
+  const ShrinkPlan plan = shrink_plan(rows, s, cus);
+  const size_t need = hidden_bytes(rows, s, plan);
   st = check_workspace(workspace, workspace_bytes, need,
                        {x, c, y, id, range_a(s), range_b(s), range_ranks(s), range_scales(s)});
   if (st != GEMM_OK) return st;
   int dev = 0, dev_cus = 0;
   st = gemm::host_check_device(&dev, &dev_cus);
   if (st != GEMM_OK) return st;
+  const LoraLaunches &launches = lora_launches(s.type);
   return with_workspace(workspace, need, dev, stream, [&](void *ws) {
     const LoraRows r = rows_of(rows, s, ids);
-    const int splits = shrink_splits(rows, s.K, cus);
     ShrinkArgs sa{};
     sa.r = r;
-    sa.p[0] = shrink_of(X, ldx, s.A, s.rank, s.K, splits, static_cast<float *>(ws), nullptr);
-    const int launch_st = launch_shrink(sa, 1, s.type, cus, stream);
+    sa.p[0] = shrink_of(X, ldx, s.A, s.rank, s.K, plan.splits, ws, plan.few, nullptr);
+    const int launch_st = launches.shrink(sa, 1, plan, stream);
     if (launch_st != GEMM_OK) return launch_st;
-    const ExpandArgs ea{r, static_cast<const float *>(ws), splits, s.B, static_cast<long long>(s.rank) * s.N, s.rank,
+    const ExpandArgs ea{r, ws, plan.splits, s.B, static_cast<long long>(s.rank) * s.N, s.rank,
                         C, ldc, Y, ldy, s.N, 1, 1, in_place};
-    return launch_expand(ea, s.type, cus, stream);
+    return launches.expand(ea, plan.few, cus, stream);
   });
 }
 
@@ -252,37 +222,36 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
   int dev = 0, dev_cus = 0;
   st = gemm::host_check_device(&dev, &dev_cus);
   if (st != GEMM_OK) return st;
+  const LoraLaunches &launches = lora_launches(s.type);
   return with_workspace(workspace, l.bytes, dev, stream, [&](void *ws) {
     char *w = static_cast<char *>(ws);
     const LoraRows r = rows_of(rows, s, ids);
-    LoraPlan *plan = reinterpret_cast<LoraPlan *>(w + l.plan);
+    ShrinkPlan plan = shrink_plan(rows, s, cus);
+    plan.splits = 1;   // (the gradients' parts are of whole sums)
+    LoraPlan *header = reinterpret_cast<LoraPlan *>(w + l.plan);
     Slot *slots = reinterpret_cast<Slot *>(w + l.slots);
     int2 *sums = reinterpret_cast<int2 *>(w + l.sums);
     int *order = reinterpret_cast<int *>(w + l.order), *position = reinterpret_cast<int *>(w + l.position);
     const int a_tiles = dX ? static_cast<int>(std::min<long long>(ceil_div(s.K, kTransRows), 256)) : 0;
     const int b_tiles = static_cast<int>(std::min<long long>(ceil_div(s.N, kTransRows), 256));
-    const PrepareArgs pa{r, l.slot_rows, s.N, plan, slots, sums, order, position, s.A, s.B, w + l.at, w + l.bt,
+    const PrepareArgs pa{r, l.slot_rows, s.N, header, slots, sums, order, position, s.A, s.B, w + l.at, w + l.bt,
                          s.K, a_tiles, b_tiles};
-    with_type(s.type, [&](auto t) {
-      hipLaunchKernelGGL(prepare_kernel<decltype(t)::value>,
-                         dim3(static_cast<unsigned>(1 + (rows ? s.adapters * (a_tiles + b_tiles) : 0))), dim3(1024), 0, stream, pa);
-    });
-    int launch_st = launched();
+    int launch_st = launches.prepare(pa, 1 + (rows ? s.adapters * (a_tiles + b_tiles) : 0), stream);
     if (launch_st != GEMM_OK) return launch_st;
-    float *g = reinterpret_cast<float *>(w + l.g);
+    void *g = w + l.g;
     if (rows > 0) {
       ShrinkArgs sa{};
       sa.r = r;
       sa.position = position;
       sa.positions = l.positions;
-      sa.p[0] = shrink_of(dY, lddy, w + l.bt, s.rank, s.N, 1, dX ? g : nullptr, dA ? w + l.parts_g : nullptr);
-      if (dA) sa.p[1] = shrink_of(X, ldx, s.A, s.rank, s.K, 1, nullptr, w + l.parts_h);
-      launch_st = launch_shrink(sa, dA ? 2 : 1, s.type, cus, stream);
+      sa.p[0] = shrink_of(dY, lddy, w + l.bt, s.rank, s.N, 1, dX ? g : nullptr, plan.few, dA ? w + l.parts_g : nullptr);
+      if (dA) sa.p[1] = shrink_of(X, ldx, s.A, s.rank, s.K, 1, nullptr, false, w + l.parts_h);
+      launch_st = launches.shrink(sa, dA ? 2 : 1, plan, stream);
       if (launch_st != GEMM_OK) return launch_st;
       if (dX) {
         const ExpandArgs ea{r, g, 1, w + l.at, static_cast<long long>(s.rank) * s.K, s.rank, C, ldc, dX, lddx, s.K, 1, 1,
                             in_place};
-        launch_st = launch_expand(ea, s.type, cus, stream);
+        launch_st = launches.expand(ea, plan.few, cus, stream);
         if (launch_st != GEMM_OK) return launch_st;
       }
     }
@@ -291,28 +260,16 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
     if (rows > 0) {
       const int lane = s.type == kF32 ? 4 : 8;
       const int blocks0 = static_cast<int>(ceil_div(s.K, 16 * lane)), blocks = blocks0 + static_cast<int>(ceil_div(s.N, 16 * lane));
-      GradArgs ga{r, plan, slots, order, l.positions,
+      GradArgs ga{r, header, slots, order, l.positions,
                   {{X, ldx, s.K, w + l.parts_g, partial_a, dA}, {dY, lddy, s.N, w + l.parts_h, partial_b, dB}},
                   blocks0, blocks, 0, 16 * rank_tiles(s.rank), s.rank > 64 ? 2 : 1};
-      const long long slot_blocks = static_cast<long long>(blocks) * ga.rank_blocks;
-      launch_st = in_ranges(l.most_slots, max_blocks(256) / slot_blocks, [&](long long slot0, int count) {
-        ga.slot0 = static_cast<int>(slot0);
-        with_type(s.type, [&](auto t) {
-          with_rank(std::min(s.rank, 64), [&](auto rt) {
-            if constexpr (decltype(rt)::value <= 4)
-              hipLaunchKernelGGL((grad_kernel<decltype(t)::value, decltype(rt)::value>),
-                                 dim3(static_cast<unsigned>(count * slot_blocks)), dim3(256), 0, stream, ga);
-          });
-        });
-        return launched();
-      });
+      launch_st = launches.grads(ga, l.most_slots, stream);
       if (launch_st != GEMM_OK) return launch_st;
     }
     const long long size_a = static_cast<long long>(s.rank) * s.K, size_b = static_cast<long long>(s.rank) * s.N;
     const int blocks = static_cast<int>(std::min<long long>(ceil_div(std::max(size_a, size_b), 1024), 64));
     const GradSumArgs ga{sums, {partial_a, partial_b}, {dA, dB}, {size_a, size_b}, blocks};
-    hipLaunchKernelGGL(grad_sum_kernel, dim3(static_cast<unsigned>(2 * blocks * s.adapters)), dim3(256), 0, stream, ga);
-    return launched();
+    return launches.sum(ga, 2 * blocks * s.adapters, stream);
   });
 }
 

@@ -1,0 +1,4 @@
+// The low-rank adapters' kernels for one element type.
+#include "lora_launch_type.hpp"
+
+const gemm::mx::LoraLaunches &gemm::mx::lora_launches_f32() { return launches_of<kF32>(); }

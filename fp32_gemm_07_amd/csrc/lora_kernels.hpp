@@ -39,11 +39,9 @@ struct LoraRows {
   const int *ids;
   const int *ranks;      // null: all `rank`
   const float *scales;   // null: all 1
-  __device__ inline int id(int row) const {   // -1: none
-    if (row >= rows) return -1;
-    const int a = ids[row];
-    return a >= 0 && a < adapters ? a : -1;
-  }
+  // A row's adapter, -1: none. (For rows past the last: the last one's.)
+  __device__ inline int load_id(int row) const { return ids[min(row, rows - 1)]; }
+  __device__ inline int id_of(int loaded) const { return loaded >= 0 && loaded < adapters ? loaded : -1; }
   __device__ inline int rank_of(int a) const { return ranks ? max(0, min(rank, ranks[a])) : rank; }
 };
 
@@ -56,19 +54,21 @@ template <int TYPE>
 __device__ inline uintx4 load_k(const typename Elem<TYPE>::store *p) {
   return *reinterpret_cast<const uintx4_any *>(p);
 }
-// The same at a row's end: `left` values (may be negative), zeros behind them.
+// The same at a row's end: `left` values (may be negative), zeros behind them. (All loads at
+// once, then the choice: one after the other each would be waited for.)
 template <int TYPE>
 __device__ inline uintx4 load_k(const typename Elem<TYPE>::store *p, int left) {
   if (left >= kLaneK<TYPE>) return load_k<TYPE>(p);
   uintx4 v = {};
-  if constexpr (TYPE == kF32) {
+  if (left > 0) {
+    typename Elem<TYPE>::store x[kLaneK<TYPE>];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) v[i] = __builtin_bit_cast(unsigned, p[i]);
-  } else {
+    for (int i = 0; i < kLaneK<TYPE>; ++i) x[i] = p[min(i, left - 1)];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) v[i / 2] |= static_cast<unsigned>(p[i]) << (16 * (i % 2));
+    for (int i = 0; i < kLaneK<TYPE>; ++i) {
+      if constexpr (TYPE == kF32) v[i] = i < left ? __builtin_bit_cast(unsigned, x[i]) : 0u;
+      else v[i / 2] |= i < left ? static_cast<unsigned>(x[i]) << (16 * (i % 2)) : 0u;
+    }
   }
   return v;
 }
@@ -115,7 +115,8 @@ struct Units {
   const LoraRows &r;
   const bool with_none;      // rows without an adapter make units too
   int window, end;
-  int my_id, next_id;        // of this lane's row in the window, and in the next one
+  int my_id;                 // of this lane's row in the window (-2: past the last row)
+  int next_id;               // of its row in the next one, as loaded: on its way meanwhile
   unsigned long long todo = 0, same = 0;
   int base = 0;
   // The current unit.
@@ -125,19 +126,15 @@ struct Units {
 
   __device__ inline Units(const LoraRows &rows, bool none, int first, int last)
       : r(rows), with_none(none), window(first - 1), end(last) {
-    next_id = fetch(first);
-  }
-  // (-2: past the last row)
-  __device__ inline int fetch(int w) const {
-    const int at = w * 64 + (threadIdx.x & 63);
-    return w < end && at < r.rows ? r.id(at) : -2;
+    next_id = r.load_id(first * 64 + (threadIdx.x & 63));
   }
   __device__ inline bool next() {
     if (!same) {
       while (!todo) {
         if (++window >= end) return false;
-        my_id = next_id;
-        next_id = fetch(window + 1);
+        const int at = window * 64 + (threadIdx.x & 63);
+        my_id = at < r.rows ? r.id_of(next_id) : -2;
+        next_id = r.load_id(at + 64);
         todo = __ballot(with_none ? my_id >= -1 : my_id >= 0);
       }
       id = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
@@ -145,8 +142,18 @@ struct Units {
       todo &= ~same;
       base = 0;
     }
-    // Lane l's row of the window goes to the lane of its number among the unit's.
     const int lane = threadIdx.x & 63, i16 = lane & 15;
+    if (same == ~0ull) {   // the whole window: row by row
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        real[m] = true;
+        row[m] = window * 64 + base + m * 16 + i16;
+      }
+      base += 16 * MT;
+      if (base == 64) same = 0;
+      return true;
+    }
+    // Lane l's row of the window goes to the lane of its number among the unit's.
     const int count = __popcll(same);
     const int number = __popcll(same & ((1ull << lane) - 1)) - base;
     const bool mine = (same >> lane & 1) && number >= 0 && number < 64;
@@ -172,8 +179,9 @@ struct Shrink {
   long long w_adapter, ldw;
   int K, k_split;      // columns of a workgroup's range, a multiple of 64
   int splits;
-  float *h;            // [split][rows][RP] sums of each range, or null
-  void *parts;         // for the gradients: [3][RP][positions] bfloat16 parts ([RP][positions] floats), or null
+  void *h;             // for expand, or null: [rows][3][RP] bfloat16 parts; for FP32 or where
+  bool floats;         // expand is to sum over ranges [split][rows][RP] floats
+  void *parts;         // for the gradients, or null: [3][RP][positions] bfloat16 parts, for FP32 [RP][positions] floats
 };
 struct ShrinkArgs {
   LoraRows r;
@@ -208,13 +216,15 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
   int turn = 0;
   for (int n = 0; unit.next(); ++n) {
     if (n % a.units_by != group) continue;
+    // (The adapter's own rank comes in at the end alone, so that no load waits for it.)
     const int id = unit.id, rank = a.r.rank_of(id);
+    const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
     f32x4 acc[MT][RT] = {};
-    if (rank > 0) {
+    {
       const store *w = static_cast<const store *>(p.w) + id * p.w_adapter + g * kLane;
       const store *wr[RT], *zr[MT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) wr[t] = w + min(t * 16 + i16, rank - 1) * p.ldw;   // (past the rank: not kept)
+      for (int t = 0; t < RT; ++t) wr[t] = w + min(t * 16 + i16, a.r.rank - 1) * p.ldw;   // (past the rank: not kept)
 #pragma unroll
       for (int m = 0; m < MT; ++m) zr[m] = static_cast<const store *>(p.z) + unit.row[m] * p.ldz + g * kLane;
       struct Fetched {
@@ -270,7 +280,6 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) half[((wave * MT + m) * RT + t) * 64 + lane] = acc[m][t];
     __syncthreads();
-    const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -284,25 +293,40 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
         for (int i = 0; i < 4; ++i) v[i] = t * 16 + 4 * g + i < rank ? v[i] * scale : 0.0f;
         const int row = unit.row[m];
         if (!unit.real[m]) continue;
-        if (p.h)
-          *reinterpret_cast<f32x4 *>(p.h + (static_cast<long long>(split) * a.r.rows + row) * RP + t * 16 + 4 * g) = v;
-        if (p.parts) {
-          const int at = a.position[row];
-          const long long plane = static_cast<long long>(RP) * a.positions;
+        if (p.h && (TYPE == kF32 || p.floats))
+          *reinterpret_cast<f32x4 *>(static_cast<float *>(p.h) + (static_cast<long long>(split) * a.r.rows + row) * RP +
+                                     t * 16 + 4 * g) = v;
+        const int at = p.parts ? a.position[row] : 0;
+        if constexpr (TYPE == kF32) {
+          if (p.parts) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              static_cast<float *>(p.parts)[static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at] = v[i];
+          }
+        } else {
+          typedef u16 u16x4 __attribute__((ext_vector_type(4)));
+          u16x4 part[3];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const long long to = static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at;
-            if constexpr (TYPE == kF32) {
-              static_cast<float *>(p.parts)[to] = v[i];
-            } else {
-              float rest = v[i];
+            float rest = v[i];
 #pragma unroll
-              for (int q = 0; q < 3; ++q) {
-                const u16 part = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
-                static_cast<u16 *>(p.parts)[q * plane + to] = part;
-                rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part);
-              }
+            for (int q = 0; q < 3; ++q) {
+              part[q][i] = static_cast<u16>(__builtin_bit_cast(unsigned, rest) >> 16);
+              rest = __builtin_isinf(rest) ? 0.0f : rest - Elem<kBf16>::get(part[q][i]);
             }
+          }
+          if (p.h && !p.floats) {
+            u16 *to = static_cast<u16 *>(p.h) + static_cast<long long>(row) * (3 * RP) + t * 16 + 4 * g;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *reinterpret_cast<u16x4 *>(to + q * RP) = part[q];
+          }
+          if (p.parts) {
+            const long long plane = static_cast<long long>(RP) * a.positions;
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                static_cast<u16 *>(p.parts)[q * plane + static_cast<long long>(t * 16 + 4 * g + i) * a.positions + at] = part[q][i];
           }
         }
       }
@@ -313,7 +337,7 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
 // expand.
 struct ExpandArgs {
   LoraRows r;
-  const float *h;          // [splits][rows][RP]
+  const void *h;           // as shrink left it: parts, or sums of `splits` ranges
   int splits;
   const void *w;           // adapter a's N x rank at w + a * w_adapter, row stride ldw
   long long w_adapter, ldw;
@@ -322,44 +346,69 @@ struct ExpandArgs {
   void *y;
   long long ldy;
   int N, windows;          // of a workgroup
-  int units_by;
+  int units_by;            // workgroups that the units are dealt out among
   bool in_place;           // c is y
 };
 
 // A wave keeps 16 J rows of an adapter's B in registers and takes unit after unit, every
 // units_by-th of its windows'; they are loaded again where the adapter changes. C and H of
-// the next unit are on their way meanwhile. Row m of instruction j is column 4 J (m / 4) +
-// 4 j + m % 4 of the wave's, so that a lane's results are 4 J neighbouring columns of
-// one row of Y.
-template <int TYPE, int RT, int J>
+// the next units are on their way meanwhile. The products leave through LDS, so that C and Y
+// move as whole lines of a row (128 bytes with J = 4), which the layout of the
+// instructions' results, 16 rows beside each other, would cut into halves.
+// SUM: H are floats of several ranges of K (few rows), which are summed here. What is loaded
+// for a unit depends on nothing else, so that the compiler can count how many loads may be
+// on their way: without a C, Y is read in its place and the values are not used.
+template <int TYPE, int RT, int J, bool SUM>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   typedef typename Elem<TYPE>::store store;
-  constexpr int RP = 16 * RT, COLS = 4 * J, kLane = kLaneK<TYPE>, CW = (COLS + kLane - 1) / kLane;
+  constexpr int RP = 16 * RT, kLane = kLaneK<TYPE>, COLS = 16 * J;
   constexpr int KS = TYPE == kF32 ? RT : (RT + 1) / 2;   // operands along the rank: of 16 or 32
   constexpr int PB = TYPE == kF16 ? 2 : 1;               // parts of B
   constexpr int PH = TYPE == kF32 ? 1 : 3;               // parts of H
+  constexpr int VEC = J == 1 ? 4 : kLane;                // values of C and Y that a lane moves at a time
+  constexpr int kRowLanes = COLS / VEC, kRowsAt = 64 / kRowLanes, CW = 16 / kRowsAt;
+  constexpr int kDepth = KS * PH + CW <= 8 ? 4 : 2;      // units on their way (SUM: one)
+  constexpr int kStride = COLS + 4;                      // floats of a row in LDS
+  __shared__ __attribute__((aligned(16))) float stages[4][16 * kStride];
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col_blocks = (a.N + 64 * J - 1) / (64 * J);
-  const int nb = (blockIdx.x % col_blocks * 4 + wave) * 16 * J;
+  float *stage = stages[wave];
+  const int col_blocks = (a.N + 4 * COLS - 1) / (4 * COLS);
+  const int nb = (blockIdx.x % col_blocks * 4 + wave) * COLS;
   if (nb >= a.N) return;
   const int group = blockIdx.x / col_blocks % a.units_by;
   const int window0 = blockIdx.x / col_blocks / a.units_by * a.windows;
   const int window1 = min(window0 + a.windows, (a.r.rows + 63) / 64);
-  const int n_lane = nb + COLS * g, left = a.N - n_lane;
+  const int n_lane = nb + lane % kRowLanes * VEC, left = a.N - n_lane;
 
   uintx4 b[J][KS][PB];
   int have = -1;
+  const store *c_or_y = static_cast<const store *>(a.c ? a.c : a.y);
+  const long long ld_c_or_y = a.c ? a.ldc : a.ldy;
   auto load_adapter = [&](int id) __attribute__((always_inline)) {
     const int rank = a.r.rank_of(id);
     const store *w = static_cast<const store *>(a.w) + id * a.w_adapter;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int n = min(nb + COLS * (i16 >> 2) + 4 * j + (i16 & 3), a.N - 1);
+      const int n = min(nb + 16 * j + i16, a.N - 1);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int r = s * 4 * kLane + g * kLane;
-        b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, rank - r);
+        b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, a.r.rank - r);
+      }
+    }
+    // What is stored behind the adapter's own rank goes (after the loads: none waits for the rank).
+    if (rank < a.r.rank) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int real = rank - (s * 4 * kLane + g * kLane);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == kF32) b[j][s][0][i] = i < real ? b[j][s][0][i] : 0;
+            else b[j][s][0][i] = 2 * i + 1 < real ? b[j][s][0][i] : 2 * i < real ? b[j][s][0][i] & 0xffff : 0;
+          }
       }
     }
     if constexpr (PB == 2) {
@@ -373,22 +422,24 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
           b[j][s][1] = __builtin_bit_cast(uintx4, parts[1]);
         }
     }
+    // (here, or every use of them would wait for all loads)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) arrived(b[j][s][0]);
   };
 
   struct Fetched {
-    int id, row;
-    bool real;
-    uintx4 c[CW];
-    f32x4 h[KS][kLane / 4];
+    int id;
+    int row[CW];   // of the lane's values; ~row past the unit's last
+    uintx4 c[CW], h[KS][PH];
   };
   Units<1> unit(a.r, !a.in_place, window0, window1);
-  int n = -1;
+  int skip = group;   // units of other workgroups before the next of this one's
   auto advance = [&]() __attribute__((always_inline)) {
-    bool more;
-    do {
-      more = unit.next();
-      ++n;
-    } while (more && n % a.units_by != group);
+    bool more = unit.next();
+    for (; more && skip > 0; --skip) more = unit.next();
+    skip = a.units_by - 1;
     return more;
   };
   // WHOLE: all of the wave's columns exist.
@@ -396,123 +447,204 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
     constexpr bool WHOLE = decltype(whole)::value;
     auto fetch = [&](Fetched &f) __attribute__((always_inline)) {
       f.id = unit.id;
-      f.row = unit.row[0];
-      f.real = unit.real[0];
-      if (a.c) {
-        const store *c = static_cast<const store *>(a.c) + f.row * a.ldc + n_lane;
+      const int mine = unit.row[0], marked = unit.real[0] ? mine : ~mine;
 #pragma unroll
-        for (int q = 0; q < CW; ++q) {
-          if constexpr (COLS < kLane) f.c[q] = load_k<TYPE>(c, WHOLE ? COLS : min(COLS, left));
-          else if constexpr (WHOLE) f.c[q] = load_k<TYPE>(c + q * kLane);
-          else f.c[q] = load_k<TYPE>(c + q * kLane, left - q * kLane);
+      for (int q = 0; q < CW; ++q) {
+        f.row[q] = __shfl(marked, q * kRowsAt + lane / kRowLanes);
+        const store *c = c_or_y + max(f.row[q], ~f.row[q]) * ld_c_or_y + n_lane;
+        if constexpr (VEC < kLane) {
+          typedef store store4 __attribute__((ext_vector_type(4), aligned(sizeof(store))));
+          store4 v = {};
+          if (WHOLE || left >= 4) {
+            v = *reinterpret_cast<const store4 *>(c);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < left) v[i] = c[i];
+          }
+          f.c[q] = uintx4{static_cast<unsigned>(v[0]) | static_cast<unsigned>(v[1]) << 16,
+                          static_cast<unsigned>(v[2]) | static_cast<unsigned>(v[3]) << 16, 0, 0};
+        } else if constexpr (WHOLE) {
+          f.c[q] = load_k<TYPE>(c);
+        } else {
+          f.c[q] = load_k<TYPE>(c, left);
         }
       }
-      const float *h = a.h + static_cast<long long>(f.row) * RP;
+      // (Of the 32 ranks of an operand the upper 16 do not exist where RP is 16: the lower again.)
+      if constexpr (TYPE != kF32 && !SUM) {
+        const u16 *h = static_cast<const u16 *>(a.h) + static_cast<long long>(mine) * (3 * RP);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        // (the upper half of 32 ranks where RP is 16: the lower again, not used)
-        const int r = (s * 4 * kLane + g * kLane) % RP;
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < kLane / 4; ++i) f.h[s][i] = reinterpret_cast<const f32x4 *>(h + r)[i];
-      }
-      for (int q = 1; q < a.splits; ++q) {
-        const float *part = h + static_cast<long long>(q) * a.r.rows * RP;
+          for (int q = 0; q < PH; ++q)
+            f.h[s][q] = *reinterpret_cast<const uintx4 *>(h + q * RP + (s * 32 + g * 8) % RP);
+      } else {
+        const float *h = static_cast<const float *>(a.h) + static_cast<long long>(mine) * RP;
+        const long long range = static_cast<long long>(a.r.rows) * RP;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const int r = (s * 4 * kLane + g * kLane) % RP;
+          const float *from = h + (s * 4 * kLane + g * kLane) % RP;
+          f32x4 v[kLane / 4];
 #pragma unroll
-          for (int i = 0; i < kLane / 4; ++i) f.h[s][i] += reinterpret_cast<const f32x4 *>(part + r)[i];
+          for (int i = 0; i < kLane / 4; ++i) v[i] = reinterpret_cast<const f32x4 *>(from)[i];
+          if constexpr (SUM) {   // four more ranges at a time
+            for (int q = 1; q < a.splits; q += 4) {
+              f32x4 x[4][kLane / 4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < kLane / 4; ++i)
+                  x[m][i] = reinterpret_cast<const f32x4 *>(from + min(q + m, a.splits - 1) * range)[i];
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < kLane / 4; ++i) v[i] += q + m < a.splits ? x[m][i] : f32x4{};
+            }
+          }
+          if constexpr (TYPE == kF32) {
+            f.h[s][0] = __builtin_bit_cast(uintx4, v[0]);
+          } else {
+            float y[8];
+            floats8(v[0], v[1], y);
+            bf16x8 parts[3];
+            split8<3>(y, parts);
+#pragma unroll
+            for (int q = 0; q < PH; ++q) f.h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
+          }
         }
       }
     };
-    auto finish = [&](const Fetched &f) __attribute__((always_inline)) {
-      float out[COLS];
+    // H B^T of a unit to LDS: lane (g, i16) has columns 16 j + 4 g .. + 3 of row i16.
+    auto product = [&](const Fetched &f) __attribute__((always_inline)) {
+      const bool upper = RP % 32 != 0 && g >= 2;   // ranks that do not exist
+      uintx4 h[KS][PH];
 #pragma unroll
-      for (int q = 0; q < COLS; ++q) {
-        if (!a.c) {
-          out[q] = 0.0f;
-        } else if constexpr (TYPE == kF32) {
-          const unsigned w = f.c[q / 4][q % 4];
-          out[q] = __builtin_bit_cast(float, w);
-        } else {
-          const unsigned w = f.c[q / 8][q % 8 / 2];
-          out[q] = Elem<TYPE>::get(static_cast<u16>(q % 2 ? w >> 16 : w));
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int q = 0; q < PH; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[s][q][i] = TYPE != kF32 && upper ? 0u : f.h[s][q][i];
+      f32x4 sum[J] = {};
+      if constexpr (TYPE == kF32) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int s = 0; s < KS; ++s) sum[j] = multiply<kF32>(b[j][s][0], h[s][0], sum[j]);
+      } else {
+        auto first = [&](int j, f32x4 acc) __attribute__((always_inline)) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) acc = multiply<kBf16>(b[j][s][0], h[s][0], acc);
+          return acc;
+        };
+        float check = 0.0f;   // NaN with anything that is not finite
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          // small products first (the third part of H times the second of B is below 2^-24)
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int q = PH - 1; q > 0; --q) sum[j] = multiply<kBf16>(b[j][s][0], h[s][q], sum[j]);
+            if constexpr (PB == 2) {
+              sum[j] = multiply<kBf16>(b[j][s][1], h[s][1], sum[j]);
+              sum[j] = multiply<kBf16>(b[j][s][1], h[s][0], sum[j]);
+            }
+          }
+          sum[j] = first(j, sum[j]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) check = fmaf(sum[j][v], 0.0f, check);
+        }
+        if (__any(check != check)) {
+          // The other parts of an infinity, or products of zeros with one, are NaN: where the first
+          // parts' sum is not finite it stands alone.
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const f32x4 alone = first(j, f32x4{});
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sum[j][v] = __builtin_isfinite(alone[v]) ? sum[j][v] : alone[v];
+          }
         }
       }
+      wave_order();
+#pragma unroll
+      for (int j = 0; j < J; ++j) *reinterpret_cast<f32x4 *>(stage + i16 * kStride + 16 * j + 4 * g) = sum[j];
+      wave_order();
+    };
+    auto finish = [&](const Fetched &f) __attribute__((always_inline)) {
       if (f.id >= 0) {
         if (f.id != have) {
           load_adapter(f.id);
           have = f.id;
         }
-        uintx4 h[KS][PH];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          if constexpr (TYPE == kF32) {
-            h[s][0] = __builtin_bit_cast(uintx4, f.h[s][0]);
-          } else {
-            float x[8];
-            floats8(f.h[s][0], f.h[s][1], x);
-            if (s * 32 + g * 8 >= RP) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-            }
-            bf16x8 parts[3];
-            split8<3>(x, parts);
-#pragma unroll
-            for (int q = 0; q < PH; ++q) h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          // first: the products of the first parts; where their sum is not finite it is
-          // the result (the other parts of an infinity, or its products with zeros, are NaN)
-          f32x4 first = {}, rest = {};
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            if constexpr (TYPE == kF32) {
-              first = multiply<kF32>(b[j][s][0], h[s][0], first);
-            } else {
-              first = multiply<kBf16>(b[j][s][0], h[s][0], first);
-#pragma unroll
-              for (int q = 1; q < PH; ++q) rest = multiply<kBf16>(b[j][s][0], h[s][q], rest);
-              if constexpr (PB == 2) {   // (the third part of H times the second of B is below 2^-24)
-                rest = multiply<kBf16>(b[j][s][1], h[s][0], rest);
-                rest = multiply<kBf16>(b[j][s][1], h[s][1], rest);
-              }
-            }
-          }
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            out[4 * j + v] += TYPE == kF32 || !__builtin_isfinite(first[v]) ? first[v] : first[v] + rest[v];
-          }
-        }
+        product(f);
       }
-      if (!f.real) return;
-      store *y = static_cast<store *>(a.y) + f.row * a.ldy + n_lane;
-      if constexpr (COLS >= 8) {
 #pragma unroll
-        for (int q = 0; q < COLS; q += 8) store8<TYPE>(y + q, WHOLE ? 8 : left - q, reinterpret_cast<float(&)[8]>(out[q]));
-      } else {
+      for (int q = 0; q < CW; ++q) {
+        float out[8];
 #pragma unroll
-        for (int q = 0; q < COLS; ++q)
-          if (WHOLE || q < left) y[q] = Elem<TYPE>::put(out[q]);
+        for (int i = 0; i < VEC; ++i) {
+          const unsigned w = TYPE == kF32 ? f.c[q][i % 4] : f.c[q][i / 2];
+          if (!a.c) out[i] = 0.0f;
+          else if constexpr (TYPE == kF32) out[i] = __builtin_bit_cast(float, w);
+          else out[i] = Elem<TYPE>::get(static_cast<u16>(i % 2 ? w >> 16 : w));
+        }
+        if (f.id >= 0) {
+          const float *from = stage + (q * kRowsAt + lane / kRowLanes) * kStride + lane % kRowLanes * VEC;
+#pragma unroll
+          for (int i = 0; i < VEC; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(from + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[i + k] += v[k];
+          }
+        }
+        if (f.row[q] < 0) continue;
+        store *y = static_cast<store *>(a.y) + f.row[q] * a.ldy + n_lane;
+        if constexpr (VEC == 8) {
+          store8<TYPE>(y, WHOLE ? 8 : left, out);
+        } else {
+          typedef store store4 __attribute__((ext_vector_type(4), aligned(sizeof(store))));
+          if (WHOLE || left >= 4) {
+            *reinterpret_cast<store4 *>(y) =
+                store4{Elem<TYPE>::put(out[0]), Elem<TYPE>::put(out[1]), Elem<TYPE>::put(out[2]), Elem<TYPE>::put(out[3])};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < left) y[i] = Elem<TYPE>::put(out[i]);
+          }
+        }
       }
     };
     if (!advance()) return;
-    Fetched even, odd;
-    fetch(even);
+    if (unit.id >= 0) {   // (before what H may have to be summed from)
+      load_adapter(unit.id);
+      have = unit.id;
+    }
+    if constexpr (SUM) {
+      Fetched f;
+      do {
+        fetch(f);
+        finish(f);
+      } while (advance());
+      return;
+    }
+    // (After the last unit the same again: a branch around loads would wait for them.)
+    Fetched f[kDepth];
+    bool more[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      more[d] = d == 0 || (more[d - 1] && advance());
+      fetch(f[d]);
+    }
     while (true) {
-      bool more = advance();
-      fetch(odd);   // (after the last unit the same again: a branch around loads would wait for them)
-      finish(even);
-      if (!more) break;
-      more = advance();
-      fetch(even);
-      finish(odd);
-      if (!more) break;
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (!more[d]) return;
+        finish(f[d]);
+        more[d] = more[(d + kDepth - 1) % kDepth] && advance();
+        fetch(f[d]);
+      }
     }
   };
-  if (nb + 16 * J <= a.N) run(std::true_type());
+  if (nb + COLS <= a.N) run(std::true_type());
   else run(std::false_type());
 }
 
@@ -610,12 +742,25 @@ __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
   __syncthreads();
   const int per = ((a.r.rows + W - 1) / W + 63) / 64 * 64;
   const int from = min(a.r.rows, wave * per), to = min(a.r.rows, from + per);
-  for (int row0 = from; row0 < to; row0 += 64) {
-    const int id = row0 + lane < to ? a.r.id(row0 + lane) : -1;
+  // step(row, id) for 64 of the wave's rows after the other, the ids of 8 such on their way at a time.
+  auto over_rows = [&](auto &&step) __attribute__((always_inline)) {
+    constexpr int kAt = 8;
+    for (int row0 = from; row0 < to; row0 += 64 * kAt) {
+      int loaded[kAt];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) loaded[i] = a.r.load_id(row0 + i * 64 + lane);
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const int row = row0 + i * 64 + lane;
+        if (row - lane < to) step(row, row < to ? a.r.id_of(loaded[i]) : -1);
+      }
+    }
+  };
+  over_rows([&](int, int id) {
     const unsigned long long same = same_id(id, id >= 0, bits);
     if (id >= 0 && (same & ((1ull << lane) - 1)) == 0) count[wave * kLoraMaxAdapters + id] += __popcll(same);
     wave_order();
-  }
+  });
   __syncthreads();
   // Thread t has adapter t: its rows, positions (rounded up to 32), slots and partial sums,
   // and running sums of the last three over all adapters.
@@ -651,20 +796,18 @@ __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
     for (int w = 0; w < W; ++w) count[w * kLoraMaxAdapters + id] += before[0];
   }
   __syncthreads();
-  for (int row0 = from; row0 < to; row0 += 64) {
-    const int row = row0 + lane;
-    const int mine = row < to ? a.r.id(row) : -1;
+  over_rows([&](int row, int mine) {
     const unsigned long long same = same_id(mine, mine >= 0, bits);
-    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int number = __popcll(same & ((1ull << lane) - 1));
     if (mine >= 0) {
-      const int at = count[wave * kLoraMaxAdapters + mine] + rank;
+      const int at = count[wave * kLoraMaxAdapters + mine] + number;
       a.order[at] = row;
       a.position[row] = at;
     }
     wave_order();
-    if (mine >= 0 && rank == 0) count[wave * kLoraMaxAdapters + mine] += __popcll(same);
+    if (mine >= 0 && number == 0) count[wave * kLoraMaxAdapters + mine] += __popcll(same);
     wave_order();
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -721,14 +864,13 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) rows[i] = a.order[slot.first + min(at + g * kRows + i, slot.count - 1)];
   };
-  const bool whole = (block * 16 + 16) * CL <= p.cols;
-  auto fetch = [&](Fetched &f, int at, const int (&rows)[kRows]) __attribute__((always_inline)) {
-    if (whole) {
+  // WHOLE: all of the workgroup's columns exist.
+  auto fetch = [&](auto whole, Fetched &f, int at, const int (&rows)[kRows]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) f.x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + rows[i] * p.ldz + n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) f.x[i] = load_k<TYPE>(static_cast<const store *>(p.z) + rows[i] * p.ldz + n, left);
+    for (int i = 0; i < kRows; ++i) {
+      const store *z = static_cast<const store *>(p.z) + rows[i] * p.ldz + n;
+      if constexpr (decltype(whole)::value) f.x[i] = load_k<TYPE>(z);
+      else f.x[i] = load_k<TYPE>(z, left);
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -793,12 +935,12 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
   // one is multiplied.
   int at = wave * kStep;
   const int steps = (slot.count - at + 4 * kStep - 1) / (4 * kStep);
-  if (steps > 0) {
+  auto run = [&](auto whole) __attribute__((always_inline)) {
     int rows[kRows];
     auto step = [&](Fetched &cur, Fetched &next) __attribute__((always_inline)) {
       // (past the last step: its rows, and positions that exist, once more)
       const int then = min(at + 4 * kStep, wave * kStep + (steps - 1) * 4 * kStep);
-      fetch(next, then, rows);
+      fetch(whole, next, then, rows);
       rows_of(then + 4 * kStep, rows);
       __builtin_amdgcn_sched_barrier(0);
       if (at + kStep > slot.count) cut(cur, at);
@@ -807,9 +949,13 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     };
     Fetched even, odd;
     rows_of(at, rows);
-    fetch(even, at, rows);
+    fetch(whole, even, at, rows);
     rows_of(min(at + 4 * kStep, wave * kStep + (steps - 1) * 4 * kStep), rows);
     in_turn(steps, even, odd, step);
+  };
+  if (steps > 0) {
+    if ((block * 16 + 16) * CL <= p.cols) run(std::true_type());
+    else run(std::false_type());
   }
   // The waves' sums in order.
   for (int w = 3; w > 0; --w) {
@@ -852,6 +998,7 @@ struct GradSumArgs {
   long long size[2];     // of one adapter's
   int blocks;            // workgroups for each adapter's, of each of the two
 };
+template <int>
 __global__ __launch_bounds__(256) void grad_sum_kernel(GradSumArgs a) {
   const int id = blockIdx.x / (2 * a.blocks), block = blockIdx.x % (2 * a.blocks);
   const int2 s = a.sums[id];

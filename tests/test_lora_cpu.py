@@ -88,8 +88,10 @@ def test_workspace_sizes():
     for bad in ({"n": 0}, {"rank": 129}, {"type": 4}, {"count": 1025}):
         assert lib.gemm_lora_workspace_bytes(8, adapters(**bad)) == lib.gemm_lora_backward_workspace_bytes(8, adapters(**bad)) == 0, bad
     assert lib.gemm_lora_workspace_bytes(0, adapters()) == lib.gemm_lora_workspace_bytes(-1, adapters()) == 0
-    # H alone for many rows, whatever the columns
-    assert lib.gemm_lora_workspace_bytes(1 << 20, adapters(n=1 << 18, k=1 << 18, rank=128)) == (1 << 20) * 128 * 4
+    # H alone for many rows, whatever the columns: floats, or three bfloat16 parts
+    many = {"n": 1 << 18, "k": 1 << 18, "rank": 128}
+    assert lib.gemm_lora_workspace_bytes(1 << 20, adapters(**many)) == (1 << 20) * 128 * 4
+    assert lib.gemm_lora_workspace_bytes(1 << 20, adapters(type=1, **many)) == (1 << 20) * 128 * 6
     # past 32 bits: B once more
     assert lib.gemm_lora_backward_workspace_bytes(1, adapters(n=1 << 18, rank=128, count=1024)) > (1 << 18) * 128 * 1024 * 4
 
