@@ -205,7 +205,9 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
   int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
   const int split = block % p.splits;
   block /= p.splits;
-  const int group = block % a.units_by, window = block / a.units_by;
+  // (Workgroups that a window has no unit for come last: dealt out between the others they
+  // would leave whole XCDs idle.)
+  const int windows = (a.r.rows + 63) / 64, group = block / windows, window = block - group * windows;
   const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int k_wave = (p.k_split / W + 63) / 64 * 64;
@@ -376,9 +378,9 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   const int col_blocks = (a.N + 4 * COLS - 1) / (4 * COLS);
   const int nb = (blockIdx.x % col_blocks * 4 + wave) * COLS;
   if (nb >= a.N) return;
-  const int group = blockIdx.x / col_blocks % a.units_by;
-  const int window0 = blockIdx.x / col_blocks / a.units_by * a.windows;
-  const int window1 = min(window0 + a.windows, (a.r.rows + 63) / 64);
+  const int windows = (a.r.rows + 63) / 64, ranges = (windows + a.windows - 1) / a.windows;
+  const int range = blockIdx.x / col_blocks, group = range / ranges;   // (group slowest, as in shrink)
+  const int window0 = (range - group * ranges) * a.windows, window1 = min(window0 + a.windows, windows);
   const int n_lane = nb + lane % kRowLanes * VEC, left = a.N - n_lane;
 
   uintx4 b[J][KS][PB];
