@@ -37,14 +37,16 @@ void with_experts(int experts, F &&f) {
   else f(std::integral_constant<int, 32>());
 }
 
-template <int TYPE, int PER, class KEY>
-int launch_route(const RouteArgs &a, int cus, hipStream_t stream) {
-  const size_t row_keys = a.groups > a.top_groups ? sizeof(KEY) * a.experts : 0;
+template <int TYPE, int PER, bool VALUES>
+int launch_route(RouteArgs a, int cus, hipStream_t stream) {
+  // LDS for a row's keys: doubles, or whole numbers where groups are chosen.
+  const size_t row_keys = VALUES ? 8 * static_cast<size_t>(a.experts) : a.groups > a.top_groups ? 4 * static_cast<size_t>(a.experts + a.experts % 2) : 0;
+  a.row_bytes = static_cast<int>(row_keys);
   // Few tokens: one workgroup, which needs no counts zeroed by a launch before it.
   // (Of fewer waves where a lane holds more experts: their values take its registers.)
-  constexpr int kOne = PER <= 8 ? 1024 : PER == 16 ? 512 : 256;
+  constexpr int kOne = PER <= (VALUES ? 4 : 8) ? 1024 : PER <= 16 ? 512 : 256;
   if (a.counts && a.tokens <= 64) {
-    hipLaunchKernelGGL((route_kernel<TYPE, PER, KEY, kOne>), dim3(1), dim3(kOne), row_keys * (kOne / 16), stream, a);
+    hipLaunchKernelGGL((route_kernel<TYPE, PER, VALUES, kOne>), dim3(1), dim3(kOne), row_keys * (kOne / 16), stream, a);
     return launched();
   }
   if (a.counts) {
@@ -52,9 +54,17 @@ int launch_route(const RouteArgs &a, int cus, hipStream_t stream) {
     const int st = launched();
     if (st != GEMM_OK) return st;
   }
-  const long long blocks = std::min<long long>(ceil_div(a.tokens, 16), 8LL * cus);
-  hipLaunchKernelGGL((route_kernel<TYPE, PER, KEY, 256>), dim3(static_cast<unsigned>(blocks)), dim3(256),
-                     row_keys * 16, stream, a);
+  // Each workgroup adds its counts to the same few words, which takes some 15 ns each: no more
+  // than one a CU (65536 tokens on 64 experts: 256 of 1024 threads 24 us, 2048 of 256 48).
+  const long long blocks = ceil_div(a.tokens, 16);
+  if (a.counts && blocks > cus) {
+    hipLaunchKernelGGL((route_kernel<TYPE, PER, VALUES, kOne>),
+                       dim3(static_cast<unsigned>(std::min<long long>(ceil_div(a.tokens, kOne / 16), cus))), dim3(kOne),
+                       row_keys * (kOne / 16), stream, a);
+  } else {
+    hipLaunchKernelGGL((route_kernel<TYPE, PER, VALUES, 256>), dim3(static_cast<unsigned>(std::min(blocks, 8LL * cus))),
+                       dim3(256), row_keys * 16, stream, a);
+  }
   return launched();
 }
 
@@ -84,13 +94,13 @@ int gemm_route(int tokens, const gemm_route_t *router, const void *logits, int l
   const int size = r.experts / r.groups;
   const RouteArgs a{tokens, r.experts, r.top_k, r.score, r.groups, r.top_groups, r.group_top, r.renormalize != 0,
                     r.scale, logits, ld_logits, bias, chosen, weights, counts,
-                    static_cast<unsigned>(ceil_div(1 << 20, size)), size};
+                    static_cast<unsigned>(ceil_div(1 << 20, size)), size, 0};
   // Scores are computed where the order of the logits does not settle the choice.
   const bool values = bias || (r.top_groups < r.groups && r.group_top == 2 && size > 1);
   with_type(logits_type, [&](auto t) {
     with_experts(r.experts, [&](auto per) {
       constexpr int T = decltype(t)::value, PER = decltype(per)::value;
-      st = values ? launch_route<T, PER, double>(a, cus, stream) : launch_route<T, PER, unsigned>(a, cus, stream);
+      st = values ? launch_route<T, PER, true>(a, cus, stream) : launch_route<T, PER, false>(a, cus, stream);
     });
   });
   return st;

@@ -9,9 +9,9 @@
 //
 // Values that the choice compares are exact or 64 bits wide. Both scores rise with the
 // logit, so where neither a bias nor sums of a group's scores come in, logits are compared
-// themselves (as whole numbers in their order); else the scores are computed in FP64, so that
-// experts whose scores lie next to each other are not taken for equal or the other way
-// round by roundings of FP32.
+// themselves (as whole numbers in their order). Else scores are computed in FP32 first; where
+// two values that the choice sets apart lie nearer to each other than their errors (one token in
+// some hundred), FP64 values settle it: of 16 candidates, a lane each, or of all.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -36,6 +36,7 @@ struct RouteArgs {
   int *counts;             // zeroed, or written whole by the only workgroup
   unsigned group_mul;      // e * group_mul >> 20 = e / (experts / groups) for e < 512
   int group_size;
+  int row_bytes;           // of the LDS that a row's keys pass through
 };
 
 struct RouteGradArgs {
@@ -88,16 +89,24 @@ __device__ inline T row_total(T v) {
 }
 
 // What the choice compares: whole numbers in the order of logits, 0 for one that is not
-// to be chosen; or values of 64 bits, -inf for those.
+// to be chosen; or values, -inf for those: estimates in FP32, or as they are in FP64.
 template <class KEY>
 struct KeyOf;
 template <>
 struct KeyOf<unsigned> {
+  static constexpr bool sums = false, estimate = false;
   static constexpr unsigned none = 0;
   static __device__ inline bool some(unsigned k) { return k != 0; }
 };
 template <>
+struct KeyOf<float> {
+  static constexpr bool sums = true, estimate = true;
+  static constexpr float none = -__builtin_inff();
+  static __device__ inline bool some(float k) { return k > -__builtin_inff(); }
+};
+template <>
 struct KeyOf<double> {
+  static constexpr bool sums = true, estimate = false;
   static constexpr double none = -__builtin_huge_val();
   static __device__ inline bool some(double k) { return k > -__builtin_huge_val(); }
 };
@@ -138,12 +147,110 @@ __device__ inline void best_of(const KEY (&key)[PER], int l16, KEY &best, int &a
   at = expert_of(at, l16);
 }
 
-// The best groups, as bits: a group's value is the largest key of its experts or the sum
-// of the two largest. The row's keys pass through LDS, where a lane looks a whole group over,
-// starting at another place than its neighbours (their groups lie a multiple of some
-// power of two apart).
+// The two largest keys of group g, in a row's LDS: looked over by one lane, starting at another
+// place than its neighbours (their groups lie a multiple of some power of two apart).
+template <class KEY>
+__device__ inline void group_top(const RouteArgs &a, int g, int l16, const KEY *keys, KEY &first, KEY &second) {
+  first = second = KeyOf<KEY>::none;
+  int at = l16 % a.group_size;
+  for (int i = 0; i < a.group_size; ++i) {
+    const KEY k = keys[g * a.group_size + at];
+    if (++at == a.group_size) at = 0;
+    second = k > first ? first : k > second ? k : second;
+    first = k > first ? k : first;
+  }
+}
+template <class KEY>
+__device__ inline KEY group_value(const RouteArgs &a, KEY first, KEY second) {
+  // (whole numbers are compared where the largest alone counts)
+  if constexpr (KeyOf<KEY>::sums) return a.group_top == 2 && KeyOf<KEY>::some(second) ? first + second : first;
+  else return first;
+}
+
+// The best groups, as bits, from the values of groups l16, l16 + 16, ... `apart`, for floats:
+// how much the last group that stays is worth more than the best that does not.
+constexpr int kRowGroups = kRouteMaxGroups / 16;
+template <class KEY>
+__device__ inline unsigned long long choose_groups(const RouteArgs &a, KEY (&value)[kRowGroups], int l16,
+                                                   KEY *apart = nullptr) {
+  unsigned long long stay = 0;
+  KEY last = KeyOf<KEY>::none;
+  for (int n = 0; n <= a.top_groups; ++n) {
+    KEY best = KeyOf<KEY>::none;
+    int at = kRouteMaxGroups;
+#pragma unroll
+    for (int m = 0; m < kRowGroups; ++m) {
+      if (value[m] > best) {
+        best = value[m];
+        at = m * 16 + l16;
+      }
+    }
+    const KEY most = row_max(best);
+    const bool some = KeyOf<KEY>::some(most);
+    if constexpr (KeyOf<KEY>::sums)
+      if (apart) *apart = some ? last - most : -KeyOf<KEY>::none;
+    if (n == a.top_groups || !some) break;   // (rows differ: the lanes of one leave together)
+    last = most;
+    const int g = row_min(best == most ? at : kRouteMaxGroups);
+    stay |= 1ull << g;
+#pragma unroll
+    for (int m = 0; m < kRowGroups; ++m)
+      if (m * 16 + l16 == g) value[m] = KeyOf<KEY>::none;
+  }
+  return stay;
+}
+template <class KEY>
+__device__ inline unsigned long long best_groups(const RouteArgs &a, int l16, const KEY *keys, KEY *apart = nullptr) {
+  KEY value[kRowGroups];
+#pragma unroll
+  for (int m = 0; m < kRowGroups; ++m) {
+    KEY first = KeyOf<KEY>::none, second = KeyOf<KEY>::none;
+    if (m * 16 + l16 < a.groups) group_top(a, m * 16 + l16, l16, keys, first, second);
+    value[m] = group_value(a, first, second);
+  }
+  return choose_groups(a, value, l16, apart);
+}
+
+// A sigmoid score with its bias in FP64.
+template <int TYPE>
+__device__ inline double sigmoid_value(const RouteArgs &a, const typename Elem<TYPE>::store *row, int e) {
+  const double v = 1.0 / (1.0 + exp(-static_cast<double>(Elem<TYPE>::get(row[e]))));
+  return a.bias ? v + static_cast<double>(a.bias[e]) : v;
+}
+
+// Where the estimates (in LDS) leave the groups open: the same from the FP64 values of the few
+// experts of each group that may be among its two largest.
+template <int TYPE>
+__device__ unsigned long long settle_groups(const RouteArgs &a, const typename Elem<TYPE>::store *row, int l16,
+                                            const float *keys, float error) {
+  double value[kRowGroups];
+#pragma unroll
+  for (int m = 0; m < kRowGroups; ++m) value[m] = KeyOf<double>::none;
+  const int size = a.group_size;
+#pragma unroll 1
+  for (int g = l16; g < a.groups; g += 16) {
+    float first, second;
+    group_top(a, g, l16, keys, first, second);
+    const float from = (a.group_top == 2 ? second : first) - 2.0f * error;
+    double top[2] = {KeyOf<double>::none, KeyOf<double>::none};
+#pragma unroll 1
+    for (int e = g * size; e < g * size + size; ++e) {
+      if (!KeyOf<float>::some(keys[e]) || keys[e] < from) continue;
+      const double v = sigmoid_value<TYPE>(a, row, e);
+      top[1] = v > top[0] ? top[0] : v > top[1] ? v : top[1];
+      top[0] = v > top[0] ? v : top[0];
+    }
+#pragma unroll
+    for (int m = 0; m < kRowGroups; ++m)
+      if (m * 16 + l16 == g) value[m] = group_value(a, top[0], top[1]);
+  }
+  return choose_groups(a, value, l16);
+}
+
+// A row's keys to LDS.
 template <int PER, class KEY>
-__device__ inline unsigned long long best_groups(const RouteArgs &a, const KEY (&key)[PER], int l16, KEY *keys) {
+__device__ inline const KEY *put_keys(const RouteArgs &a, const KEY (&key)[PER], int l16, void *lds) {
+  KEY *keys = static_cast<KEY *>(lds);
   wave_order();
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
@@ -151,52 +258,134 @@ __device__ inline unsigned long long best_groups(const RouteArgs &a, const KEY (
     if (e < a.experts) keys[e] = key[j];
   }
   wave_order();
-  constexpr int kMine = kRouteMaxGroups / 16;
-  KEY value[kMine];
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    const int g = m * 16 + l16;
-    KEY first = KeyOf<KEY>::none, second = KeyOf<KEY>::none;
-    if (g < a.groups) {
-      int at = l16 % a.group_size;
-      for (int i = 0; i < a.group_size; ++i) {
-        const KEY k = keys[g * a.group_size + at];
-        if (++at == a.group_size) at = 0;
-        second = k > first ? first : k > second ? k : second;
-        first = k > first ? k : first;
-      }
-    }
-    // (whole numbers are compared where the largest alone counts)
-    if constexpr (sizeof(KEY) == 8)
-      value[m] = a.group_top == 2 && KeyOf<KEY>::some(second) ? first + second : first;
-    else
-      value[m] = first;
-  }
-  unsigned long long stay = 0;
-  for (int n = 0; n < a.top_groups; ++n) {
-    KEY best = KeyOf<KEY>::none;
-    int at = kRouteMaxGroups;
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-      if (value[m] > best) {
-        best = value[m];
-        at = m * 16 + l16;
-      }
-    }
-    const KEY most = row_max(best);
-    if (!KeyOf<KEY>::some(most)) break;   // (rows differ: the lanes of one leave together)
-    const int g = row_min(best == most ? at : kRouteMaxGroups);
-    stay |= 1ull << g;
-#pragma unroll
-    for (int m = 0; m < kMine; ++m)
-      if (m * 16 + l16 == g) value[m] = KeyOf<KEY>::none;
-  }
-  return stay;
+  return keys;
 }
 
-// Routes the token t of this lane's row.
-template <int TYPE, int PER, class KEY>
-__device__ inline void route_token(const RouteArgs &a, long long t, int *counts, KEY *keys) {
+// The choice: lane n's into `mine`, in descending order. Float keys are known up to `error`:
+// where two that have to be told apart lie within that, `sure` is false, and the row's 16
+// lanes have the 16 best instead, `rest` being the best of the others.
+template <int PER, class KEY>
+__device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l16, float error, bool &sure, KEY &rest) {
+  KEY best;
+  int at;
+  best_of<PER, KEY>(key, l16, best, at);
+  int mine = -1;
+  KEY last = KeyOf<KEY>::none;
+  sure = true;
+  for (int n = 0;; ++n) {
+    const KEY most = row_max(best);
+    if constexpr (KeyOf<KEY>::estimate) {
+      // (not greater: also where both are infinite)
+      if (n > 0 && n <= a.top_k && KeyOf<KEY>::some(most) && !(last - most > 2.0f * error)) sure = false;
+      last = rest = most;
+    }
+    if (n >= a.top_k && (sure || n == 16)) break;   // (rows differ: the lanes of one leave together)
+    const int expert = row_min(best == most ? at : kRouteMaxExperts);
+    if (l16 == n && KeyOf<KEY>::some(most)) mine = expert;
+    if (expert == at && KeyOf<KEY>::some(best)) {   // its lane looks for its next
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (expert_of(j, l16) == expert) key[j] = KeyOf<KEY>::none;
+      best_of<PER, KEY>(key, l16, best, at);
+    }
+  }
+  return mine;
+}
+
+// The choice among 16 candidates, one in each lane (-1: none), on their FP64 values. `sure` is
+// false where an expert that is none of them may be among the best after all.
+template <int TYPE>
+__device__ int settle_experts(const RouteArgs &a, const typename Elem<TYPE>::store *row, int l16, int candidate,
+                              float rest, float error, bool &sure) {
+  const double v = candidate >= 0 ? sigmoid_value<TYPE>(a, row, candidate) : KeyOf<double>::none;
+  const int number = candidate >= 0 ? candidate : kRouteMaxExperts + l16;
+  int ahead = 0;
+  for (int n = 0; n < 16; ++n) {
+    const double w = row_lane(v, n);
+    const int other = row_lane(number, n);
+    ahead += w > v || (w == v && other < number) ? 1 : 0;
+  }
+  // to lane `ahead` of the row (all different)
+  const int mine = __builtin_amdgcn_ds_permute(((threadIdx.x & 48) + ahead) * 4, candidate);
+  const unsigned worst = row_max(ahead == a.top_k - 1 && !(v - static_cast<double>(rest) > 2.0f * error) ? 1u : 0u);
+  sure = !KeyOf<float>::some(rest) || worst == 0;
+  return l16 < a.top_k ? mine : -1;
+}
+
+// Keys of experts whose group does not stay go.
+template <int PER, class KEY>
+__device__ inline void leave_groups(const RouteArgs &a, KEY (&key)[PER], int l16, unsigned long long stay) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const unsigned g = (static_cast<unsigned>(expert_of(j, l16)) * a.group_mul) >> 20;
+    if (!(stay >> (g & 63) & 1)) key[j] = KeyOf<KEY>::none;
+  }
+}
+
+// The FP64 values of all experts into LDS, and the groups that stay by them (all, without
+// groups): where a few candidates do not settle the choice, and for softmax, whose values need
+// the sum of all. Loops that are not unrolled: a launch waits for its slowest wave, and their
+// instructions are quickly there.
+template <int TYPE>
+__device__ unsigned long long all_doubles(const RouteArgs &a, const typename Elem<TYPE>::store *row, float top, int l16,
+                                          double *keys) {
+  const double none = KeyOf<double>::none;
+  double sum = 0.0;
+  wave_order();
+#pragma unroll 1
+  for (int e = l16; e < a.experts; e += 16) {
+    const float l = Elem<TYPE>::get(row[e]);
+    double v = exp(a.score == kSoftmax ? static_cast<double>(l) - static_cast<double>(top) : -static_cast<double>(l));
+    if (a.score == kSoftmax) sum += l == -__builtin_inff() ? 0.0 : v;
+    else v = 1.0 / (1.0 + v);
+    keys[e] = l == -__builtin_inff() ? none : v;
+  }
+  const double scale = a.score == kSoftmax ? row_total(sum) : 1.0;
+#pragma unroll 1
+  for (int e = l16; e < a.experts; e += 16) {
+    double v = keys[e];
+    if (v > none) {
+      if (a.score == kSoftmax) v /= scale;
+      if (a.bias) v += static_cast<double>(a.bias[e]);
+      keys[e] = v;
+    }
+  }
+  wave_order();
+  if (a.groups == a.top_groups) return ~0ull;
+  return best_groups<double>(a, l16, keys);
+}
+
+// The choice by them.
+__device__ inline int choose_by_doubles(const RouteArgs &a, unsigned long long stay, int l16, double *keys) {
+  const double none = KeyOf<double>::none;
+#pragma unroll 1
+  for (int e = l16; e < a.experts; e += 16)
+    if (!(stay >> ((static_cast<unsigned>(e) * a.group_mul >> 20) & 63) & 1)) keys[e] = none;
+  wave_order();
+  int mine = -1;
+#pragma unroll 1
+  for (int n = 0; n < a.top_k; ++n) {
+    double best = none;
+    int at = kRouteMaxExperts;
+#pragma unroll 4
+    for (int e = l16; e < a.experts; e += 16) {
+      const double v = keys[e];
+      at = v > best ? e : at;
+      best = v > best ? v : best;
+    }
+    const double most = row_max(best);
+    const int expert = row_min(best == most ? at : kRouteMaxExperts);
+    if (!(most > none)) break;   // (the row's lanes leave together)
+    if (l16 == n) mine = expert;
+    if ((expert & 15) == l16) keys[expert] = none;
+    wave_order();
+  }
+  return mine;
+}
+
+// VALUES: the order of the logits does not settle the choice.
+template <int TYPE, int PER, bool VALUES>
+__device__ inline void route_token(const RouteArgs &a, long long t, int *counts, double *keys) {
   typedef typename Elem<TYPE>::store store;
   const int l16 = threadIdx.x & 15;
   const store *row = static_cast<const store *>(a.logits) + t * a.ld;
@@ -214,59 +403,77 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
   }
   top = row_max(top);
   bool bad = row_max(largest) >= (a.score == kSoftmax ? 0x7f800000u : 0x7f800001u);
-  KEY key[PER];
-  if constexpr (sizeof(KEY) == 4) {
+  int mine = -1;
+  if constexpr (!VALUES) {
+    unsigned key[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) key[j] = l[j] == -__builtin_inff() ? 0u : logit_key(l[j]);
+    if (a.groups > a.top_groups)
+      leave_groups<PER, unsigned>(a, key, l16, best_groups<unsigned>(a, l16, put_keys<PER>(a, key, l16, keys)));
+    bool sure;
+    unsigned rest;
+    mine = choose_experts<PER, unsigned>(a, key, l16, 0.0f, sure, rest);
   } else {
-    double s[PER], sum = 0.0;
+    // Estimates: e^x by v_exp_f32 is off by |x| 2^-23 (the argument's rounding, times log2 e) + 2^-23
+    // of itself, and |x| e^x < 0.37; a reciprocal, a product, a sum of up to 36 terms by 2^-24
+    // each. So a sigmoid is within 2^-21, a softmax within 2^-18 of the largest, here twice
+    // that; adding the bias rounds once more.
+    float key[PER], bias[PER], sum = 0.0f, most = 0.0f;
+    if (a.bias) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      if (a.score == kSoftmax) {
-        s[j] = exp(static_cast<double>(l[j]) - static_cast<double>(top));
-        sum += s[j];
-      } else {
-        s[j] = 1.0 / (1.0 + exp(-static_cast<double>(l[j])));
-      }
+      for (int j = 0; j < PER; j += 4) load_logits<kF32>(a.bias, expert_of(j, l16), a.experts, &bias[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) bias[j] = 0.0f;
     }
-    const double scale = a.score == kSoftmax ? row_total(sum) : 1.0;
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const int e = expert_of(j, l16);
-      double v = a.score == kSoftmax ? s[j] / scale : s[j];
-      if (a.bias && e < a.experts) {
-        const float b = a.bias[e];
-        nan |= b != b;
-        v += static_cast<double>(b);
+      if (a.score == kSoftmax) {
+        key[j] = __expf(l[j] - top);
+        sum += key[j];
+      } else {
+        key[j] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
       }
-      key[j] = l[j] == -__builtin_inff() ? KeyOf<KEY>::none : v;
     }
-    bad |= row_max(nan ? 1u : 0u) != 0;
-  }
-  if (a.groups > a.top_groups) {
-    const unsigned long long stay = best_groups<PER, KEY>(a, key, l16, keys);
+    float error = 0x1p-20f;
+    if (a.score == kSoftmax) {
+      const float inverse = 1.0f / row_total(sum);
+      error = 0x1p-17f * inverse;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) key[j] *= inverse;
+    }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const unsigned g = (static_cast<unsigned>(expert_of(j, l16)) * a.group_mul) >> 20;
-      if (!(stay >> (g & 63) & 1)) key[j] = KeyOf<KEY>::none;
+      nan |= bias[j] != bias[j];
+      key[j] = l[j] == -__builtin_inff() ? KeyOf<float>::none : key[j] + bias[j];
+      most = fmaxf(most, KeyOf<float>::some(key[j]) ? fabsf(key[j]) : 0.0f);
     }
-  }
-  KEY best;
-  int at;
-  best_of<PER, KEY>(key, l16, best, at);
-  int mine = -1;
-  for (int n = 0; n < a.top_k; ++n) {
-    const KEY most = row_max(best);
-    const int expert = row_min(best == most ? at : kRouteMaxExperts);
-    if (l16 == n && KeyOf<KEY>::some(most) && !bad) mine = expert;
-    if (expert == at && KeyOf<KEY>::some(best)) {   // its lane looks for its next
+    bad |= row_max(nan ? 1u : 0u) != 0;
+    error += 0x1p-23f * row_max(most);
+    if (a.groups > a.top_groups) {
+      float apart;
+      const float *in_lds = put_keys<PER>(a, key, l16, keys);
+      unsigned long long stay = best_groups<float>(a, l16, in_lds, &apart);
+      if (!(apart > 5.0f * error) && !bad)   // of sums of two, and a rounding (a row's lanes go together)
+        stay = a.score == kSigmoid ? settle_groups<TYPE>(a, row, l16, in_lds, error) : all_doubles<TYPE>(a, row, top, l16, keys);
+      leave_groups<PER, float>(a, key, l16, stay);
+    }
+    if (!a.bias) {   // the groups are settled: the logits say the rest
+      unsigned order[PER], rest;
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (expert_of(j, l16) == expert) key[j] = KeyOf<KEY>::none;
-      best_of<PER, KEY>(key, l16, best, at);
+      for (int j = 0; j < PER; ++j) order[j] = KeyOf<float>::some(key[j]) ? logit_key(l[j]) : 0u;
+      bool exact;
+      mine = choose_experts<PER, unsigned>(a, order, l16, 0.0f, exact, rest);
+    } else {
+      float rest;
+      bool sure;
+      mine = choose_experts<PER, float>(a, key, l16, error, sure, rest);
+      if (!sure && !bad && a.score == kSigmoid) mine = settle_experts<TYPE>(a, row, l16, mine, rest, error, sure);
+      if (!sure && !bad) mine = choose_by_doubles(a, all_doubles<TYPE>(a, row, top, l16, keys), l16, keys);
     }
   }
+  if (bad) mine = -1;
   // Weights: lane n has the n-th choice. Renormalised ones are ratios to the largest
   // chosen score, which neither underflow together nor divide zero by zero:
   // sigmoid(l) = e^min(l, 0) / (1 + e^-|l|).
@@ -300,7 +507,7 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
 // Tokens over the rows of the grid's workgroups, each row taking every so many. Counts
 // are summed in LDS; a workgroup that is the only one writes them whole, several add theirs
 // (whole numbers: the order of the additions does not show).
-template <int TYPE, int PER, class KEY, int THREADS>
+template <int TYPE, int PER, bool VALUES, int THREADS>
 __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
   __shared__ int counts[kRouteMaxExperts];
   extern __shared__ __attribute__((aligned(16))) unsigned char dynamic[];   // a key for each row's experts, with groups
@@ -309,10 +516,10 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
     __syncthreads();
   }
   const int row = threadIdx.x >> 4;
-  KEY *keys = reinterpret_cast<KEY *>(dynamic) + row * a.experts;
+  double *keys = reinterpret_cast<double *>(dynamic + row * a.row_bytes);
   const long long rows = static_cast<long long>(gridDim.x) * (THREADS / 16);
   for (long long t = static_cast<long long>(blockIdx.x) * (THREADS / 16) + row; t < a.tokens; t += rows)
-    route_token<TYPE, PER, KEY>(a, t, a.counts ? counts : nullptr, keys);
+    route_token<TYPE, PER, VALUES>(a, t, a.counts ? counts : nullptr, keys);
   if (a.counts) {
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += THREADS) {

@@ -419,8 +419,8 @@ int gemm_mx_moe_routed(int tokens, int hidden, int inter, int experts, int top_k
  *       are worth most stay;
  *   S = the top_k experts of largest v that are left, all ties to the lowest index;
  *   w_e = scale * s_e, or scale * s_e / sum_S s when renormalize.
- * Where neither a bias nor sums of scores come in, the choice compares the logits
- * themselves (s rises with l); else v is computed and compared in 64 bits. Weights
+ * Without a bias the logits themselves are compared (s rises with l), and sums of two scores
+ * in 64 bits; with one v, in 64 bits. Weights
  * are FP32; renormalised ones are taken as ratios, so they are right also where every
  * score underflows.
  * An expert whose logit or bias is -inf is never chosen. A token with a NaN among its

@@ -43,7 +43,8 @@ def route(l, bias, r):
     T, E = l.shape
     chosen, weights = np.full((T, r.top_k), -1, np.int32), np.zeros((T, r.top_k))
     size = E // r.groups
-    by_value = bias is not None or (r.top_groups < r.groups and r.group_top == 2 and size > 1)
+    # without a bias the order is the logits'; sums of scores alone need the scores
+    sums = r.top_groups < r.groups and r.group_top == 2 and size > 1
     for t in range(T):
         if np.isnan(l[t]).any() or (r.score == SOFTMAX and (l[t] == np.inf).any()) or (bias is not None and np.isnan(bias).any()):
             weights[t] = np.nan
@@ -53,13 +54,12 @@ def route(l, bias, r):
             left &= bias > -np.inf
         if not left.any():
             continue
-        v = scores(l[t], r.score) if by_value else l[t].copy()
-        if bias is not None:
-            v = v + bias
+        v = l[t].copy() if bias is None else scores(l[t], r.score) + bias
         if r.top_groups < r.groups:
+            u = scores(l[t], r.score) if sums and bias is None else v
             worth = np.full(r.groups, -np.inf)
             for g in range(r.groups):
-                mine = np.sort(v[g * size:(g + 1) * size][left[g * size:(g + 1) * size]])[::-1][:r.group_top]
+                mine = np.sort(u[g * size:(g + 1) * size][left[g * size:(g + 1) * size]])[::-1][:r.group_top]
                 if len(mine):
                     worth[g] = mine.sum()
             best = [g for g in np.argsort(-worth, kind="stable")[:r.top_groups] if worth[g] > -np.inf]

@@ -176,6 +176,33 @@ def test_values_next_to_each_other():
     check_route(l, "f32", b, ref.Router(E, 2, ref.SOFTMAX), "a large bias")
 
 
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+def test_logits_next_to_each_other(score):
+    """Logits that differ by less than FP64 scores tell are told apart where there is no bias; groups
+    whose two best scores are the same tie, to the lowest."""
+    E = 24
+    l = np.full((3, E), -2.0, np.float32)
+    l[0, [5, 11]] = [1e-30, 2e-30]                # groups of 6: two in the first two
+    l[0, [12, 18]] = 2e-30
+    l[1, [3, 9, 15, 21]] = [40.0, 41.0, 42.0, 40.5]
+    l[2] = 0.0
+    for g, tg, gt in ((1, 1, 1), (4, 2, 1), (4, 2, 2), (4, 3, 2)):
+        check_route(l, "f32", None, ref.Router(E, 4, score, g, tg, gt, True), f"logits next to each other {score} groups {g} {tg} {gt}")
+
+
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+def test_near_ties_everywhere(score):
+    """Values a few FP32 steps apart in every token: estimates settle nothing, by groups or by experts, with
+    more near each other than there are candidates."""
+    rng = np.random.default_rng(12)
+    T, E = 40, 96
+    l = (1.0 + rng.integers(0, 9, (T, E)) * 2.0 ** -22).astype(np.float32)
+    b = (rng.integers(-3, 4, E) * 2.0 ** -23).astype(np.float32)
+    for g, tg, gt in ((1, 1, 1), (8, 3, 1), (8, 3, 2), (48, 20, 2)):
+        for k in (1, 6, 16):
+            check_route(l, "f32", b, ref.Router(E, k, score, g, tg, gt, True), f"near ties {score} groups {g} {tg} {gt} top {k}")
+
+
 def test_no_tokens_zero_the_counts():
     n = ints(16)
     lib.gemm_route(0, lib.gemm_route_t(16, 2), None, 0, 16, None, None, None, n, stream())
