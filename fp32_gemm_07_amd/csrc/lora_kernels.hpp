@@ -701,9 +701,12 @@ __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (blockIdx.x > 0) {
     const int tiles = a.a_tiles + a.b_tiles, id = (blockIdx.x - 1) / tiles, rank = a.r.rank;
-    bool used = false;
-    for (int row = threadIdx.x; row < a.r.rows; row += 1024) used |= a.r.ids[row] == id;
-    if (!__syncthreads_or(used)) return;
+    bool used = false;   // 8192 ids on their way at a time
+    for (int row0 = 0; !__syncthreads_or(used); row0 += 8 * 1024) {
+      if (row0 >= a.r.rows) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) used |= a.r.load_id(row0 + i * 1024 + threadIdx.x) == id;
+    }
     store *tile = reinterpret_cast<store *>(lds);   // [rank][64], a row of 65
     const int at = (blockIdx.x - 1) % tiles;
     const bool second = at >= a.a_tiles;
