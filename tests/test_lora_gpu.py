@@ -339,3 +339,27 @@ def test_gradient_against_differences():
             array[at] += 1
             assert loss() - base == grad[at], at
             array[at] -= 1
+
+
+@pytest.mark.parametrize("kind,small,back", [("f16", -24, 14), ("bf16", -120, 110), ("f32", -120, 110)])
+def test_small_values(kind, small, back):
+    """Whole numbers times the smallest half (subnormal there), or near the smallest normal float: sums stay
+    exact, and the scale brings them back."""
+    rng = np.random.default_rng(10)
+    c = Case(rng, 40, 70, 90, 10, 3, kind, True, whole=True)
+    c.x, c.scales = c.x * np.float32(2.0 ** small), c.scales * np.float32(2.0 ** back)
+    check_forward(c, f"small values {kind}", base="none", exact=True)
+    c.dc[:] = 0
+    c.dy, c.x = c.dy * np.float32(2.0 ** small), c.x * np.float32(2.0 ** -small)
+    check_backward(c, f"small gradients {kind}", base="none", exact=True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [63, 64, 65, 128, 129, 4096, 4159])
+def test_row_counts_around_the_kernels_borders(rows, kind):
+    """Windows of 64 rows, the layouts for few and many rows, units of two tiles with an odd one."""
+    rng = np.random.default_rng(rows)
+    for mixed in (False, True):
+        c = Case(rng, rows, 130, 70, 18, 4, kind, mixed, whole=True, pad=2)
+        check_forward(c, f"rows {rows} {kind} mixed {mixed}", base="place", exact=True)
+        check_backward(c, f"rows {rows} {kind} mixed {mixed}", base="place", exact=True)
