@@ -62,6 +62,13 @@ Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, i
   return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, floats, parts};
 }
 
+// Whether one kernel makes both products: where the adapters' A, read again for every 128 columns
+// of Y, come to 16 MB at most if every row has another.
+bool one_kernel(int rows, const gemm_lora_t &s) {
+  const double again = static_cast<double>(ceil_div(s.N, kSmallCols)) * rows * s.rank * s.K * elem_size(s.type);
+  return rows <= 64 && s.rank <= 32 && again <= 16 << 20;
+}
+
 // Bytes of what shrink leaves for expand.
 size_t hidden_bytes(int rows, const gemm_lora_t &s, const ShrinkPlan &plan) {
   const size_t each = s.type != GEMM_TYPE_F32 && !plan.few ? 6 : 4 * static_cast<size_t>(plan.splits);
@@ -137,6 +144,7 @@ extern "C" {
 
 size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set) {
   if (check_set(rows, set) != GEMM_OK || rows == 0) return 0;
+  if (one_kernel(rows, *set)) return 0;
   return hidden_bytes(rows, *set, shrink_plan(rows, *set, gemm::host_planning_cus()));
 }
 
@@ -160,7 +168,8 @@ int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, i
   if (st != GEMM_OK) return st;
   const int cus = gemm::host_planning_cus();
   const ShrinkPlan plan = shrink_plan(rows, s, cus);
-  const size_t need = hidden_bytes(rows, s, plan);
+  const bool one = one_kernel(rows, s);
+  const size_t need = one ? 0 : hidden_bytes(rows, s, plan);
   st = check_workspace(workspace, workspace_bytes, need,
                        {x, c, y, id, range_a(s), range_b(s), range_ranks(s), range_scales(s)});
   if (st != GEMM_OK) return st;
@@ -168,6 +177,10 @@ int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, i
   st = gemm::host_check_device(&dev, &dev_cus);
   if (st != GEMM_OK) return st;
   const LoraLaunches &launches = lora_launches(s.type);
+  if (one)
+    return launches.small(SmallArgs{rows_of(rows, s, ids), X, ldx, s.A, s.B, C, ldc, Y, ldy, s.N, s.K, std::min(rows, 64),
+                                    in_place},
+                          stream);
   return with_workspace(workspace, need, dev, stream, [&](void *ws) {
     const LoraRows r = rows_of(rows, s, ids);
     ShrinkArgs sa{};

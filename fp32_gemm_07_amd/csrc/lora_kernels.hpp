@@ -354,6 +354,131 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
   }
 }
 
+// 16 J rows of an adapter's N x rank matrix from row n0 on, as operands: row m of operand j is row
+// n0 + 16 j + m.
+template <int TYPE, int J, int KS, int PB>
+__device__ __attribute__((always_inline)) inline void load_b(const typename Elem<TYPE>::store *w, long long ldw, int n0, int N, int stored,
+                                                                 uintx4 (&b)[J][KS][PB]) {
+  constexpr int kLane = kLaneK<TYPE>;
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int n = min(n0 + 16 * j + i16, N - 1);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int r = s * 4 * kLane + g * kLane;
+      b[j][s][0] = load_k<TYPE>(w + n * ldw + r, stored - r);
+    }
+  }
+}
+
+// What is stored behind the adapter's own rank goes (apart from the loads: none waits for the
+// rank); halfs in two parts (PB).
+template <int TYPE, int J, int KS, int PB>
+__device__ __attribute__((always_inline)) inline void finish_b(int stored, int rank, uintx4 (&b)[J][KS][PB]) {
+  constexpr int kLane = kLaneK<TYPE>;
+  const int g = (threadIdx.x & 63) >> 4;
+  if (rank < stored) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int real = rank - (s * 4 * kLane + g * kLane);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (TYPE == kF32) b[j][s][0][i] = i < real ? b[j][s][0][i] : 0;
+          else b[j][s][0][i] = 2 * i + 1 < real ? b[j][s][0][i] : 2 * i < real ? b[j][s][0][i] & 0xffff : 0;
+        }
+    }
+  }
+  if constexpr (PB == 2) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        bf16x8 parts[2];
+        split_halfs(b[j][s][0], parts);
+        b[j][s][0] = __builtin_bit_cast(uintx4, parts[0]);
+        b[j][s][1] = __builtin_bit_cast(uintx4, parts[1]);
+      }
+  }
+}
+
+// The lane's columns of H of one row as operands, from floats: bfloat16 parts, or as they are.
+template <int TYPE, int PH>
+__device__ __attribute__((always_inline)) inline void hidden_operand(const f32x4 (&v)[kLaneK<TYPE> / 4], uintx4 (&h)[PH]) {
+  if constexpr (TYPE == kF32) {
+    h[0] = __builtin_bit_cast(uintx4, v[0]);
+  } else {
+    float y[8];
+    floats8(v[0], v[1], y);
+    bf16x8 parts[3];
+    split8<3>(y, parts);
+#pragma unroll
+    for (int q = 0; q < PH; ++q) h[q] = __builtin_bit_cast(uintx4, parts[q]);
+  }
+}
+
+// sum = B H^T of such operands. Small products come first (the third part of H times the second
+// of B is below 2^-24). The other parts of an infinity, or products of zeros with one, are NaN:
+// where the first parts' sum is not finite it stands alone.
+template <int TYPE, int J, int KS, int PB, int PH>
+__device__ __attribute__((always_inline)) inline void multiply_parts(const uintx4 (&b)[J][KS][PB], const uintx4 (&h)[KS][PH], f32x4 (&sum)[J]) {
+  if constexpr (TYPE == kF32) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      sum[j] = f32x4{};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) sum[j] = multiply<kF32>(b[j][s][0], h[s][0], sum[j]);
+    }
+  } else {
+    auto first = [&](int j, f32x4 acc) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) acc = multiply<kBf16>(b[j][s][0], h[s][0], acc);
+      return acc;
+    };
+    float check = 0.0f;   // NaN with anything that is not finite
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      sum[j] = f32x4{};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int q = PH - 1; q > 0; --q) sum[j] = multiply<kBf16>(b[j][s][0], h[s][q], sum[j]);
+        if constexpr (PB == 2) {
+          sum[j] = multiply<kBf16>(b[j][s][1], h[s][1], sum[j]);
+          sum[j] = multiply<kBf16>(b[j][s][1], h[s][0], sum[j]);
+        }
+      }
+      sum[j] = first(j, sum[j]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) check = fmaf(sum[j][v], 0.0f, check);
+    }
+    if (__any(check != check)) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const f32x4 alone = first(j, f32x4{});
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[j][v] = __builtin_isfinite(alone[v]) ? sum[j][v] : alone[v];
+      }
+    }
+  }
+}
+
+// 4 neighbouring values of a row, the first `left` of them.
+template <int TYPE>
+__device__ inline void store4(typename Elem<TYPE>::store *p, int left, const float *v) {
+  typedef typename Elem<TYPE>::store store;
+  typedef store vec4 __attribute__((ext_vector_type(4), aligned(sizeof(store))));
+  if (left >= 4) {
+    *reinterpret_cast<vec4 *>(p) = vec4{Elem<TYPE>::put(v[0]), Elem<TYPE>::put(v[1]), Elem<TYPE>::put(v[2]), Elem<TYPE>::put(v[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = Elem<TYPE>::put(v[i]);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // expand.
 struct ExpandArgs {
@@ -408,41 +533,8 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   const long long ld_c_or_y = a.c ? a.ldc : a.ldy;
   auto load_adapter = [&](int id) __attribute__((always_inline)) {
     const int rank = a.r.rank_of(id);
-    const store *w = static_cast<const store *>(a.w) + id * a.w_adapter;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int n = min(nb + 16 * j + i16, a.N - 1);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int r = s * 4 * kLane + g * kLane;
-        b[j][s][0] = load_k<TYPE>(w + n * a.ldw + r, a.r.rank - r);
-      }
-    }
-    // What is stored behind the adapter's own rank goes (after the loads: none waits for the rank).
-    if (rank < a.r.rank) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int real = rank - (s * 4 * kLane + g * kLane);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (TYPE == kF32) b[j][s][0][i] = i < real ? b[j][s][0][i] : 0;
-            else b[j][s][0][i] = 2 * i + 1 < real ? b[j][s][0][i] : 2 * i < real ? b[j][s][0][i] & 0xffff : 0;
-          }
-      }
-    }
-    if constexpr (PB == 2) {
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          bf16x8 parts[2];
-          split_halfs(b[j][s][0], parts);
-          b[j][s][0] = __builtin_bit_cast(uintx4, parts[0]);
-          b[j][s][1] = __builtin_bit_cast(uintx4, parts[1]);
-        }
-    }
+    load_b<TYPE>(static_cast<const store *>(a.w) + id * a.w_adapter, a.ldw, nb, a.N, a.r.rank, b);
+    finish_b<TYPE>(a.r.rank, rank, b);
     // (here, or every use of them would wait for all loads)
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -522,16 +614,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
                 for (int i = 0; i < kLane / 4; ++i) v[i] += q + m < a.splits ? x[m][i] : f32x4{};
             }
           }
-          if constexpr (TYPE == kF32) {
-            f.h[s][0] = __builtin_bit_cast(uintx4, v[0]);
-          } else {
-            float y[8];
-            floats8(v[0], v[1], y);
-            bf16x8 parts[3];
-            split8<3>(y, parts);
-#pragma unroll
-            for (int q = 0; q < PH; ++q) f.h[s][q] = __builtin_bit_cast(uintx4, parts[q]);
-          }
+          hidden_operand<TYPE>(v, f.h[s]);
         }
       }
     };
@@ -545,46 +628,8 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
         for (int q = 0; q < PH; ++q)
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[s][q][i] = TYPE != kF32 && upper ? 0u : f.h[s][q][i];
-      f32x4 sum[J] = {};
-      if constexpr (TYPE == kF32) {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int s = 0; s < KS; ++s) sum[j] = multiply<kF32>(b[j][s][0], h[s][0], sum[j]);
-      } else {
-        auto first = [&](int j, f32x4 acc) __attribute__((always_inline)) {
-#pragma unroll
-          for (int s = 0; s < KS; ++s) acc = multiply<kBf16>(b[j][s][0], h[s][0], acc);
-          return acc;
-        };
-        float check = 0.0f;   // NaN with anything that is not finite
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          // small products first (the third part of H times the second of B is below 2^-24)
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-#pragma unroll
-            for (int q = PH - 1; q > 0; --q) sum[j] = multiply<kBf16>(b[j][s][0], h[s][q], sum[j]);
-            if constexpr (PB == 2) {
-              sum[j] = multiply<kBf16>(b[j][s][1], h[s][1], sum[j]);
-              sum[j] = multiply<kBf16>(b[j][s][1], h[s][0], sum[j]);
-            }
-          }
-          sum[j] = first(j, sum[j]);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) check = fmaf(sum[j][v], 0.0f, check);
-        }
-        if (__any(check != check)) {
-          // The other parts of an infinity, or products of zeros with one, are NaN: where the first
-          // parts' sum is not finite it stands alone.
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const f32x4 alone = first(j, f32x4{});
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sum[j][v] = __builtin_isfinite(alone[v]) ? sum[j][v] : alone[v];
-          }
-        }
-      }
+      f32x4 sum[J];
+      multiply_parts<TYPE>(b, h, sum);
       wave_order();
 #pragma unroll
       for (int j = 0; j < J; ++j) *reinterpret_cast<f32x4 *>(stage + i16 * kStride + 16 * j + 4 * g) = sum[j];
@@ -622,15 +667,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
         if constexpr (VEC == 8) {
           store8<TYPE>(y, WHOLE ? 8 : left, out);
         } else {
-          typedef store store4 __attribute__((ext_vector_type(4), aligned(sizeof(store))));
-          if (WHOLE || left >= 4) {
-            *reinterpret_cast<store4 *>(y) =
-                store4{Elem<TYPE>::put(out[0]), Elem<TYPE>::put(out[1]), Elem<TYPE>::put(out[2]), Elem<TYPE>::put(out[3])};
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < left) y[i] = Elem<TYPE>::put(out[i]);
-          }
+          store4<TYPE>(y, WHOLE ? 4 : left, out);
         }
       }
     };
@@ -666,6 +703,156 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
     }
   };
   if (nb + COLS <= a.N) run(std::true_type());
+  else run(std::false_type());
+}
+
+// ---------------------------------------------------------------------------
+// Both products in one kernel, for a few rows on adapters of a rank up to 32.
+struct SmallArgs {
+  LoraRows r;          // up to 64 rows
+  const void *x;
+  long long ldx;
+  const void *a, *b;   // as in gemm.h
+  const void *c;       // null: zeros
+  long long ldc;
+  void *y;
+  long long ldy;
+  int N, K, units_by;
+  bool in_place;
+};
+constexpr int kSmallWaves = 8, kSmallCols = 16 * kSmallWaves;
+
+// One workgroup: 128 columns of Y, every units_by-th unit. Its waves share K for H, each workgroup
+// for itself: A is read once for each 128 columns, from L2. Then each wave makes 16 columns. What
+// bounds it is the chain of waits, so whatever a unit needs is loaded at once: B, C, the first
+// operands of H.
+template <int TYPE, int RT>
+__global__ __launch_bounds__(64 * kSmallWaves) void small_kernel(SmallArgs a) {
+  typedef typename Elem<TYPE>::store store;
+  typedef store vec4 __attribute__((ext_vector_type(4), aligned(sizeof(store))));
+  constexpr int W = kSmallWaves, kLane = kLaneK<TYPE>, kChunk = 4 * kLane, U = RT == 1 ? 8 : 4;
+  constexpr int KS = TYPE == kF32 ? RT : (RT + 1) / 2, PB = TYPE == kF16 ? 2 : 1, PH = TYPE == kF32 ? 1 : 3;
+  constexpr int kStride = 20;   // floats of a row in LDS
+  __shared__ __attribute__((aligned(16))) f32x4 sums[W * RT * 64];
+  __shared__ __attribute__((aligned(16))) float stages[W][16 * kStride];
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col_blocks = (a.N + kSmallCols - 1) / kSmallCols;
+  const int group = blockIdx.x / col_blocks;
+  const int nb = (blockIdx.x - group * col_blocks) * kSmallCols + wave * 16;   // (may lie past the last column)
+  const int k_wave = ((a.K + W - 1) / W + 63) / 64 * 64;
+  const int ka = min(a.K, wave * k_wave), kb = min(a.K, ka + k_wave);
+  float *stage = stages[wave];
+  // A lane moves 4 columns of one row of C and Y. (Without a C, Y is read and not used.)
+  const int col = nb + lane % 4 * 4, left = a.N - col;
+  const store *c_or_y = static_cast<const store *>(a.c ? a.c : a.y) + min(col, a.N - 1);
+  const long long ld_c_or_y = a.c ? a.ldc : a.ldy;
+
+  Units<1> unit(a.r, !a.in_place, 0, 1);
+  auto run = [&](auto whole) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    for (int n = 0; unit.next(); ++n) {
+      if (n % a.units_by != group) continue;
+      const int id = max(unit.id, 0);   // (without an adapter: one's loads, not used)
+      const int marked = __shfl(unit.real[0] ? unit.row[0] : ~unit.row[0], lane / 4), row = max(marked, ~marked);
+      const long long adapter = static_cast<long long>(id) * a.r.rank;
+      uintx4 b[1][KS][PB];
+      load_b<TYPE>(static_cast<const store *>(a.b) + adapter * a.N, a.r.rank, min(nb, a.N - 1), a.N, a.r.rank, b);
+      const store *from_c = c_or_y + row * ld_c_or_y;
+      vec4 c = {};
+      if constexpr (WHOLE) {
+        c = *reinterpret_cast<const vec4 *>(from_c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = from_c[max(0, min(i, left - 1))];
+      }
+      const int rank = a.r.rank_of(id);
+      const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
+      const store *w = static_cast<const store *>(a.a) + adapter * a.K + g * kLane;
+      const store *z = static_cast<const store *>(a.x) + unit.row[0] * a.ldx + g * kLane;
+      const store *wr[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) wr[t] = w + static_cast<long long>(min(t * 16 + i16, a.r.rank - 1)) * a.K;
+      f32x4 acc[RT] = {};
+      struct Fetched {
+        uintx4 w[U][RT], z[U];
+      };
+      int k = ka;
+      const int batches = (kb - ka) / (U * kChunk);
+      if (batches > 0) {
+        Fetched even, odd;
+        two_deep(
+            batches, even, odd,
+            [&](Fetched &f) __attribute__((always_inline)) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                f.z[u] = load_k<TYPE>(z + k + u * kChunk);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) f.w[u][t] = load_k<TYPE>(wr[t] + k + u * kChunk);
+              }
+              k += U * kChunk;
+            },
+            [&](const Fetched &f) __attribute__((always_inline)) {
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[t] = multiply<TYPE>(f.w[u][t], f.z[u], acc[t]);
+            });
+      }
+      // (the rest two chunks at a time)
+      for (; k < kb; k += 2 * kChunk) {
+        const int rest = kb - k - g * kLane;
+        uintx4 zv[2], wv[2][RT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          zv[u] = load_k<TYPE>(z + k + u * kChunk, rest - u * kChunk);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) wv[u][t] = load_k<TYPE>(wr[t] + k + u * kChunk, rest - u * kChunk);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[t] = multiply<TYPE>(wv[u][t], zv[u], acc[t]);
+      }
+      __syncthreads();   // (the unit before has been read)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) sums[(wave * RT + t) * 64 + lane] = acc[t];
+      __syncthreads();
+      // The lane's columns of H of row i16, scaled, zeros past the rank: value v of lane (g, i16) of tile t
+      // is column 16 t + 4 g + v.
+      finish_b<TYPE>(a.r.rank, rank, b);
+      uintx4 h[KS][PH];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        f32x4 v[kLane / 4];
+#pragma unroll
+        for (int i = 0; i < kLane / 4; ++i) {
+          const int r = s * 4 * kLane + g * kLane + 4 * i;
+          const f32x4 *from = sums + r % (16 * RT) / 16 * 64 + r % 16 / 4 * 16 + i16;
+          v[i] = from[0];
+#pragma unroll
+          for (int q = 1; q < W; ++q) v[i] += from[q * RT * 64];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) v[i][m] = r + m < rank ? v[i][m] * scale : 0.0f;
+        }
+        hidden_operand<TYPE>(v, h[s]);
+      }
+      f32x4 sum[1];
+      multiply_parts<TYPE>(b, h, sum);
+      wave_order();
+      *reinterpret_cast<f32x4 *>(stage + i16 * kStride + 4 * g) = sum[0];
+      wave_order();
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(stage + lane / 4 * kStride + lane % 4 * 4);
+      float out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        out[i] = a.c ? Elem<TYPE>::get(c[i]) : 0.0f;
+        out[i] = unit.id >= 0 ? out[i] + v[i] : out[i];
+      }
+      if (marked >= 0) store4<TYPE>(static_cast<store *>(a.y) + row * a.ldy + col, left, out);
+    }
+  };
+  if (nb + 16 <= a.N) run(std::true_type());
   else run(std::false_type());
 }
 

@@ -20,6 +20,7 @@ struct LoraLaunches {
   int (*shrink)(ShrinkArgs a, int problems, const ShrinkPlan &plan, hipStream_t stream);
   // Fills in windows and units_by.
   int (*expand)(const ExpandArgs &a, bool few, int cus, hipStream_t stream);
+  int (*small)(const SmallArgs &a, hipStream_t stream);
   int (*prepare)(const PrepareArgs &a, int blocks, hipStream_t stream);
   int (*grads)(GradArgs a, int most_slots, hipStream_t stream);
   int (*sum)(const GradSumArgs &a, int blocks, hipStream_t stream);

@@ -60,6 +60,14 @@ int launch_expand(const ExpandArgs &a, bool few, int cus, hipStream_t stream) {
 }
 
 template <int TYPE>
+int launch_small(const SmallArgs &a, hipStream_t stream) {
+  const dim3 blocks(static_cast<unsigned>(host::ceil_div(a.N, kSmallCols) * a.units_by));
+  if (a.r.rank <= 16) hipLaunchKernelGGL((small_kernel<TYPE, 1>), blocks, dim3(64 * kSmallWaves), 0, stream, a);
+  else hipLaunchKernelGGL((small_kernel<TYPE, 2>), blocks, dim3(64 * kSmallWaves), 0, stream, a);
+  return host::launched();
+}
+
+template <int TYPE>
 int launch_prepare(const PrepareArgs &a, int blocks, hipStream_t stream) {
   hipLaunchKernelGGL(prepare_kernel<TYPE>, dim3(static_cast<unsigned>(blocks)), dim3(1024), 0, stream, a);
   return host::launched();
@@ -87,7 +95,7 @@ int launch_sum(const GradSumArgs &a, int blocks, hipStream_t stream) {
 
 template <int TYPE>
 const LoraLaunches &launches_of() {
-  static const LoraLaunches l{launch_shrink<TYPE>, launch_expand<TYPE>, launch_prepare<TYPE>, launch_grads<TYPE>,
+  static const LoraLaunches l{launch_shrink<TYPE>, launch_expand<TYPE>, launch_small<TYPE>, launch_prepare<TYPE>, launch_grads<TYPE>,
                               launch_sum<TYPE>};
   return l;
 }

@@ -499,8 +499,9 @@ typedef struct gemm_lora {
 
 /* X rows x K, C and Y rows x N, with row strides. C null: zeros. C may be Y with the same
  * stride (rows without an adapter are then left as they are); otherwise Y overlaps
- * nothing else. workspace: as gemm_mx, gemm_lora_workspace_bytes(...) bytes;
- * GEMM_ERR_WORKSPACE also where the library can get none. */
+ * nothing else. workspace: as gemm_mx, gemm_lora_workspace_bytes(...) bytes
+ * (0 for a few rows on small adapters); GEMM_ERR_WORKSPACE also where the library can
+ * get none. */
 int gemm_lora(int rows, const gemm_lora_t *set, const int *ids, const void *X, int ldx,
               const void *C, int ldc, void *Y, int ldy, void *workspace, size_t workspace_bytes,
               hipStream_t stream);

@@ -53,12 +53,14 @@ def test_forward_refusals():
     for p in (X, A, B, RANKS, SCALES, IDS, X - last, A + 4 * (3 * 4 * 16 - 1), B + 4 * (3 * 4 * 24 - 1)):
         assert forward(y=p) == lib.GEMM_ERR_ALIAS, hex(p)
     assert forward(y=C + 4) == forward(y=C, ldy=25) == forward(y=C - last) == lib.GEMM_ERR_ALIAS
-    need = lib.gemm_lora_workspace_bytes(8, adapters())
-    assert need >= 8 * 4 * 4
-    assert forward(wb=need - 1) == lib.GEMM_ERR_WORKSPACE
-    assert forward(ws=WS + 8) == lib.GEMM_ERR_ALIGNMENT
+    assert lib.gemm_lora_workspace_bytes(8, adapters()) == 0   # one kernel
+    wide = {"rows": 65, "ldx": 16}
+    need = lib.gemm_lora_workspace_bytes(65, adapters())
+    assert need >= 65 * 4 * 4
+    assert forward(wb=need - 1, **wide) == lib.GEMM_ERR_WORKSPACE
+    assert forward(ws=WS + 8, **wide) == lib.GEMM_ERR_ALIGNMENT
     for p in (X, C, Y, IDS, A, B, RANKS, SCALES):
-        assert forward(ws=p, wb=need) == lib.GEMM_ERR_ALIAS
+        assert forward(ws=p, wb=need, **wide) == lib.GEMM_ERR_ALIAS
     assert forward(rows=0, ids=None, x=None, c=None, y=None, a=None, b=None, ws=None, wb=0) == lib.GEMM_OK
 
 

@@ -186,13 +186,13 @@ def test_graph_replays_match_eager(what):
 
 def test_library_workspace_is_refused_while_capturing():
     t = torch()
-    c = Case(np.random.default_rng(1), 20, 64, 64, 8, 2, "f32", True)
+    c = Case(np.random.default_rng(1), 70, 64, 64, 8, 2, "f32", True)   # (a few rows need no workspace)
     s_ = c.set()
-    x, y = dev(c.x), t.empty(20, 64, device="cuda:0")
+    x, y = dev(c.x), t.empty(70, 64, device="cuda:0")
     da, db = t.empty(c.a.size, device="cuda:0"), t.empty(c.b.size, device="cuda:0")
     t.cuda.synchronize()
-    for call in (lambda s: lib.gemm_lora(20, s_, c.di, x, 64, None, 64, y, 64, None, 0, s),
-                 lambda s: lib.gemm_lora_backward(20, s_, c.di, x, 64, x, 64, None, 64, y, 64, da, db, None, 0, s)):
+    for call in (lambda s: lib.gemm_lora(70, s_, c.di, x, 64, None, 64, y, 64, None, 0, s),
+                 lambda s: lib.gemm_lora_backward(70, s_, c.di, x, 64, x, 64, None, 64, y, 64, da, db, None, 0, s)):
         with pytest.raises(lib.GemmError) as e:
             graph = t.cuda.CUDAGraph()
             with t.cuda.graph(graph):
