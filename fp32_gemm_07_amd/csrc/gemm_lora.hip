@@ -62,11 +62,14 @@ Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, i
   return Shrink{z, ldz, w, static_cast<long long>(rank) * K, K, K, k_split, splits, h, floats, parts};
 }
 
-// Whether one kernel makes both products: where the adapters' A, read again for every 128 columns
-// of Y, come to 16 MB at most if every row has another.
+// Whether one kernel makes both products: where its waves' shares of K are short, and the adapters'
+// A, read again for every 128 columns of Y, come to 16 MB at most if every row has another.
+// In graphs, bfloat16, rank 16: 1 row of 4096 x 4096 takes 8.2 us so and 7.8 by two kernels
+// (8.8 and 11.9 launched one by one), of 8192 x 8192 12.4 and 8.1, of 1024 x 1024 5.0 and 7.3;
+// 8 rows of 2048 x 2048 7.4 and 8.9, 16 of 4096 x 1024 14.2 and 13.4.
 bool one_kernel(int rows, const gemm_lora_t &s) {
   const double again = static_cast<double>(ceil_div(s.N, kSmallCols)) * rows * s.rank * s.K * elem_size(s.type);
-  return rows <= 64 && s.rank <= 32 && again <= 16 << 20;
+  return rows <= 64 && s.rank <= 32 && s.K * rank_tiles(s.rank) <= 4096 && again <= 16 << 20;
 }
 
 // Bytes of what shrink leaves for expand.

@@ -140,8 +140,8 @@ struct Units {
   int window, end;
   int my_id;                 // of this lane's row in the window (-2: past the last row)
   int next_id;               // of its row in the next one, as loaded: on its way meanwhile
-  unsigned long long todo = 0, same = 0;
-  int base = 0;
+  unsigned long long todo = 0, same = 0, mask;
+  int base = 0, first;
   // The current unit.
   int id;
   int row[MT];               // of column i16; rows - 1 past the unit's last
@@ -151,7 +151,9 @@ struct Units {
       : r(rows), with_none(none), window(first - 1), end(last) {
     next_id = r.load_id(first * 64 + (threadIdx.x & 63));
   }
-  __device__ inline bool next() {
+  // The next unit, without its rows: a window of many units is stepped through by workgroups that
+  // want few of them (64 rows on 64 adapters of 1024 x 1024, rank 8: 29 us with the rows of each).
+  __device__ inline bool step() {
     if (!same) {
       while (!todo) {
         if (++window >= end) return false;
@@ -165,31 +167,34 @@ struct Units {
       todo &= ~same;
       base = 0;
     }
+    mask = same;
+    first = base;
+    base += 16 * MT;
+    if (base >= __popcll(same)) same = 0;
+    return true;
+  }
+  // Its rows.
+  __device__ inline void rows() {
     const int lane = threadIdx.x & 63, i16 = lane & 15;
-    if (same == ~0ull) {   // the whole window: row by row
+    if (mask == ~0ull) {   // the whole window: row by row
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         real[m] = true;
-        row[m] = window * 64 + base + m * 16 + i16;
+        row[m] = window * 64 + first + m * 16 + i16;
       }
-      base += 16 * MT;
-      if (base == 64) same = 0;
-      return true;
+      return;
     }
     // Lane l's row of the window goes to the lane of its number among the unit's.
-    const int count = __popcll(same);
-    const int number = __popcll(same & ((1ull << lane) - 1)) - base;
-    const bool mine = (same >> lane & 1) && number >= 0 && number < 64;
+    const int count = __popcll(mask);
+    const int number = __popcll(mask & ((1ull << lane) - 1)) - first;
+    const bool mine = (mask >> lane & 1) && number >= 0 && number < 64;
     const int from = __builtin_amdgcn_ds_permute((mine ? number : 63) * 4, mine ? lane : 0);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      real[m] = m * 16 + i16 < count - base;
+      real[m] = m * 16 + i16 < count - first;
       const int at = window * 64 + __shfl(from, m * 16 + i16);
       row[m] = real[m] ? at : r.rows - 1;
     }
-    base += 16 * MT;
-    if (base >= count) same = 0;
-    return true;
   }
 };
 
@@ -239,8 +244,11 @@ __global__ __launch_bounds__(64 * W) void shrink_kernel(ShrinkArgs a) {
 
   Units<MT> unit(a.r, false, window, window + 1);
   int turn = 0;
-  for (int n = 0; unit.next(); ++n) {
-    if (n % a.units_by != group) continue;
+  int skip = group;   // units of other workgroups before the next of this one's
+  while (unit.step()) {
+    if (skip-- > 0) continue;
+    skip = a.units_by - 1;
+    unit.rows();
     // (The adapter's own rank comes in at the end alone, so that no load waits for it.)
     const int id = unit.id, rank = a.r.rank_of(id);
     const float scale = a.r.scales ? a.r.scales[id] : 1.0f;
@@ -550,9 +558,10 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
   Units<1> unit(a.r, !a.in_place, window0, window1);
   int skip = group;   // units of other workgroups before the next of this one's
   auto advance = [&]() __attribute__((always_inline)) {
-    bool more = unit.next();
-    for (; more && skip > 0; --skip) more = unit.next();
+    bool more = unit.step();
+    for (; more && skip > 0; --skip) more = unit.step();
     skip = a.units_by - 1;
+    if (more) unit.rows();
     return more;
   };
   // WHOLE: all of the wave's columns exist.
@@ -751,8 +760,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void small_kernel(SmallArgs a) {
   Units<1> unit(a.r, !a.in_place, 0, 1);
   auto run = [&](auto whole) __attribute__((always_inline)) {
     constexpr bool WHOLE = decltype(whole)::value;
-    for (int n = 0; unit.next(); ++n) {
-      if (n % a.units_by != group) continue;
+    int skip = group;
+    while (unit.step()) {
+      if (skip-- > 0) continue;
+      skip = a.units_by - 1;
+      unit.rows();
       const int id = max(unit.id, 0);   // (without an adapter: one's loads, not used)
       const int marked = __shfl(unit.real[0] ? unit.row[0] : ~unit.row[0], lane / 4), row = max(marked, ~marked);
       const long long adapter = static_cast<long long>(id) * a.r.rank;
