@@ -64,9 +64,10 @@ Shrink shrink_of(const void *z, long long ldz, const void *w, int rank, int K, i
 
 // Whether one kernel makes both products: where its waves' shares of K are short, and the adapters'
 // A, read again for every 128 columns of Y, come to 16 MB at most if every row has another.
-// In graphs, bfloat16, rank 16: 1 row of 4096 x 4096 takes 8.2 us so and 7.8 by two kernels
-// (8.8 and 11.9 launched one by one), of 8192 x 8192 12.4 and 8.1, of 1024 x 1024 5.0 and 7.3;
-// 8 rows of 2048 x 2048 7.4 and 8.9, 16 of 4096 x 1024 14.2 and 13.4.
+// In graphs, bfloat16, rank 16: 1 row of 4096 x 4096 takes 8.0 us so and 7.6 by two kernels
+// (8.8 and 11.9 launched one by one), of 8192 x 8192 12.3 and 7.9, of 1024 x 1024 4.8 and 7.1;
+// 8 rows of 2048 x 2048 6.7 and 8.5, 32 of 1024 x 1024 7.3 and 12.4, 16 of 4096 x 1024 7.9 and
+// 9.5; rank 32, 1 row of 4096 x 4096 11.4 and 8.1.
 bool one_kernel(int rows, const gemm_lora_t &s) {
   const double again = static_cast<double>(ceil_div(s.N, kSmallCols)) * rows * s.rank * s.K * elem_size(s.type);
   return rows <= 64 && s.rank <= 32 && s.K * rank_tiles(s.rank) <= 4096 && again <= 16 << 20;

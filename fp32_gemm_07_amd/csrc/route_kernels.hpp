@@ -11,7 +11,7 @@
 // logit, so where neither a bias nor sums of a group's scores come in, logits are compared
 // themselves (as whole numbers in their order). Else scores are computed in FP32 first; where
 // two values that the choice sets apart lie nearer to each other than their errors (one token in
-// some hundred), FP64 values settle it: of 16 candidates, a lane each, or of all.
+// some hundred), FP64 values settle it: of a few candidates, a lane each, or of all.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -262,8 +262,8 @@ __device__ inline const KEY *put_keys(const RouteArgs &a, const KEY (&key)[PER],
 }
 
 // The choice: lane n's into `mine`, in descending order. Float keys are known up to `error`:
-// where two that have to be told apart lie within that, `sure` is false, and the row's 16
-// lanes have the 16 best instead, `rest` being the best of the others.
+// where two that have to be told apart lie within that, `sure` is false, and the row's lanes
+// have two more (up to 16) instead, `rest` being the best of the others.
 template <int PER, class KEY>
 __device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l16, float error, bool &sure, KEY &rest) {
   KEY best;
@@ -279,7 +279,7 @@ __device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l1
       if (n > 0 && n <= a.top_k && KeyOf<KEY>::some(most) && !(last - most > 2.0f * error)) sure = false;
       last = rest = most;
     }
-    if (n >= a.top_k && (sure || n == 16)) break;   // (rows differ: the lanes of one leave together)
+    if (n >= a.top_k && (sure || n == min(a.top_k + 2, 16))) break;   // (rows differ: the lanes of one leave together)
     const int expert = row_min(best == most ? at : kRouteMaxExperts);
     if (l16 == n && KeyOf<KEY>::some(most)) mine = expert;
     if (expert == at && KeyOf<KEY>::some(best)) {   // its lane looks for its next
@@ -292,7 +292,7 @@ __device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l1
   return mine;
 }
 
-// The choice among 16 candidates, one in each lane (-1: none), on their FP64 values. `sure` is
+// The choice among candidates, one in each lane (-1: none), on their FP64 values. `sure` is
 // false where an expert that is none of them may be among the best after all.
 template <int TYPE>
 __device__ int settle_experts(const RouteArgs &a, const typename Elem<TYPE>::store *row, int l16, int candidate,
@@ -414,10 +414,11 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
     unsigned rest;
     mine = choose_experts<PER, unsigned>(a, key, l16, 0.0f, sure, rest);
   } else {
-    // Estimates: e^x by v_exp_f32 is off by |x| 2^-23 (the argument's rounding, times log2 e) + 2^-23
-    // of itself, and |x| e^x < 0.37; a reciprocal, a product, a sum of up to 36 terms by 2^-24
-    // each. So a sigmoid is within 2^-21, a softmax within 2^-18 of the largest, here twice
-    // that; adding the bias rounds once more.
+    // Estimates. e^-l by v_exp_f32 is off by (|l| + 1) 2^-23 of itself (the argument's rounding, its
+    // own), a sigmoid by s (1 - s) of that, which is below 2^-24 for both terms together with
+    // |l| s (1 - s) < 0.23; 1 + e^-l and the reciprocal add 2^-24 + 2^-23: within 2^-22, taken
+    // twice. A softmax: |x| e^x < 0.37, a product, a sum of up to 36 terms: within 2^-18 of the
+    // largest, taken twice. Adding the bias rounds once more.
     float key[PER], bias[PER], sum = 0.0f, most = 0.0f;
     if (a.bias) {
 #pragma unroll
@@ -436,7 +437,7 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
         key[j] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
       }
     }
-    float error = 0x1p-20f;
+    float error = 0x1p-21f;
     if (a.score == kSoftmax) {
       const float inverse = 1.0f / row_total(sum);
       error = 0x1p-17f * inverse;
@@ -450,7 +451,7 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
       most = fmaxf(most, KeyOf<float>::some(key[j]) ? fabsf(key[j]) : 0.0f);
     }
     bad |= row_max(nan ? 1u : 0u) != 0;
-    error += 0x1p-23f * row_max(most);
+    error += 0x1p-24f * row_max(most);
     if (a.groups > a.top_groups) {
       float apart;
       const float *in_lds = put_keys<PER>(a, key, l16, keys);
