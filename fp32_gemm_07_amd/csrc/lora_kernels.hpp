@@ -1205,6 +1205,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     }
   }
   if (wave != 0) return;
+  const int own = a.r.rank_of(slot.adapter);   // (behind it zeros, whatever Z holds)
   const long long size = static_cast<long long>(a.r.rank) * p.cols;
   float *out = slot.partial < 0 ? p.out + slot.adapter * size : p.partial + slot.partial * size;
 #pragma unroll
@@ -1215,7 +1216,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
       if (r >= a.r.rank) continue;
 #pragma unroll
       for (int j = 0; j < CL; ++j)
-        if (j < left) out[second ? static_cast<long long>(n + j) * a.r.rank + r : static_cast<long long>(r) * p.cols + n + j] = acc[j][t][v];
+        if (j < left) out[second ? static_cast<long long>(n + j) * a.r.rank + r : static_cast<long long>(r) * p.cols + n + j] = r < own ? acc[j][t][v] : 0.0f;
     }
 }
 

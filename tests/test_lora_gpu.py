@@ -320,6 +320,37 @@ def test_same_bits_every_time(kind):
             assert np.array_equal(p, q)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,rank", [(40, 8), (40, 100), (1500, 24)])
+def test_gradients_do_not_mix(rows, rank, kind):
+    """A NaN or infinity in a row reaches the gradients of that row and of its adapter, up to that
+    adapter's own rank: behind it, and where no row has the adapter, they are zeros."""
+    rng = np.random.default_rng(rows + rank)
+    c = Case(rng, rows, 70, 96, rank, 6, kind, True)
+    c.ranks[:] = [rank, 3, rank // 2, rank, 0, rank]
+    c.a, c.b = mxref.to_type(rng.normal(size=c.a.shape), KINDS[kind]), mxref.to_type(rng.normal(size=c.b.shape), KINDS[kind])
+    c.ids = np.arange(rows, dtype=np.int32) % 6 - 1        # every sixth has none; none has adapter 5
+    clean = run_backward(c)
+    c.x[0], c.dy[6] = np.nan, np.inf                       # of no adapter
+    c.x[8], c.dy[14] = np.nan, np.inf                      # of adapter 1
+    c.x[15], c.dy[9] = np.inf, np.nan                      # of adapter 2
+    c.x[11], c.dy[5] = np.nan, np.inf                      # of adapter 4, rank 0
+    say(f"gradients do not mix {rows} r{rank} {kind}")
+    dx, da, db = run_backward(c)
+    same = ~np.isin(np.arange(rows), [5, 6, 9, 14])
+    assert np.array_equal(dx[same], clean[0][same])
+    assert np.array_equal(dx[6], clean[0][6]) and np.array_equal(dx[5], clean[0][5])
+    assert not np.isfinite(dx[[9, 14]]).any()
+    for i in range(6):
+        own = c.ranks[i]
+        assert (da[i, own:] == 0).all() and (db[i, :, own:] == 0).all(), i
+        if i in (1, 2):
+            assert not np.isfinite(da[i, :own]).any() and not np.isfinite(db[i, :, :own]).any()
+        else:
+            assert np.array_equal(da[i], clean[1][i]) and np.array_equal(db[i], clean[2][i])
+    assert (da[5] == 0).all() and (db[5] == 0).all()
+
+
 def test_gradient_against_differences():
     """Differences of what gemm_lora itself gives: the sum of Y dY is linear in each input, so with whole
     numbers and steps of 1 the differences are exact."""
