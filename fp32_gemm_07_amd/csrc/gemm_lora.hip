@@ -249,11 +249,11 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
     Slot *slots = reinterpret_cast<Slot *>(w + l.slots);
     int2 *sums = reinterpret_cast<int2 *>(w + l.sums);
     int *order = reinterpret_cast<int *>(w + l.order), *position = reinterpret_cast<int *>(w + l.position);
-    const int a_tiles = dX ? static_cast<int>(std::min<long long>(ceil_div(s.K, kTransRows), 256)) : 0;
-    const int b_tiles = static_cast<int>(std::min<long long>(ceil_div(s.N, kTransRows), 256));
+    const int a_tiles = dX ? static_cast<int>(ceil_div(s.K, kTransRows)) : 0, b_tiles = static_cast<int>(ceil_div(s.N, kTransRows));
+    const long long tiles = static_cast<long long>(std::min(rows, s.adapters)) * (a_tiles + b_tiles);   // at most
     const PrepareArgs pa{r, l.slot_rows, s.N, header, slots, sums, order, position, s.A, s.B, w + l.at, w + l.bt,
                          s.K, a_tiles, b_tiles};
-    int launch_st = launches.prepare(pa, 1 + (rows ? s.adapters * (a_tiles + b_tiles) : 0), stream);
+    int launch_st = launches.prepare(pa, 1 + static_cast<int>(std::min(tiles, 2LL * cus)), stream);
     if (launch_st != GEMM_OK) return launch_st;
     void *g = w + l.g;
     if (rows > 0) {

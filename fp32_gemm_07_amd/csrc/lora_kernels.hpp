@@ -894,9 +894,9 @@ struct PrepareArgs {
   const void *a, *b;    // rank x K and N x rank for each adapter
   void *at, *bt;        // K x rank and rank x N for each
   int K;
-  int a_tiles, b_tiles; // workgroups for each adapter's
+  int a_tiles, b_tiles; // of each adapter's: kTransRows columns of A, rows of B
 };
-constexpr int kTransRows = 64;   // columns of A, rows of B that a workgroup transposes at a time
+constexpr int kTransRows = 64;   // columns of A, rows of B of a tile
 
 // Lanes of the wave that have the same id (valid ones).
 __device__ inline unsigned long long same_id(int id, bool valid, int bits) {
@@ -912,8 +912,9 @@ __device__ inline unsigned long long same_id(int id, bool valid, int bits) {
 // Workgroup 0 sorts the rows by adapter, keeping their order (so that sums over them do not
 // depend on timing): every wave counts a stretch of rows, running sums over adapters and
 // waves say where each wave's rows of an adapter go, and each wave puts its
-// rows there. An adapter's positions begin at a multiple of 32. The other workgroups transpose
-// one adapter's A or B, if any row has that adapter.
+// rows there. An adapter's positions begin at a multiple of 32. The other workgroups share the
+// tiles of A and B, which they transpose, of those adapters that rows have. (64 rows on 32 of
+// 1024 adapters, 4096 x 4096, rank 16: 156 us backward, and 640 with workgroups for every adapter; 8192 rows on 64: 161 and 185.)
 // 10 us for 8192 rows and 4 adapters of rank 32 and 4096 x 4096: the waits of a few dependent steps.
 template <int TYPE>
 __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
@@ -923,23 +924,41 @@ __global__ __launch_bounds__(1024) void prepare_kernel(PrepareArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (blockIdx.x > 0) {
-    const int tiles = a.a_tiles + a.b_tiles, id = (blockIdx.x - 1) / tiles, rank = a.r.rank;
-    bool used = false;   // 8192 ids on their way at a time
-    for (int row0 = 0; !__syncthreads_or(used); row0 += 8 * 1024) {
-      if (row0 >= a.r.rows) return;
+    // The adapters that rows have, in order: first a flag for each, then their list in its place.
+    int *used = lds + kLoraMaxRank * (kTransRows + 1), *sums = lds + W * kLoraMaxAdapters;
+    used[threadIdx.x] = 0;
+    __syncthreads();
+    for (int row0 = 0; row0 < a.r.rows; row0 += 8 * 1024) {   // 8192 ids on their way at a time
+      int loaded[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) used |= a.r.load_id(row0 + i * 1024 + threadIdx.x) == id;
+      for (int i = 0; i < 8; ++i) loaded[i] = a.r.load_id(row0 + i * 1024 + threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (a.r.id_of(loaded[i]) >= 0) used[loaded[i]] = 1;
     }
+    __syncthreads();
+    const bool mine = used[threadIdx.x] != 0;
+    const unsigned long long wave_has = __ballot(mine);
+    if (lane == 0) sums[wave] = __popcll(wave_has);
+    __syncthreads();
+    int many_used = 0, before = 0;
+    for (int w = 0; w < W; ++w) {
+      before += w < wave ? sums[w] : 0;
+      many_used += sums[w];
+    }
+    if (mine) used[before + __popcll(wave_has & ((1ull << lane) - 1))] = threadIdx.x;
+    __syncthreads();
+
     store *tile = reinterpret_cast<store *>(lds);   // [rank][64], a row of 65
-    const int at = (blockIdx.x - 1) % tiles;
-    const bool second = at >= a.a_tiles;
-    const int size = second ? a.N : a.K;            // across the ranks
-    const long long adapter = static_cast<long long>(id) * rank * size;
-    const store *from = static_cast<const store *>(second ? a.b : a.a) + adapter;
-    store *to = static_cast<store *>(second ? a.bt : a.at) + adapter;
-    const int step = (second ? a.b_tiles : a.a_tiles) * kTransRows;
-    for (int n0 = (second ? at - a.a_tiles : at) * kTransRows; n0 < size; n0 += step) {
-      const int many = min(kTransRows, size - n0);
+    const int tiles = a.a_tiles + a.b_tiles, rank = a.r.rank;
+    for (int unit = blockIdx.x - 1; unit < many_used * tiles; unit += gridDim.x - 1) {
+      const int id = used[unit / tiles], at = unit % tiles;
+      const bool second = at >= a.a_tiles;
+      const int size = second ? a.N : a.K;            // across the ranks
+      const int n0 = (second ? at - a.a_tiles : at) * kTransRows, many = min(kTransRows, size - n0);
+      const long long adapter = static_cast<long long>(id) * rank * size;
+      const store *from = static_cast<const store *>(second ? a.b : a.a) + adapter;
+      store *to = static_cast<store *>(second ? a.bt : a.at) + adapter;
       // the ranks along a row (B, A transposed), or 64 neighbours of one rank (A, B transposed)
       auto along = [&](bool load) {
         for (int i = threadIdx.x; i < many * rank; i += 1024) {

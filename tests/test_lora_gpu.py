@@ -310,6 +310,16 @@ def test_backward_many_rows_of_one_adapter():
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_backward_many_adapters(kind):
+    """More tiles to transpose than workgroups; whole numbers, so every bit counts."""
+    rng = np.random.default_rng(31)
+    for mixed in (False, True):
+        c = Case(rng, 900, 300, 260, 5, 1000, kind, mixed, whole=True)
+        check_backward(c, f"900 rows on 1000 adapters {kind}", exact=True)
+        check_backward(c, f"900 rows on 1000 adapters, no dX {kind}", exact=True, dx=False)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_same_bits_every_time(kind):
     rng = np.random.default_rng(9)
     c = Case(rng, 1500, 300, 260, 40, 5, kind, True)
