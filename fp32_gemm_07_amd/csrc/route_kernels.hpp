@@ -160,11 +160,14 @@ __device__ inline void group_top(const RouteArgs &a, int g, int l16, const KEY *
     first = k > first ? k : first;
   }
 }
+// What a group is worth: a sum of two keys, of estimates half of it: two finite keys near the
+// type's lowest value (a bias that masks) would add to -inf in FP32, a group without experts.
 template <class KEY>
 __device__ inline KEY group_value(const RouteArgs &a, KEY first, KEY second) {
   // (whole numbers are compared where the largest alone counts)
-  if constexpr (KeyOf<KEY>::sums) return a.group_top == 2 && KeyOf<KEY>::some(second) ? first + second : first;
-  else return first;
+  if constexpr (!KeyOf<KEY>::sums) return first;
+  const KEY half = KeyOf<KEY>::estimate ? KEY(0.5) : KEY(1);
+  return a.group_top != 2 ? first : KeyOf<KEY>::some(second) ? half * first + half * second : half * first;
 }
 
 // The best groups, as bits, from the values of groups l16, l16 + 16, ... `apart`, for floats:
@@ -456,7 +459,7 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
       float apart;
       const float *in_lds = put_keys<PER>(a, key, l16, keys);
       unsigned long long stay = best_groups<float>(a, l16, in_lds, &apart);
-      if (!(apart > 5.0f * error) && !bad)   // of sums of two, and a rounding (a row's lanes go together)
+      if (!(apart > 2.5f * error) && !bad)   // of halves of sums of two, and a rounding (a row's lanes go together)
         stay = a.score == kSigmoid ? settle_groups<TYPE>(a, row, l16, in_lds, error) : all_doubles<TYPE>(a, row, top, l16, keys);
       leave_groups<PER, float>(a, key, l16, stay);
     }

@@ -374,3 +374,27 @@ def test_layer_on_the_layers_own_choice():
     lib.gemm_mx_moe(T, H, I, E, k, True, dev(l), E, dev(x), 0, H, w1[2], w1[3], w2[2], w2[3], z, H, None, 0, stream())
     want, bound = mxref.moe(x.astype(np.float64), mxref.route(l, k, True), mxref.decode(w1[0], w1[1], H), mxref.decode(w2[0], w2[1], I), I, 3, 3)
     assert (np.abs(y - z.cpu().numpy()) <= 2 * bound).all()
+
+
+LOWEST = float(np.finfo(np.float32).min)
+
+
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+@pytest.mark.parametrize("E,g,tg,gt,k", [(8, 4, 2, 2, 4), (16, 4, 2, 2, 6), (16, 4, 3, 2, 9), (96, 8, 3, 2, 16), (300, 10, 2, 2, 5), (48, 16, 5, 1, 12)])
+def test_bias_of_a_types_lowest_and_largest_values(E, g, tg, gt, k, score):
+    """Finite biases whose sums of two pass float32: a group of such experts is worth what 64 bits say, and its
+    experts fill up where the others do not suffice. Only a bias of -inf takes an expert out."""
+    rng = np.random.default_rng(E + k)
+    l = logits(rng, 24, E, "f32")
+    l[0] = 0.25
+    size = E // g
+    masks = [np.where(np.arange(E) < size, 0.0, LOWEST),             # all groups but the first
+             np.where(np.arange(E) < E - size, LOWEST, 0.0),         # all but the last
+             np.full(E, LOWEST), np.full(E, -LOWEST),
+             np.where(np.arange(E) // size % 2 == 1, -LOWEST, 0.0),  # sums past the largest value
+             np.where(np.arange(E) % size == 0, 0.0, LOWEST),        # one expert left in each group
+             np.where(np.arange(E) % size < 2, LOWEST, -np.inf)]
+    masks += [rng.choice([0.0, LOWEST, -LOWEST, -2e38, 2e38, -1e38, -1e9, -np.inf, np.inf], E) for _ in range(12)]
+    for n, b in enumerate(masks):
+        check_route(l, "f32", b.astype(np.float32), ref.Router(E, k, score, g, tg, gt, True),
+                    f"bias of lowest values {n}: {E} experts groups {g} {tg} {gt} top {k} {score}")
