@@ -752,7 +752,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void small_kernel(SmallArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col_blocks = (a.N + kSmallCols - 1) / kSmallCols;
   const int group = blockIdx.x / col_blocks;
-  const int nb = (blockIdx.x - group * col_blocks) * kSmallCols + wave * 16;   // (may lie past the last column)
+  const int col0 = (blockIdx.x - group * col_blocks) * kSmallCols;
+  const int nb = col0 + wave * 16;   // (may lie past the last column)
   const int k_wave = ((a.K + W - 1) / W + 63) / 64 * 64;
   const int ka = min(a.K, wave * k_wave), kb = min(a.K, ka + k_wave);
   float *stage = stages[wave];
@@ -868,7 +869,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void small_kernel(SmallArgs a) {
       if (marked >= 0) store4<TYPE>(static_cast<store *>(a.y) + row * a.ldy + col, left, out);
     }
   };
-  if (nb + 16 <= a.N) run(std::true_type());
+  // WHOLE: all of the workgroup's columns exist. (Of the workgroup's, not of the wave's: its waves
+  // have to meet at the same barriers.)
+  if (col0 + kSmallCols <= a.N) run(std::true_type());
   else run(std::false_type());
 }
 

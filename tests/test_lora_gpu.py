@@ -404,3 +404,16 @@ def test_row_counts_around_the_kernels_borders(rows, kind):
         c = Case(rng, rows, 130, 70, 18, 4, kind, mixed, whole=True, pad=2)
         check_forward(c, f"rows {rows} {kind} mixed {mixed}", base="place", exact=True)
         check_backward(c, f"rows {rows} {kind} mixed {mixed}", base="place", exact=True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [1, 4, 16, 17, 100, 127, 128, 129, 141, 144, 240, 255, 257, 400])
+def test_columns_around_a_workgroups_last(n, kind):
+    """Both products in one kernel where a workgroup's 128 columns end inside the matrix, inside a wave's 16 or
+    before some of its waves begin: the waves share K and its barriers whatever they have to store."""
+    rng = np.random.default_rng(n)
+    for rows, rank in ((1, 7), (40, 16), (64, 32)):
+        c = Case(rng, rows, n, 333, rank, 9, kind, True, whole=True, pad=n % 2)
+        assert lib.gemm_lora_workspace_bytes(rows, c.set()) == 0   # (one kernel)
+        for base in ("other", "place", "none"):
+            check_forward(c, f"{n} columns, {rows} rows, rank {rank} {kind} {base}", base, exact=True)
