@@ -459,7 +459,9 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
       float apart;
       const float *in_lds = put_keys<PER>(a, key, l16, keys);
       unsigned long long stay = best_groups<float>(a, l16, in_lds, &apart);
-      if (!(apart > 2.5f * error) && !bad)   // of halves of sums of two, and a rounding (a row's lanes go together)
+      // Half a sum of two is off by the mean of their errors and a rounding of its own, together by
+      // no more than 2 errors, so the difference of two by 4. (A row's lanes go together.)
+      if (!(apart > 4.0f * error) && !bad)
         stay = a.score == kSigmoid ? settle_groups<TYPE>(a, row, l16, in_lds, error) : all_doubles<TYPE>(a, row, top, l16, keys);
       leave_groups<PER, float>(a, key, l16, stay);
     }

@@ -398,3 +398,52 @@ def test_bias_of_a_types_lowest_and_largest_values(E, g, tg, gt, k, score):
     for n, b in enumerate(masks):
         check_route(l, "f32", b.astype(np.float32), ref.Router(E, k, score, g, tg, gt, True),
                     f"bias of lowest values {n}: {E} experts groups {g} {tg} {gt} top {k} {score}")
+
+
+def logit_of(score, sign, off):
+    """The float32 logit whose sigmoid lies nearest behind score + sign * off, on that side (float64), and how far."""
+    at = score + sign * off
+    l = np.float32(np.log(at / (1.0 - at)))
+    for _ in range(8):
+        far = sign * (1.0 / (1.0 + np.exp(-np.float64(l))) - score)
+        if far >= off:
+            return l, far
+        l = np.nextafter(l, np.float32(sign * np.inf), dtype=np.float32)
+    return l, -1.0
+
+
+@pytest.mark.parametrize("largest", [16, 64, 1024])
+@pytest.mark.parametrize("last", [False, True])
+def test_groups_next_to_each_other_under_a_large_bias(largest, last):
+    """Two groups of two experts under biases near a power of two, so that a value in float32 is a whole number of
+    `unit`. One group's values lie next to half a unit and round down, and so does their sum; the other's
+    round up: their float32 sums are 4 units apart, while in 64 bits the first is worth a little more."""
+    rng = np.random.default_rng(largest)
+    unit = largest * 2.0 ** -23
+    many = 0
+    for _ in range(30):
+        score = rng.uniform(0.55, 0.9)                       # of the expert that gets most of its value from there
+        whole = int(score / unit)
+        one, two = rng.integers(0, 40, 2)
+        add = np.array([0, one, whole // 2 + two, whole - whole // 2 + one - two])   # units above `largest`: both sums the same
+        rows = []
+        for _ in range(400):
+            t = np.array([whole + rng.integers(-3, 4), *rng.integers(0, 4, 3)])
+            m = add + t                                      # the units below each value
+            if m[0] % 2 or not m[1] % 2 or (m[0] + m[1]) % 4 != 1 or m[0] + m[1] != m[2] + m[3]:
+                continue
+            small = [logit_of((t[n] + 0.5) * unit, -1 if n == 1 else 1, 2.0 ** -19 * (t[n] + 0.5) * unit) for n in (1, 2, 3)]
+            lost = sum(far for _, far in small)
+            l, far = logit_of((t[0] + 0.5) * unit, 1, 1.5 * lost + 2.0 ** -29)
+            if min(far for _, far in small) > 0 and 0 < far < 2.0 ** -25:
+                rows.append([l] + [v for v, _ in small])
+        if not rows:
+            continue
+        many += len(rows)
+        l = np.array(rows, np.float32)
+        b = (largest + add * unit).astype(np.float32)
+        if last:
+            l, b = l[:, ::-1].copy(), b[::-1].copy()
+        chosen = check_route(l, "f32", b, ref.Router(4, 2, ref.SIGMOID, 2, 1, 2, True), f"groups next to each other, biases near {largest} {last}")
+        assert (chosen // 2 == int(last)).all()
+    assert many > 20
