@@ -110,6 +110,11 @@ struct KeyOf<double> {
   static constexpr double none = -__builtin_huge_val();
   static __device__ inline bool some(double k) { return k > -__builtin_huge_val(); }
 };
+// How far two estimates of up to `v` have to lie apart to be in order: a score is off by up to
+// `error`, and the bias's addition rounds once. (By the values that are compared, not by the largest of all:
+// an expert masked by a bias of -1e9 would leave nothing settled. 4096 tokens on 8 of 256 in groups
+// with such a one 41 us and 13.)
+__device__ inline float margin(float error, float v) { return fmaf(0x1p-23f, fabsf(v), 2.0f * error); }
 __device__ inline unsigned logit_key(float v) {   // v finite or +inf
   const unsigned b = __builtin_bit_cast(unsigned, v + 0.0f);   // -0 equals +0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -170,15 +175,12 @@ __device__ inline KEY group_value(const RouteArgs &a, KEY first, KEY second) {
   return a.group_top != 2 ? first : KeyOf<KEY>::some(second) ? half * first + half * second : half * first;
 }
 
-// The best groups, as bits, from the values of groups l16, l16 + 16, ... `apart`, for floats:
-// how much the last group that stays is worth more than the best that does not.
+// The best groups, as bits, from the values of groups l16, l16 + 16, ...; those that stay lose theirs.
 constexpr int kRowGroups = kRouteMaxGroups / 16;
 template <class KEY>
-__device__ inline unsigned long long choose_groups(const RouteArgs &a, KEY (&value)[kRowGroups], int l16,
-                                                   KEY *apart = nullptr) {
+__device__ inline unsigned long long choose_groups(const RouteArgs &a, KEY (&value)[kRowGroups], int l16) {
   unsigned long long stay = 0;
-  KEY last = KeyOf<KEY>::none;
-  for (int n = 0; n <= a.top_groups; ++n) {
+  for (int n = 0; n < a.top_groups; ++n) {
     KEY best = KeyOf<KEY>::none;
     int at = kRouteMaxGroups;
 #pragma unroll
@@ -189,11 +191,7 @@ __device__ inline unsigned long long choose_groups(const RouteArgs &a, KEY (&val
       }
     }
     const KEY most = row_max(best);
-    const bool some = KeyOf<KEY>::some(most);
-    if constexpr (KeyOf<KEY>::sums)
-      if (apart) *apart = some ? last - most : -KeyOf<KEY>::none;
-    if (n == a.top_groups || !some) break;   // (rows differ: the lanes of one leave together)
-    last = most;
+    if (!KeyOf<KEY>::some(most)) break;   // (rows differ: the lanes of one leave together)
     const int g = row_min(best == most ? at : kRouteMaxGroups);
     stay |= 1ull << g;
 #pragma unroll
@@ -202,16 +200,42 @@ __device__ inline unsigned long long choose_groups(const RouteArgs &a, KEY (&val
   }
   return stay;
 }
+// The same from a row's keys. With estimates `sure` says whether every group that stays is worth more than
+// every other, whatever the errors: half a sum of two is off by the mean of theirs and a rounding of
+// its own, error + 2^-24 (|first| + |second|) together; twice the second term, for the bounds' roundings.
 template <class KEY>
-__device__ inline unsigned long long best_groups(const RouteArgs &a, int l16, const KEY *keys, KEY *apart = nullptr) {
+__device__ inline unsigned long long best_groups(const RouteArgs &a, int l16, const KEY *keys, float error, bool &sure) {
   KEY value[kRowGroups];
+  float least[kRowGroups], off[kRowGroups];
 #pragma unroll
   for (int m = 0; m < kRowGroups; ++m) {
-    KEY first = KeyOf<KEY>::none, second = KeyOf<KEY>::none;
-    if (m * 16 + l16 < a.groups) group_top(a, m * 16 + l16, l16, keys, first, second);
-    value[m] = group_value(a, first, second);
+    value[m] = KeyOf<KEY>::none;
+    least[m] = __builtin_inff();
+    off[m] = 0.0f;
+    if (m * 16 + l16 < a.groups) {
+      KEY first, second;
+      group_top(a, m * 16 + l16, l16, keys, first, second);
+      value[m] = group_value(a, first, second);
+      if constexpr (KeyOf<KEY>::estimate) {
+        const float both = fabsf(first) + (a.group_top == 2 && KeyOf<KEY>::some(second) ? fabsf(second) : 0.0f);
+        off[m] = fmaf(0x1p-23f, fminf(both, 0x1.fffffep127f), error);   // (finite: an infinite bias is exact)
+        if (KeyOf<KEY>::some(first)) least[m] = value[m] - off[m];
+      }
+    }
   }
-  return choose_groups(a, value, l16, apart);
+  const unsigned long long stay = choose_groups(a, value, l16);
+  sure = true;
+  if constexpr (KeyOf<KEY>::estimate) {
+    float most = KeyOf<float>::none;
+#pragma unroll
+    for (int m = 0; m < kRowGroups; ++m) most = fmaxf(most, value[m] + off[m]);
+    most = row_max(most);
+    bool open = false;
+#pragma unroll
+    for (int m = 0; m < kRowGroups; ++m) open |= !KeyOf<float>::some(value[m]) && !(least[m] > most);   // (one that stays)
+    sure = row_max(open && KeyOf<float>::some(most) ? 1u : 0u) == 0;
+  }
+  return stay;
 }
 
 // A sigmoid score with its bias in FP64.
@@ -234,7 +258,7 @@ __device__ unsigned long long settle_groups(const RouteArgs &a, const typename E
   for (int g = l16; g < a.groups; g += 16) {
     float first, second;
     group_top(a, g, l16, keys, first, second);
-    const float from = (a.group_top == 2 ? second : first) - 2.0f * error;
+    const float last = a.group_top == 2 ? second : first, from = last - margin(error, last);
     double top[2] = {KeyOf<double>::none, KeyOf<double>::none};
 #pragma unroll 1
     for (int e = g * size; e < g * size + size; ++e) {
@@ -264,8 +288,8 @@ __device__ inline const KEY *put_keys(const RouteArgs &a, const KEY (&key)[PER],
   return keys;
 }
 
-// The choice: lane n's into `mine`, in descending order. Float keys are known up to `error`:
-// where two that have to be told apart lie within that, `sure` is false, and the row's lanes
+// The choice: lane n's into `mine`, in descending order. Of float keys, where two that
+// have to be told apart lie within their margin, `sure` is false, and the row's lanes
 // have two more (up to 16) instead, `rest` being the best of the others.
 template <int PER, class KEY>
 __device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l16, float error, bool &sure, KEY &rest) {
@@ -279,7 +303,8 @@ __device__ inline int choose_experts(const RouteArgs &a, KEY (&key)[PER], int l1
     const KEY most = row_max(best);
     if constexpr (KeyOf<KEY>::estimate) {
       // (not greater: also where both are infinite)
-      if (n > 0 && n <= a.top_k && KeyOf<KEY>::some(most) && !(last - most > 2.0f * error)) sure = false;
+      if (n > 0 && n <= a.top_k && KeyOf<KEY>::some(most) && !(last - most > margin(error, fmaxf(fabsf(last), fabsf(most)))))
+        sure = false;
       last = rest = most;
     }
     if (n >= a.top_k && (sure || n == min(a.top_k + 2, 16))) break;   // (rows differ: the lanes of one leave together)
@@ -310,7 +335,7 @@ __device__ int settle_experts(const RouteArgs &a, const typename Elem<TYPE>::sto
   }
   // to lane `ahead` of the row (all different)
   const int mine = __builtin_amdgcn_ds_permute(((threadIdx.x & 48) + ahead) * 4, candidate);
-  const unsigned worst = row_max(ahead == a.top_k - 1 && !(v - static_cast<double>(rest) > 2.0f * error) ? 1u : 0u);
+  const unsigned worst = row_max(ahead == a.top_k - 1 && !(v - static_cast<double>(rest) > margin(error, rest)) ? 1u : 0u);
   sure = !KeyOf<float>::some(rest) || worst == 0;
   return l16 < a.top_k ? mine : -1;
 }
@@ -355,7 +380,8 @@ __device__ unsigned long long all_doubles(const RouteArgs &a, const typename Ele
   }
   wave_order();
   if (a.groups == a.top_groups) return ~0ull;
-  return best_groups<double>(a, l16, keys);
+  bool sure;
+  return best_groups<double>(a, l16, keys, 0.0f, sure);
 }
 
 // The choice by them.
@@ -411,9 +437,9 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
     unsigned key[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) key[j] = l[j] == -__builtin_inff() ? 0u : logit_key(l[j]);
-    if (a.groups > a.top_groups)
-      leave_groups<PER, unsigned>(a, key, l16, best_groups<unsigned>(a, l16, put_keys<PER>(a, key, l16, keys)));
     bool sure;
+    if (a.groups > a.top_groups)
+      leave_groups<PER, unsigned>(a, key, l16, best_groups<unsigned>(a, l16, put_keys<PER>(a, key, l16, keys), 0.0f, sure));
     unsigned rest;
     mine = choose_experts<PER, unsigned>(a, key, l16, 0.0f, sure, rest);
   } else {
@@ -421,8 +447,8 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
     // own), a sigmoid by s (1 - s) of that, which is below 2^-24 for both terms together with
     // |l| s (1 - s) < 0.23; 1 + e^-l and the reciprocal add 2^-24 + 2^-23: within 2^-22, taken
     // twice. A softmax: |x| e^x < 0.37, a product, a sum of up to 36 terms: within 2^-18 of the
-    // largest, taken twice. Adding the bias rounds once more.
-    float key[PER], bias[PER], sum = 0.0f, most = 0.0f;
+    // largest, taken twice. (Adding the bias: margin.)
+    float key[PER], bias[PER], sum = 0.0f;
     if (a.bias) {
 #pragma unroll
       for (int j = 0; j < PER; j += 4) load_logits<kF32>(a.bias, expert_of(j, l16), a.experts, &bias[j]);
@@ -451,17 +477,13 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
     for (int j = 0; j < PER; ++j) {
       nan |= bias[j] != bias[j];
       key[j] = l[j] == -__builtin_inff() ? KeyOf<float>::none : key[j] + bias[j];
-      most = fmaxf(most, KeyOf<float>::some(key[j]) ? fabsf(key[j]) : 0.0f);
     }
     bad |= row_max(nan ? 1u : 0u) != 0;
-    error += 0x1p-24f * row_max(most);
     if (a.groups > a.top_groups) {
-      float apart;
+      bool apart;
       const float *in_lds = put_keys<PER>(a, key, l16, keys);
-      unsigned long long stay = best_groups<float>(a, l16, in_lds, &apart);
-      // Half a sum of two is off by the mean of their errors and a rounding of its own, together by
-      // no more than 2 errors, so the difference of two by 4. (A row's lanes go together.)
-      if (!(apart > 4.0f * error) && !bad)
+      unsigned long long stay = best_groups<float>(a, l16, in_lds, error, apart);
+      if (!apart && !bad)   // (a row's lanes go together)
         stay = a.score == kSigmoid ? settle_groups<TYPE>(a, row, l16, in_lds, error) : all_doubles<TYPE>(a, row, top, l16, keys);
       leave_groups<PER, float>(a, key, l16, stay);
     }

@@ -447,3 +447,21 @@ def test_groups_next_to_each_other_under_a_large_bias(largest, last):
         chosen = check_route(l, "f32", b, ref.Router(4, 2, ref.SIGMOID, 2, 1, 2, True), f"groups next to each other, biases near {largest} {last}")
         assert (chosen // 2 == int(last)).all()
     assert many > 20
+
+
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+@pytest.mark.parametrize("mask", [-1e9, LOWEST, -np.inf, 1e9, -LOWEST, np.inf])
+def test_masked_experts_beside_near_ties(mask, score):
+    """How far estimates are trusted goes by the values that are compared: beside experts that a bias masks
+    (or forces), values a few FP32 steps apart, and others far apart, are told apart as without them."""
+    rng = np.random.default_rng(21)
+    T, E = 40, 96
+    near = (1.0 + rng.integers(0, 9, (T, E)) * 2.0 ** -22).astype(np.float32)
+    far = logits(rng, T, E, "f32")
+    b = (rng.integers(-3, 4, E) * 2.0 ** -23).astype(np.float32)
+    for l in (near, far):
+        for at in ([50], [3, 4, 60], list(range(12, 24)), list(range(12, 23)), list(range(0, 96, 2))):
+            masked = b.copy()
+            masked[at] = mask
+            for g, tg, gt in ((1, 1, 1), (8, 3, 1), (8, 3, 2), (48, 20, 2)):
+                check_route(l, "f32", masked, ref.Router(E, 7, score, g, tg, gt, True), f"masks {mask} at {len(at)} {score} groups {g} {tg} {gt}")
