@@ -417,3 +417,14 @@ def test_columns_around_a_workgroups_last(n, kind):
         assert lib.gemm_lora_workspace_bytes(rows, c.set()) == 0   # (one kernel)
         for base in ("other", "place", "none"):
             check_forward(c, f"{n} columns, {rows} rows, rank {rank} {kind} {base}", base, exact=True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,rank", [(4096, 48), (4159, 64), (4100, 33), (4159, 100), (4096, 128)])
+def test_many_rows_of_large_ranks(rows, rank, kind):
+    """Units of two tiles at every width above 32 ranks; whole numbers, so every bit counts."""
+    rng = np.random.default_rng(rows + rank)
+    for mixed in (False, True):
+        c = Case(rng, rows, 150, 200, rank, 3, kind, mixed, whole=True, pad=1)
+        check_forward(c, f"{rows} rows, rank {rank} {kind} mixed {mixed}", base="none" if mixed else "other", exact=True)
+        check_backward(c, f"{rows} rows, rank {rank} {kind} mixed {mixed}", base="none" if mixed else "other", exact=True)

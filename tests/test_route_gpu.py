@@ -465,3 +465,17 @@ def test_masked_experts_beside_near_ties(mask, score):
             masked[at] = mask
             for g, tg, gt in ((1, 1, 1), (8, 3, 1), (8, 3, 2), (48, 20, 2)):
                 check_route(l, "f32", masked, ref.Router(E, 7, score, g, tg, gt, True), f"masks {mask} at {len(at)} {score} groups {g} {tg} {gt}")
+
+
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+@pytest.mark.parametrize("T,E,k,g,tg,gt,kind", [
+    (4097, 64, 4, 1, 1, 1, "f32"), (20001, 24, 3, 4, 2, 2, "f32"), (5000, 128, 6, 8, 3, 2, "bf16"), (5000, 250, 8, 10, 4, 1, "f16"),
+    (4500, 256, 8, 8, 4, 2, "bf16"), (4200, 512, 5, 16, 5, 2, "f32")])
+def test_counts_of_many_tokens_by_values(T, E, k, g, tg, gt, kind, score):
+    """A bias (and sums of two) over more tokens than a workgroup of 256 a CU takes, counted by several workgroups:
+    every width of a lane's experts."""
+    rng = np.random.default_rng(T + E)
+    l = logits(rng, T, E, kind)
+    check_route(l, kind, (0.1 * rng.normal(size=E)).astype(np.float32), ref.Router(E, k, score, g, tg, gt, True), f"counts of {T}x{E} by values {score}")
+    if gt == 2:
+        check_route(l, kind, None, ref.Router(E, k, score, g, tg, gt), f"counts of {T}x{E} by sums {score}")
