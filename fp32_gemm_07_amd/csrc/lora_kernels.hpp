@@ -431,7 +431,7 @@ __device__ __attribute__((always_inline)) inline void hidden_operand(const f32x4
 
 // sum = B H^T of such operands. Small products come first (the third part of H times the second
 // of B is below 2^-24). The other parts of an infinity, or products of zeros with one, are NaN:
-// where the first parts' sum is not finite it stands alone.
+// where neither the sum nor that of the first parts is finite, the latter stands alone.
 template <int TYPE, int J, int KS, int PB, int PH>
 __device__ __attribute__((always_inline)) inline void multiply_parts(const uintx4 (&b)[J][KS][PB], const uintx4 (&h)[KS][PH], f32x4 (&sum)[J]) {
   if constexpr (TYPE == kF32) {
@@ -469,7 +469,8 @@ __device__ __attribute__((always_inline)) inline void multiply_parts(const uintx
       for (int j = 0; j < J; ++j) {
         const f32x4 alone = first(j, f32x4{});
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sum[j][v] = __builtin_isfinite(alone[v]) ? sum[j][v] : alone[v];
+        for (int v = 0; v < 4; ++v)   // (a sum that is finite stays, whatever brought the wave here)
+          sum[j][v] = __builtin_isfinite(sum[j][v]) || __builtin_isfinite(alone[v]) ? sum[j][v] : alone[v];
       }
     }
   }

@@ -428,3 +428,21 @@ def test_many_rows_of_large_ranks(rows, rank, kind):
         c = Case(rng, rows, 150, 200, rank, 3, kind, mixed, whole=True, pad=1)
         check_forward(c, f"{rows} rows, rank {rank} {kind} mixed {mixed}", base="none" if mixed else "other", exact=True)
         check_backward(c, f"{rows} rows, rank {rank} {kind} mixed {mixed}", base="none" if mixed else "other", exact=True)
+
+
+@pytest.mark.parametrize("rows", [2, 70])
+def test_a_sum_near_the_largest_float_beside_an_infinite_row(rows):
+    """A row whose H B^T stays below the largest float, though the first bfloat16 parts of H alone pass it, keeps its
+    bits when another row of its adapter becomes infinite (which has the first parts looked at alone)."""
+    c = Case(np.random.default_rng(1), rows, 17, 3, 5, 1, "bf16", True)
+    c.ids[:], c.ranks[:], c.scales[:] = 0, 5, 1.0
+    # H: twice -2^126 (1 + 2^-8 (1 - 2^-6)), whose first part is -2^126, and twice 1.5 2^127
+    c.a[0] = [[-2.0 ** 126, -2.0 ** 118, 2.0 ** 112]] * 2 + [[1.5 * 2.0 ** 127, 0, 0]] * 2 + [[0, 0, 0]]
+    c.b[:], c.x[0], c.x[1:] = 1.0, 1.0, 0.0
+    c.c[:] = -2.0 ** 127
+    say(f"a sum near the largest float, {rows} rows")
+    clean = run_forward(c)
+    c.x[1] = np.inf
+    assert np.array_equal(run_forward(c)[0], clean[0])
+    # 2^128 - 2^119 (1 - 2^-6) - 2^127, where a bfloat16's step is 2^119
+    assert (clean[0] == 2.0 ** 127 - 2.0 ** 119).all()
