@@ -210,21 +210,22 @@ int gemm_lora_backward(int rows, const gemm_lora_t *set, const int *ids, const v
   int st = check_set(rows, set);
   if (st != GEMM_OK) return st;
   const gemm_lora_t &s = *set;
-  if (ldx < s.K || lddy < s.N || (dX && C && ldc < s.K) || (dX && lddx < s.K)) return GEMM_ERR_INVALID_DIM;
-  if (!dX && !dA && !dB) return GEMM_OK;
+  const bool weights = dA || dB;   // (X is for these alone)
+  if ((weights && ldx < s.K) || lddy < s.N || (dX && C && ldc < s.K) || (dX && lddx < s.K)) return GEMM_ERR_INVALID_DIM;
+  if (!dX && !weights) return GEMM_OK;
   if (!dA != !dB) return GEMM_ERR_NULL_PTR;
   if (rows == 0 && !dA) return GEMM_OK;
-  if (rows > 0 && (!s.A || !s.B || !ids || !X || !dY)) return GEMM_ERR_NULL_PTR;
+  if (rows > 0 && (!s.A || !s.B || !ids || (weights && !X) || !dY)) return GEMM_ERR_NULL_PTR;
   const size_t es = elem_size(s.type);
-  if (!aligned_set(s, ids) || !aligned(X, es) || !aligned(dY, es) || !aligned(C, es) || !aligned(dX, es) ||
+  if (!aligned_set(s, ids) || (weights && !aligned(X, es)) || !aligned(dY, es) || !aligned(C, es) || !aligned(dX, es) ||
       !aligned(dA, 4) || !aligned(dB, 4))
     return GEMM_ERR_ALIGNMENT;
   const bool in_place = C == dX && ldc == lddx;
-  const Range x = {X, extent(rows, s.K, ldx, s.type)}, dy = {dY, extent(rows, s.N, lddy, s.type)};
+  const Range x = {X, weights ? extent(rows, s.K, ldx, s.type) : 0}, dy = {dY, extent(rows, s.N, lddy, s.type)};
   const Range c = {C, dX && C ? extent(rows, s.K, ldc, s.type) : 0}, dx = {dX, dX ? extent(rows, s.K, lddx, s.type) : 0};
   const Range id = {ids, 4 * static_cast<size_t>(rows)};
-  const size_t weights = sizeof(float) * static_cast<size_t>(s.adapters) * s.rank;
-  const Range da = {dA, dA ? weights * s.K : 0}, db = {dB, dB ? weights * s.N : 0};
+  const size_t grads = sizeof(float) * static_cast<size_t>(s.adapters) * s.rank;
+  const Range da = {dA, dA ? grads * s.K : 0}, db = {dB, dB ? grads * s.N : 0};
   const Range in[] = {x, dy, range_a(s), range_b(s), range_ranks(s), range_scales(s), id, {C, in_place ? 0 : c.bytes}};
   const Range out[] = {dx, da, db};
   st = check_outputs(out, in);

@@ -513,7 +513,8 @@ size_t gemm_lora_workspace_bytes(int rows, const gemm_lora_t *set);
  *   dA_a = sum over a's rows of (s_a B_a^T dY[i]) X[i]^T      dense FP32 arrays of the
  *   dB_a = sum over a's rows of dY[i] (s_a A_a X[i])^T        shapes of A and B
  * dA and dB are overwritten whole, with zeros where an adapter has no rows and behind
- * its rank. dX may be null, and dA and dB together. Sums over rows are FP32, in an
+ * its rank. dX may be null, and dA and dB together; without these X is not looked at and
+ * may be null too. Sums over rows are FP32, in an
  * order that depends on the sizes and ids alone. Where an input is not finite, a
  * gradient that it enters may be NaN instead of infinite. workspace: as above
  * (it holds A and B once more, so it grows with the number of adapters). */

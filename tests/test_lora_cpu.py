@@ -134,3 +134,12 @@ def test_reference_gradients_against_differences():
             down = loss()
             array[at] = keep
             assert abs((up - down) / (2 * h) - grad[at]) < 1e-7, at
+
+
+def test_backward_does_not_look_at_x_without_the_adapters_gradients():
+    """dX needs dY, A and B alone: the call comes as far as its last check, the workspace's, whatever X is."""
+    need = lib.gemm_lora_backward_workspace_bytes(8, adapters())
+    for x in ({"x": None}, {"x": None, "ldx": 0}, {"x": X + 2}, {"dx": X, "c": None}, {"dx": X, "c": X}):
+        assert backward(da=None, db=None, wb=need - 1, **x) == lib.GEMM_ERR_WORKSPACE, x
+    for x in ({"x": None}, {"x": X + 2, "da": None}):
+        assert backward(wb=need - 1, **x) in (lib.GEMM_ERR_NULL_PTR, lib.GEMM_ERR_ALIGNMENT), x

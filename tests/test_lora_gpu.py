@@ -446,3 +446,17 @@ def test_a_sum_near_the_largest_float_beside_an_infinite_row(rows):
     assert np.array_equal(run_forward(c)[0], clean[0])
     # 2^128 - 2^119 (1 - 2^-6) - 2^127, where a bfloat16's step is 2^119
     assert (clean[0] == 2.0 ** 127 - 2.0 ** 119).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [9, 300])
+def test_backward_to_the_rows_without_x(rows, kind):
+    """dX alone takes no X."""
+    t = torch()
+    c = Case(np.random.default_rng(rows), rows, 70, 90, 20, 4, kind, True)
+    want = run_backward(c, base="none", weights=False)[0]
+    s = c.set()
+    dy, dx = dev(c.dy, kind), t.full((rows, c.k), SENTINEL, device="cuda:0").to(dtype(kind))
+    say(f"dX without X {rows} {kind}")
+    lib.gemm_lora_backward(rows, s, c.di, None, 0, dy, c.n, None, 0, dx, c.k, None, None, None, 0, stream())
+    assert np.array_equal(host(dx), want)
