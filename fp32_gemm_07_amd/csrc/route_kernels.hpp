@@ -536,8 +536,8 @@ __device__ inline void route_token(const RouteArgs &a, long long t, int *counts,
 // are summed in LDS; a workgroup that is the only one writes them whole, several add theirs
 // (whole numbers: the order of the additions does not show).
 // Bound by a wave's chain of maxima, or with many tokens by its instructions: 65536 tokens on 4 of 64
-// experts 11 us by logits, 20 by values with a bias (16.8 MB read); 4096 on 8 of 256 7 and 10,
-// in groups 13; one token 4.4. Counts add 2 to 7.
+// experts 11 us by logits, 19 by values with a bias (16.8 MB read); 4096 on 8 of 256 7 and 10,
+// in groups 13, and 19 where some token needs FP64 values; one token 4.4. Counts add 2 to 7.
 template <int TYPE, int PER, bool VALUES, int THREADS>
 __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
   __shared__ int counts[kRouteMaxExperts];
